@@ -2,7 +2,8 @@
  * specv.h -- C ABI of the GB300 speculative-decoding verification library
  * (libspecv.so).
  *
- * Two operations, both defined on the pages this library restates:
+ * Two operations, both defined on the pages this library restates (and the
+ * paged key-value cache that the verified target reads, further below):
  *
  *   spec_verify    batched lossless draft verification.  For each request b
  *                  and draft position j < ell_b it forms the temperature
@@ -57,7 +58,9 @@ extern "C" {
 
 typedef void* spec_stream_t; /* a cudaStream_t */
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* SPEC_F32 and SPEC_BF16: logits.  The cache calls also take SPEC_F16, and
+ * SPEC_E4M3 (8 bits: 4 of exponent, 3 of mantissa) for the cache itself. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2, SPEC_E4M3 = 3 } spec_dtype;
 
 enum {
     SPEC_OK = 0,
@@ -75,13 +78,18 @@ enum {
     SPEC_ERR_CUDA = -11,       /* a CUDA runtime call failed (launch, attribute query) */
     SPEC_ERR_UNIFORM = -12,    /* device: a used uniform outside [0, 1) */
     SPEC_ERR_CONFIDENCE = -13, /* device: a confidence outside [0, 1] or NaN */
-    SPEC_ERR_ROW_INDEX = -14   /* device: packed rows of a request outside the packed arrays */
+    SPEC_ERR_ROW_INDEX = -14,  /* device: packed rows of a request outside the packed arrays */
+    SPEC_ERR_POOL = -15,       /* device: no free pages left for a request */
+    SPEC_ERR_CACHE_LEN = -16,  /* device: a cache length outside the request's page table or pages */
+    SPEC_ERR_PAGE = -17,       /* device: a needed page table entry outside [0, pages), or a page with no reference */
+    SPEC_ERR_REQUEST = -18     /* device: a request id outside [0, B), or one that a call may not name twice */
 };
 
 /* Limits of this build. */
 #define SPEC_MAX_BATCH 4096
 #define SPEC_MAX_GAMMA 32
 #define SPEC_MAX_SCHED_CANDIDATES 16384 /* B * (gamma - min_len) for spec_schedule */
+#define SPEC_MAX_HEAD_DIM 256           /* of a cache; a multiple of 8 */
 
 /* ------------------------------------------------------------- verification */
 
@@ -262,6 +270,190 @@ int spec_schedule_static(const float* confidence, int B, int gamma, float thresh
  */
 int spec_sts_fit(const float* confidence, const int32_t* accept_len, int n, int gamma,
                  float* out_temperature, double* out_ece);
+
+/* ------------------------------------------- the target's key-value cache */
+
+/*
+ * A verification round needs the target's keys and values of every position so
+ * far.  They live in pages of page_size tokens, and request b's position t is
+ * token t % page_size of page page_table[b][t / page_size].  One round is
+ *   spec_reserve_pages   pages for the tested tokens (positions cache_len[b] ..
+ *                        cache_len[b] + ell_b: the last emitted token and the
+ *                        ell_b drafts);
+ *   spec_append_kv       rotary positions, and their keys and values into the
+ *                        pages (per layer);
+ *   spec_attend          their attention over the cache (per layer);
+ *   spec_verify          on the logits that follow;
+ *   spec_commit_pages    cache_len[b] += accept_len[b] + 1, and the pages that
+ *                        held rejected drafts only are given back.
+ * A single decoded token is the same with gamma = 0.  Query rows are laid out
+ * as the target logits are: padded [B, gamma+1, ...], or packed with the row
+ * index that spec_pack_rows writes (target_row).  No call synchronises; all
+ * can be captured into one CUDA graph.
+ *
+ * State, all int32 on the device, owned by the caller:
+ *   page_table [B, max_pages]  page ids; -1 where a request has no page
+ *   num_pages  [B]             slots of the table that a request holds (a slot
+ *                              behind a sliding window may be -1 all the same)
+ *   ref_count  [pages]         table entries that name a page; 0 is free
+ *   cache_len  [B]             positions whose keys and values are valid
+ * Every call names the lowest free pages first, in request order, so results
+ * do not depend on timing.
+ *
+ * Errors in device data set the workspace's status word (sticky until
+ * spec_read_status; zero the workspace once before first use).
+ */
+typedef struct {
+    void* k;            /* device: keys of layer 0, page 0, token 0, head 0; 16-byte aligned */
+    void* v;            /* device: values, same strides */
+    spec_dtype dt;      /* SPEC_F32, SPEC_BF16, SPEC_F16 or SPEC_E4M3 */
+    int layers;         /* fork and compact move a page's tokens in every layer; others use layer 0 */
+    int pages, page_size, kv_heads, head_dim; /* head_dim: a multiple of 8, at most 256 */
+    /* strides in elements (16-byte multiples; the head_dim values are adjacent) */
+    long long layer_stride, page_stride, token_stride, head_stride;
+    const float* k_scale; /* device [kv_heads], SPEC_E4M3 only: the entry stands for entry * scale; */
+    const float* v_scale; /* NULL: 1 */
+} spec_cache;
+
+/* Bytes of device workspace of spec_append_kv, spec_reserve_pages,
+ * spec_commit_pages, spec_free_pages, spec_fork_pages (pages may be 0 for
+ * these) and spec_compact_pages; 0 if out of range. */
+size_t spec_cache_workspace_bytes(int B, int pages);
+
+/* Bytes of device workspace of spec_attend for these sizes (0 if out of range). */
+size_t spec_attend_workspace_bytes(int B, int gamma, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * Attention of the tested tokens over the cache.  For query row j of request
+ * b, at position p = cache_len[b] + j (0 <= j <= ell_b), and head h:
+ *   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q . k_t),
+ * over the visible positions t <= p with window == 0, p - t < window or t <
+ * sinks; k_t and v_t of KV head h / (q_heads / kv_heads).
+ *   q            device, dt (SPEC_F32, SPEC_BF16 or SPEC_F16), row r and head h
+ *                at q + r * q_row_stride + h * q_head_stride elements (16-byte
+ *                multiples); head_dim adjacent values.
+ *   q_row        NULL: request b's rows are b*(gamma+1) + j (padded).  Else
+ *                [B] int32: rows q_row[b] + j of `rows` rows (packed); a request
+ *                whose rows fall outside is skipped with SPEC_ERR_ROW_INDEX.
+ *   verify_len   [B] int32, ell_b in [0, gamma]; NULL means gamma for all.  A
+ *                request with another value has no rows (SPEC_ERR_VERIFY_LEN).
+ *   cache        dt equal to q's, or SPEC_E4M3 under SPEC_BF16 / SPEC_F16 rows.
+ *                Positions cache_len[b] .. cache_len[b] + ell_b must have been
+ *                appended.  Entries that no row sees are not read.
+ *   scale        finite; normally 1 / sqrt(head_dim).
+ *   window       0: all earlier positions; else the last `window` positions,
+ *                the token's own included.  sinks: first positions that stay
+ *                visible under a window.
+ *   out          [rows, q_heads, head_dim] dt, contiguous, 16-byte aligned.
+ *                Rows that no request has are left as they were.
+ *   out_lse      [rows, q_heads] fp32 or NULL: log sum_t w_t.
+ * A request whose positions do not fit its page table (SPEC_ERR_CACHE_LEN), or
+ * with a needed entry that is not a page (SPEC_ERR_PAGE), gets NaN rows.  A
+ * value that is not finite reaches only the rows that see it.
+ * Numbers: scores, running maximum and sum, and the output are fp32; with
+ * 16-bit rows the weights are rounded to that type (to fp16 under a SPEC_E4M3
+ * cache) for the product with v.  Bit-reproducible for given arguments; how a
+ * long cache is split depends on the whole batch's lengths, so a request's
+ * last bits may change with its company.  Two calls that share a workspace
+ * must be ordered on one stream.
+ */
+int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, spec_dtype dt, int q_heads,
+                const spec_cache* cache, const int32_t* page_table, int max_pages, const int32_t* cache_len,
+                const int32_t* verify_len, const int32_t* q_row, int rows, int B, int gamma, float scale,
+                int window, int sinks, void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                spec_stream_t stream);
+
+/*
+ * Rotary positions and the append of the tested tokens' keys and values.  Row
+ * j of request b is at position p = cache_len[b] + j.  Pair i of the first
+ * `rotary_dim` values of every q and k head is turned by the angle p * f_i:
+ *   (x, y) -> mscale * (x cos - y sin, x sin + y cos),
+ * pair i = values (i, i + rotary_dim/2), or (2i, 2i+1) if `interleaved`; the
+ * other values pass unchanged.  The turned k and v go to the request's pages
+ * (divided by their scales, clamped to +-448 and rounded to nearest even for
+ * SPEC_E4M3), the turned q to out_q.
+ *   q, k, v      device, dt, row r and head h at r * row_stride + h * head_stride
+ *                elements (16-byte multiples).
+ *   row, rows    as q_row and rows of spec_attend.
+ *   turns        device [rotary_dim / 2] uint64, or NULL with rotary_dim 0:
+ *                f_i / (2 pi) as a fraction of 2^64 (the angle of any position
+ *                is then an exact wrapping product).
+ *   out_q        [rows, q_heads, head_dim] dt, contiguous; may be q itself if q
+ *                is contiguous.  Rows that no request has are left as they were.
+ * A position outside the page table (SPEC_ERR_CACHE_LEN) or without a page
+ * (SPEC_ERR_PAGE) is not stored; its q row is turned all the same.
+ * cache->dt must be dt, or SPEC_E4M3 under SPEC_BF16 / SPEC_F16.
+ */
+int spec_append_kv(const void* q, long long q_row_stride, long long q_head_stride, const void* k, const void* v,
+                   long long k_row_stride, long long k_head_stride, long long v_row_stride,
+                   long long v_head_stride, spec_dtype dt, int q_heads, const spec_cache* cache,
+                   const int32_t* page_table, int max_pages, const int32_t* cache_len, const int32_t* verify_len,
+                   const int32_t* row, int rows, int B, int gamma, const uint64_t* turns, int rotary_dim,
+                   int interleaved, float mscale, void* out_q, void* workspace, size_t workspace_bytes,
+                   spec_stream_t stream);
+
+/*
+ * Pages for the tested tokens: request b's slots are grown to hold cache_len[b]
+ * + ell_b + 1 positions (verify_len NULL: gamma for all), with the lowest free
+ * pages in request order.  Where the pool runs out, the first request that does
+ * not fit and every growing request after it get none.
+ *   out_status [B] int32: SPEC_OK, SPEC_ERR_POOL, SPEC_ERR_VERIFY_LEN or
+ *   SPEC_ERR_CACHE_LEN (more than max_pages slots, or a negative length); a
+ *   request with an error is left as it was.
+ */
+int spec_reserve_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages,
+                       const int32_t* cache_len, const int32_t* verify_len, int B, int gamma, int max_pages,
+                       int page_size, int32_t* out_status, void* workspace, size_t workspace_bytes,
+                       spec_stream_t stream);
+
+/*
+ * After verification: out_cache_len[b] = cache_len[b] + accept_len[b] + 1 (b's
+ * last emitted token and its accepted drafts), slots behind it are given back.
+ * accept_len[b] = -1 (an invalid request) keeps cache_len[b].  With window > 0,
+ * pages that hold neither a position below `sinks` nor one that the next token
+ * (at out_cache_len[b]) sees are given back too, and their entries become -1.
+ *   out_cache_len [B]: may be cache_len.
+ * An accept length below -1, or a new length beyond the slots held, leaves the
+ * request as it was (SPEC_ERR_CACHE_LEN).
+ */
+int spec_commit_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages,
+                      const int32_t* cache_len, const int32_t* accept_len, int B, int max_pages, int page_size,
+                      int window, int sinks, int32_t* out_cache_len, void* workspace, size_t workspace_bytes,
+                      spec_stream_t stream);
+
+/* Ends requests: gives back all pages of the n requests in `requests` [n]
+ * (device), and sets their num_pages and cache_len to 0.  Naming one twice is
+ * allowed; an id outside [0, B) is skipped (SPEC_ERR_REQUEST). */
+int spec_free_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages, int32_t* cache_len,
+                    const int32_t* requests, int n, int B, int max_pages, void* workspace, size_t workspace_bytes,
+                    spec_stream_t stream);
+
+/*
+ * Branches: request dst[i] becomes a copy of request src[i] (i < n): what dst
+ * held is given back, its slots name src's full pages (one more reference
+ * each), and the partial last page is copied into a fresh one, in every layer
+ * of `cache`, its first cache_len % page_size tokens.  num_pages[dst] and
+ * cache_len[dst] follow.  One src may have many dst.
+ *   out_status [n] int32: SPEC_OK; SPEC_ERR_REQUEST for an id outside [0, B), a
+ *   dst named twice, or a dst that is also a src of this call (left as it was);
+ *   SPEC_ERR_CACHE_LEN where src's length exceeds its slots, SPEC_ERR_PAGE where
+ *   its last page is missing (left as it was); SPEC_ERR_POOL where no free page
+ *   was left for the copy, in the order of i (dst is then empty).
+ */
+int spec_fork_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int32_t* cache_len,
+                    const int32_t* src, const int32_t* dst, int n, int B, int max_pages, const spec_cache* cache,
+                    int32_t* out_status, void* workspace, size_t workspace_bytes, spec_stream_t stream);
+
+/*
+ * Compaction: the N referenced pages move to the ids 0..N-1.  Pages below N
+ * stay; the k-th lowest referenced page from N on goes to the k-th lowest free
+ * one, with its tokens of all layers, and the tables and counts are renamed.
+ *   out_page_table [B, max_pages], out_ref_count [pages]: may be page_table and
+ *   ref_count.  out_total [1] int32: N.
+ */
+int spec_compact_pages(const int32_t* page_table, const int32_t* num_pages, const int32_t* ref_count, int B,
+                       int max_pages, const spec_cache* cache, int32_t* out_page_table, int32_t* out_ref_count,
+                       int32_t* out_total, void* workspace, size_t workspace_bytes, spec_stream_t stream);
 
 /* ------------------------------------------------- verification, no workspace */
 

@@ -18,7 +18,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 LIB_PATH = os.path.join(_HERE, "libspecv.so")
-SOURCES = ["specv_verify.cu", "specv_sched.cu", "specv_api.cu", "specv_static.cu"]
+SOURCES = ["specv_verify.cu", "specv_sched.cu", "specv_api.cu", "specv_static.cu", "specv_pages.cu",
+           "specv_append.cu", "specv_attend.cu", "specv_attend_simt.cu"]
+HEADERS = ["specv_common.cuh", "specv_rowstats.cuh", "specv_cache.cuh", "specv_attend.cuh", "specv_trace.h"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 
@@ -26,8 +28,8 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", 
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_TEMPERATURE = 0, -1, -2, -3, -4
 ERR_VERIFY_LEN, ERR_TOKEN, ERR_WORKSPACE, ERR_COST_TABLE = -5, -6, -7, -8
 ERR_NONFINITE, ERR_TIMEOUT, ERR_CUDA, ERR_UNIFORM, ERR_CONFIDENCE = -9, -10, -11, -12, -13
-ERR_ROW_INDEX = -14
-F32, BF16 = 0, 1
+ERR_ROW_INDEX, ERR_POOL, ERR_CACHE_LEN, ERR_PAGE, ERR_REQUEST = -14, -15, -16, -17, -18
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
 SCHED_EXACT, SCHED_ALGORITHM1, SCHED_DCUT = 0, 1, 2
 MAX_BATCH, MAX_GAMMA, MAX_SCHED_CANDIDATES = 4096, 32, 16384
 
@@ -35,7 +37,10 @@ EXPORTED = ["spec_verify_workspace_bytes", "spec_verify", "spec_verify_stats",
             "spec_schedule_workspace_bytes", "spec_schedule", "spec_read_status",
             "spec_status_string", "spec_profile_events", "spec_verify_kernel_count",
             "spec_verify_static", "spec_schedule_static", "spec_sts_fit", "spec_verify_packed",
-            "spec_pack_rows", "spec_selftest_wait", "spec_selftest_expire_first_wait"]
+            "spec_pack_rows", "spec_selftest_wait", "spec_selftest_expire_first_wait",
+            "spec_cache_workspace_bytes", "spec_attend_workspace_bytes", "spec_attend", "spec_append_kv",
+            "spec_reserve_pages", "spec_commit_pages", "spec_free_pages", "spec_fork_pages",
+            "spec_compact_pages"]
 STATIC_WORKSPACE_BYTES = 8 << 20
 
 
@@ -53,8 +58,7 @@ def _nvcc() -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/*.cu for sm_103a into libspecv.so (in-tree, parallel TUs)."""
     srcs = [os.path.join(_CSRC, s) for s in SOURCES]
-    deps = srcs + [os.path.join(_CSRC, "specv_common.cuh"), os.path.join(_CSRC, "specv_rowstats.cuh"),
-                   os.path.join(_CSRC, "specv_trace.h"), os.path.join(_ROOT, "include", "specv.h")]
+    deps = srcs + [os.path.join(_CSRC, h) for h in HEADERS] + [os.path.join(_ROOT, "include", "specv.h")]
     if (not force and os.path.exists(LIB_PATH)
             and all(os.path.getmtime(LIB_PATH) >= os.path.getmtime(d) for d in deps)):
         return LIB_PATH
@@ -131,8 +135,34 @@ def lib():
                 L.spec_selftest_wait.restype = i32
                 L.spec_selftest_expire_first_wait.argtypes = [i32]
                 L.spec_selftest_expire_first_wait.restype = i32
+                ll, cp = ctypes.c_longlong, ctypes.POINTER(Cache)
+                L.spec_cache_workspace_bytes.argtypes = [i32, i32]
+                L.spec_cache_workspace_bytes.restype = sz
+                L.spec_attend_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+                L.spec_attend_workspace_bytes.restype = sz
+                L.spec_attend.argtypes = [vp, ll, ll, i32, i32, cp, vp, i32, vp, vp, vp, i32, i32, i32, f32, i32,
+                                          i32, vp, vp, vp, sz, vp]
+                L.spec_append_kv.argtypes = [vp, ll, ll, vp, vp, ll, ll, ll, ll, i32, i32, cp, vp, i32, vp, vp, vp,
+                                             i32, i32, i32, vp, i32, i32, f32, vp, vp, sz, vp]
+                L.spec_reserve_pages.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
+                L.spec_commit_pages.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, sz, vp]
+                L.spec_free_pages.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, vp, sz, vp]
+                L.spec_fork_pages.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, cp, vp, vp, sz, vp]
+                L.spec_compact_pages.argtypes = [vp, vp, vp, i32, i32, cp, vp, vp, vp, vp, sz, vp]
+                for f in (L.spec_attend, L.spec_append_kv, L.spec_reserve_pages, L.spec_commit_pages,
+                          L.spec_free_pages, L.spec_fork_pages, L.spec_compact_pages):
+                    f.restype = i32
                 _lib = L
     return _lib
+
+
+class Cache(ctypes.Structure):
+    """spec_cache: where the pages of a key-value cache are."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dt", ctypes.c_int), ("layers", ctypes.c_int),
+                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("layer_stride", ctypes.c_longlong), ("page_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class CostTable(ctypes.Structure):
@@ -468,3 +498,368 @@ def profile_events(before=None, after=None):
 
 def kernel_count(B: int, temperature: float) -> int:
     return int(lib().spec_verify_kernel_count(B, ctypes.c_float(temperature)))
+
+
+# ------------------------------------------------------- the key-value cache
+def _row_dtype(name, t) -> int:
+    torch = _torch()
+    code = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _on_device(name, t):
+    torch = _torch()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _cache_arg(k_cache, v_cache, k_scale, v_scale, layered=False):
+    """spec_cache of [pages, page_size, kv_heads, head_dim] tensors (with
+    `layered` also [layers, pages, ...]) of any strides with adjacent values."""
+    torch = _torch()
+    dt = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32,
+          torch.float8_e4m3fn: E4M3}.get(k_cache.dtype)
+    if dt is None:
+        raise TypeError(f"k_cache must be bfloat16, float16, float32 or float8_e4m3fn, got {k_cache.dtype}")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"v_cache must be {k_cache.dtype}, got {v_cache.dtype}")
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 and not (layered and len(shape) == 5):
+        raise ValueError(f"k_cache must be {'[layers, ' if layered else '['}pages, page_size, kv_heads, head_dim], "
+                         f"got {tuple(shape)}")
+    if v_cache.shape != shape or v_cache.stride() != strides:
+        raise ValueError("v_cache must have the shape and strides of k_cache")
+    _on_device("k_cache", k_cache)
+    _on_device("v_cache", v_cache)
+    if strides[-1] != 1 and shape[-1] != 1:
+        raise ValueError("the head_dim values of k_cache must be adjacent")
+    P, page, H, D = shape[-4:]
+    # a dimension of one entry has no stride of its own
+    unit = 64
+    ls = strides[0] if len(shape) == 5 and shape[0] > 1 else unit
+    ps, ts, hs = strides[-4] if P > 1 else unit, strides[-3] if page > 1 else unit, strides[-2] if H > 1 else unit
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if s is not None:
+            if dt != E4M3:
+                raise ValueError(f"{name} belongs to a float8_e4m3fn cache")
+            _check_tensor(name, s, torch.float32, (H,))
+    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), dt, shape[0] if len(shape) == 5 else 1, P, page, H, D, ls,
+                 ps, ts, hs, None if k_scale is None else k_scale.data_ptr(),
+                 None if v_scale is None else v_scale.data_ptr())
+
+
+def _row_strides(name, t, dtype, heads, dim, B, gamma, packed):
+    """(rows, row stride, head stride) of query-like rows: [B, gamma+1, heads,
+    dim] (padded) or [rows, heads, dim] (packed)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _on_device(name, t)
+    shape, s = t.shape, t.stride()
+    if packed:
+        if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+            raise ValueError(f"{name} must have shape [rows, {heads}, {dim}] with a row index, got {tuple(shape)}")
+        rows, rs = shape[0], s[0]
+    else:
+        if tuple(shape) != (B, gamma + 1, heads, dim):
+            raise ValueError(f"{name} must have shape {(B, gamma + 1, heads, dim)}, got {tuple(shape)}")
+        rows, rs = B * (gamma + 1), s[1] if gamma > 0 else s[0]
+        if gamma > 0 and B > 1 and s[0] != (gamma + 1) * s[1]:
+            raise ValueError(f"the rows of {name} must be equally spaced")
+    if s[-1] != 1 and dim != 1:
+        raise ValueError(f"the head_dim values of {name} must be adjacent")
+    return rows, rs if rows > 1 else heads * dim, s[-2] if heads > 1 else dim
+
+
+def _tables(page_table, cache_len, verify_len, row, B, slots):
+    torch = _torch()
+    _check_tensor("page_table", page_table, torch.int32, (B, slots))
+    _check_tensor("cache_len", cache_len, torch.int32, (B,))
+    _check_tensor("verify_len", verify_len, torch.int32, (B,), required=False)
+    _check_tensor("row", row, torch.int32, (B,), required=False)
+
+
+def _workspace(workspace, make):
+    torch = _torch()
+    if workspace is None:
+        return make()
+    _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),))
+    return workspace
+
+
+def _gamma_of(q, row, gamma):
+    if row is None:
+        if q.dim() != 4:
+            raise ValueError("q must be [B, gamma+1, heads, head_dim] without a row index")
+        if gamma is not None and gamma != q.shape[1] - 1:
+            raise ValueError(f"q has {q.shape[1]} rows a request, gamma is {gamma}")
+        return q.shape[1] - 1
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim] with a row index")
+    if gamma is None:
+        raise ValueError("packed rows need gamma")
+    return int(gamma)
+
+
+def alloc_attend_workspace(B: int, gamma: int, q_heads: int, kv_heads: int, head_dim: int, device=None):
+    """A workspace of attend (zeroed; its status word is sticky until read_status)."""
+    torch = _torch()
+    n = int(lib().spec_attend_workspace_bytes(B, gamma, q_heads, kv_heads, head_dim))
+    if n == 0:
+        raise SpecError(ERR_SHAPE, "spec_attend_workspace_bytes")
+    w = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    w[:256].zero_()
+    return w
+
+
+def alloc_cache_workspace(B: int, pages: int = 0, device=None):
+    """A workspace of append_kv and the page calls (compact_pages needs the
+    number of pages), zeroed."""
+    torch = _torch()
+    n = int(lib().spec_cache_workspace_bytes(B, pages))
+    if n == 0:
+        raise SpecError(ERR_SHAPE, "spec_cache_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def attend(q, k_cache, v_cache, page_table, cache_len, verify_len=None, row=None, *, gamma=None, scale=None,
+           window: int = 0, sinks: int = 0, k_scale=None, v_scale=None, out=None, out_lse=None, workspace=None,
+           stream=None):
+    """Run spec_attend: attention of the tested tokens over a paged cache.
+
+    q [B, gamma+1, heads, head_dim], or packed [rows, heads, head_dim] with row
+    [B] int32 (the target rows of pack_rows) and gamma; bf16, fp16 or fp32,
+    heads and rows at any 16-byte strides.  k_cache and v_cache [pages,
+    page_size, kv_heads, head_dim] of q's type or float8_e4m3fn (with k_scale,
+    v_scale [kv_heads] fp32 or None).  page_table [B, max_pages], cache_len [B],
+    verify_len [B] or None (gamma for all), int32.  scale defaults to 1 /
+    sqrt(head_dim).  out like q (contiguous; rows that no request has are left
+    as they were, and undefined in an out made here), out_lse like q without
+    head_dim, fp32.  Returns (out, workspace)."""
+    torch = _torch()
+    dt = _row_dtype("q", q)
+    gamma = _gamma_of(q, row, gamma)
+    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale)
+    B, slots = page_table.shape
+    heads, dim = q.shape[-2], cache.head_dim
+    rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, row is not None)
+    _tables(page_table, cache_len, verify_len, row, B, slots)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _check_tensor("out", out, q.dtype, q.shape)
+    _check_tensor("out_lse", out_lse, torch.float32, q.shape[:-1], required=False)
+    workspace = _workspace(workspace, lambda: alloc_attend_workspace(B, gamma, heads, cache.kv_heads, dim, q.device))
+    rc = lib().spec_attend(q.data_ptr(), rs, hs, dt, heads, cache, page_table.data_ptr(), slots,
+                           cache_len.data_ptr(), _ptr(verify_len), _ptr(row), rows, B, gamma,
+                           dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr(out_lse),
+                           workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+    _check(rc, "spec_attend")
+    return out, workspace
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     context: int = 0, low: float = 1.0, high: float = 4.0):
+    """Angle per token of each of the rotary_dim / 2 pairs, base^(-2i / rotary_dim),
+    as a float64 array for rope_table.  For contexts longer than trained:
+
+    scaling="linear": every frequency divided by `factor`;
+    scaling="base": the base times factor^(rotary_dim / (rotary_dim - 2)), which
+    keeps the highest frequency and divides the lowest by `factor`;
+    scaling="banded": with w the wavelength in tokens, frequencies with
+    context / w below `low` are divided by `factor`, those with context / w above
+    `high` are kept, and those between are blended linearly in context / w."""
+    import numpy as np
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    half = rotary_dim // 2
+    if scaling == "base":
+        if rotary_dim > 2:
+            base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    elif scaling not in (None, "linear", "banded"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    f = base ** (-np.arange(half, dtype=np.float64) / half)
+    if scaling == "linear":
+        f = f / factor
+    if scaling == "banded":
+        if context < 1 or not high > low:
+            raise ValueError("banded scaling needs the trained context and low < high")
+        keep = np.clip((context * f / (2.0 * np.pi) - low) / (high - low), 0.0, 1.0)
+        f = (1.0 - keep) * f / factor + keep * f
+    return f
+
+
+def rope_table(frequencies, device=None):
+    """The `turns` of append_kv for these angles per token (any array of
+    float64): each as a fraction of 2^64 of a turn, int64 on the device."""
+    import numpy as np
+    torch = _torch()
+    f = np.asarray(frequencies, dtype=np.float64).reshape(-1)
+    if not np.all(np.isfinite(f)):
+        raise ValueError("frequencies must be finite")
+    turns = [int(round(float(x) / (2.0 * np.pi) * 2.0 ** 64)) % 2 ** 64 for x in f]
+    return torch.from_numpy(np.array(turns, dtype=np.uint64).view(np.int64)).to(device or "cuda")
+
+
+def append_kv(q, k, v, k_cache, v_cache, page_table, cache_len, verify_len=None, row=None, *, gamma=None,
+              turns=None, interleaved: bool = False, mscale: float = 1.0, k_scale=None, v_scale=None, out_q=None,
+              workspace=None, stream=None):
+    """Run spec_append_kv: rotary positions, and the tested tokens' keys and
+    values into their pages.
+
+    q as for attend, k and v like it with kv_heads; any 16-byte strides (slices
+    of one projection are fine).  turns: rope_table's, for 2 * len(turns)
+    rotated values of each head, or None (no rotation).  out_q like q and
+    contiguous (q itself is allowed where it is contiguous).  Other arguments as
+    for attend.  Returns (out_q, workspace)."""
+    torch = _torch()
+    dt = _row_dtype("q", q)
+    gamma = _gamma_of(q, row, gamma)
+    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale)
+    B, slots = page_table.shape
+    heads, dim, H = q.shape[-2], cache.head_dim, cache.kv_heads
+    packed = row is not None
+    rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, packed)
+    krows, krs, khs = _row_strides("k", k, q.dtype, H, dim, B, gamma, packed)
+    vrows, vrs, vhs = _row_strides("v", v, q.dtype, H, dim, B, gamma, packed)
+    if krows != rows or vrows != rows:
+        raise ValueError(f"q, k and v must have the same rows, got {rows}, {krows} and {vrows}")
+    _tables(page_table, cache_len, verify_len, row, B, slots)
+    n = 0
+    if turns is not None:
+        n = turns.numel()
+        _check_tensor("turns", turns, torch.int64, (n,))
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _check_tensor("out_q", out_q, q.dtype, q.shape)
+    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, q.device))
+    rc = lib().spec_append_kv(q.data_ptr(), rs, hs, k.data_ptr(), v.data_ptr(), krs, khs, vrs, vhs, dt, heads, cache,
+                              page_table.data_ptr(), slots, cache_len.data_ptr(), _ptr(verify_len), _ptr(row), rows,
+                              B, gamma, _ptr(turns), 2 * n, 1 if interleaved else 0, mscale, out_q.data_ptr(),
+                              workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+    _check(rc, "spec_append_kv")
+    return out_q, workspace
+
+
+def _page_state(page_table, num_pages, ref_count, cache_len=None):
+    torch = _torch()
+    B, slots = page_table.shape
+    _check_tensor("page_table", page_table, torch.int32, (B, slots))
+    _check_tensor("num_pages", num_pages, torch.int32, (B,))
+    _check_tensor("ref_count", ref_count, torch.int32, (ref_count.numel(),))
+    if cache_len is not None:
+        _check_tensor("cache_len", cache_len, torch.int32, (B,))
+    return B, slots, ref_count.numel()
+
+
+def reserve_pages(page_table, num_pages, ref_count, cache_len, verify_len=None, *, gamma: int, page_size: int,
+                  out_status=None, workspace=None, stream=None):
+    """Run spec_reserve_pages: pages for positions cache_len[b] .. cache_len[b]
+    + verify_len[b] of every request.  page_table [B, max_pages], num_pages [B]
+    and ref_count [pages] are updated.  Returns (out_status [B], workspace)."""
+    torch = _torch()
+    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    _check_tensor("verify_len", verify_len, torch.int32, (B,), required=False)
+    _check_tensor("out_status", out_status, torch.int32, (B,), required=False)
+    if out_status is None:
+        out_status = torch.empty((B,), dtype=torch.int32, device=page_table.device)
+    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+    rc = lib().spec_reserve_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
+                                  cache_len.data_ptr(), _ptr(verify_len), B, gamma, slots, page_size,
+                                  out_status.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                  _stream_handle(stream))
+    _check(rc, "spec_reserve_pages")
+    return out_status, workspace
+
+
+def commit_pages(page_table, num_pages, ref_count, cache_len, accept_len, *, page_size: int, window: int = 0,
+                 sinks: int = 0, out_cache_len=None, workspace=None, stream=None):
+    """Run spec_commit_pages: cache_len + accept_len + 1 into out_cache_len (by
+    default cache_len itself), and pages behind it, or left by the window, given
+    back.  Returns (out_cache_len, workspace)."""
+    torch = _torch()
+    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    _check_tensor("accept_len", accept_len, torch.int32, (B,))
+    _check_tensor("out_cache_len", out_cache_len, torch.int32, (B,), required=False)
+    if out_cache_len is None:
+        out_cache_len = cache_len
+    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+    rc = lib().spec_commit_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
+                                 cache_len.data_ptr(), accept_len.data_ptr(), B, slots, page_size, window, sinks,
+                                 out_cache_len.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                 _stream_handle(stream))
+    _check(rc, "spec_commit_pages")
+    return out_cache_len, workspace
+
+
+def free_pages(page_table, num_pages, ref_count, cache_len, requests, *, workspace=None, stream=None):
+    """Run spec_free_pages: the requests named in `requests` [n] int32 end and
+    give their pages back.  Returns the workspace."""
+    torch = _torch()
+    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    n = requests.numel()
+    _check_tensor("requests", requests, torch.int32, (n,))
+    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+    rc = lib().spec_free_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
+                               cache_len.data_ptr(), requests.data_ptr(), n, B, slots, workspace.data_ptr(),
+                               workspace.numel(), _stream_handle(stream))
+    _check(rc, "spec_free_pages")
+    return workspace
+
+
+def fork_pages(page_table, num_pages, ref_count, cache_len, src, dst, k_cache, v_cache, *, out_status=None,
+               workspace=None, stream=None):
+    """Run spec_fork_pages: request dst[i] becomes a copy of request src[i] (src,
+    dst [n] int32), sharing full pages and copying the partial last one in every
+    layer of k_cache and v_cache ([layers, pages, page_size, kv_heads, head_dim],
+    or without layers).  Returns (out_status [n], workspace)."""
+    torch = _torch()
+    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    n = src.numel()
+    _check_tensor("src", src, torch.int32, (n,))
+    _check_tensor("dst", dst, torch.int32, (n,))
+    _check_tensor("out_status", out_status, torch.int32, (n,), required=False)
+    cache = _cache_arg(k_cache, v_cache, None, None, layered=True)
+    if cache.pages != pages:
+        raise ValueError(f"the cache has {cache.pages} pages, ref_count {pages}")
+    if out_status is None:
+        out_status = torch.empty((n,), dtype=torch.int32, device=page_table.device)
+    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+    rc = lib().spec_fork_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(),
+                               cache_len.data_ptr(), src.data_ptr(), dst.data_ptr(), n, B, slots, cache,
+                               out_status.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                               _stream_handle(stream))
+    _check(rc, "spec_fork_pages")
+    return out_status, workspace
+
+
+def compact_pages(page_table, num_pages, ref_count, k_cache, v_cache, *, out_page_table=None, out_ref_count=None,
+                  out_total=None, workspace=None, stream=None):
+    """Run spec_compact_pages: the N referenced pages move to the ids 0..N-1 in
+    every layer of k_cache and v_cache.  The renamed table and counts go to
+    out_page_table and out_ref_count (by default the inputs themselves).
+    Returns (out_total [1] = N, workspace)."""
+    torch = _torch()
+    B, slots, pages = _page_state(page_table, num_pages, ref_count)
+    _check_tensor("out_page_table", out_page_table, torch.int32, (B, slots), required=False)
+    _check_tensor("out_ref_count", out_ref_count, torch.int32, (pages,), required=False)
+    _check_tensor("out_total", out_total, torch.int32, (1,), required=False)
+    cache = _cache_arg(k_cache, v_cache, None, None, layered=True)
+    if cache.pages != pages:
+        raise ValueError(f"the cache has {cache.pages} pages, ref_count {pages}")
+    out_page_table = page_table if out_page_table is None else out_page_table
+    out_ref_count = ref_count if out_ref_count is None else out_ref_count
+    if out_total is None:
+        out_total = torch.empty((1,), dtype=torch.int32, device=page_table.device)
+    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, pages, page_table.device))
+    rc = lib().spec_compact_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), B, slots, cache,
+                                  out_page_table.data_ptr(), out_ref_count.data_ptr(), out_total.data_ptr(),
+                                  workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+    _check(rc, "spec_compact_pages")
+    return out_total, workspace

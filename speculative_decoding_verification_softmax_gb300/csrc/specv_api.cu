@@ -110,6 +110,10 @@ const char* spec_status_string(int status) {
         case SPEC_ERR_UNIFORM: return "a used uniform is outside [0, 1)";
         case SPEC_ERR_CONFIDENCE: return "a confidence is outside [0, 1]";
         case SPEC_ERR_ROW_INDEX: return "packed rows of a request lie outside the packed arrays";
+        case SPEC_ERR_POOL: return "no free cache pages left";
+        case SPEC_ERR_CACHE_LEN: return "a cache length lies outside the request's page table or pages";
+        case SPEC_ERR_PAGE: return "a needed page table entry is not a page, or a page has no reference";
+        case SPEC_ERR_REQUEST: return "a request id is out of range or named twice";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,201 @@
+// Attention over the paged cache: the C entry, the choice of kernel, and the
+// kernel that joins the parts of units that were split over blocks.
+#include "specv_attend.cuh"
+
+#include <math.h>
+
+#include <mutex>
+
+#include "specv_trace.h"
+
+namespace specv {
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = kJoinThreads / 32;
+
+// Joins the parts of the unit that block blockIdx.x left open: the block's own
+// and those of the blocks after it, in order.  With each part's maximum m_i
+// and sum l_i, M = max m_i: out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// One warp a row.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a, CacheView c) {
+    pdl_wait();
+    const int4 open = a.open[blockIdx.x];
+    if (open.x == 0) return;
+    const Request req = request_of<64>(a, c, open.y);  // rows do not depend on the tile size
+    const int h = open.z / req.row_tiles, r0 = (open.z - h * req.row_tiles) * a.tile_rows;
+    const int R = min((req.ell + 1) * a.group - r0, a.tile_rows);
+    const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= R) return;
+    const int dim = c.head_dim;
+    const float* first = part_at(a, blockIdx.x, 1);
+    const float* rest = part_at(a, blockIdx.x + 1, 0);
+    const long long hop = 2 * a.part_floats;
+    const int n = open.x;
+    // maxima and sums, a part a lane
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) {
+        const float* p = i == 0 ? first : rest + (i - 1) * hop;
+        M = fmaxf(M, p[a.tile_rows * dim + r]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f;
+    float acc[SPEC_MAX_HEAD_DIM / 32];
+#pragma unroll
+    for (int e = 0; e < SPEC_MAX_HEAD_DIM / 32; ++e) acc[e] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float w = 0.0f, l = 0.0f;
+        if (i0 + lane < n) {
+            const float* p = i0 + lane == 0 ? first : rest + (i0 + lane - 1) * hop;
+            w = exp2f(p[a.tile_rows * dim + r] - base);
+            l = p[a.tile_rows * (dim + 1) + r] * w;
+        }
+        L += warp_sum(l);
+        const int m = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < m; ++i) {
+            const float* p = (i0 + i == 0 ? first : rest + (i0 + i - 1) * hop) + r * dim;
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+            for (int e = 0; e < SPEC_MAX_HEAD_DIM / 32; ++e)
+                if (lane + 32 * e < dim) acc[e] = fmaf(wi, p[lane + 32 * e], acc[e]);
+        }
+    }
+    int j;
+    const long long row = out_row(a, req, h, r0 + r, &j);
+    const float inv = 1.0f / L;
+#pragma unroll
+    for (int e = 0; e < SPEC_MAX_HEAD_DIM / 32; ++e)
+        if (lane + 32 * e < dim) ((T*)a.out)[row * dim + lane + 32 * e] = from_f32<T>(acc[e] * inv);
+    if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
+}
+
+}  // namespace specv
+
+// ===================================================================== host
+using namespace specv;
+
+namespace {
+
+std::mutex g_at_mu;
+int g_at_sms[64];
+
+int sm_count(int& sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+    std::lock_guard<std::mutex> lk(g_at_mu);
+    if (!g_at_sms[dev] &&
+        cudaDeviceGetAttribute(&g_at_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    sms = g_at_sms[dev];
+    return SPEC_OK;
+}
+
+bool heads_ok(int q_heads, int kv_heads) {
+    return q_heads >= 1 && kv_heads >= 1 && q_heads <= 65535 && q_heads % kv_heads == 0;
+}
+
+// The workspace's size may not depend on the GPU: it is that of the largest
+// grid the library launches.
+constexpr int kMostSms = 160;
+
+size_t header_bytes() { return 256 + (sizeof(int4) * kMostSms * 4 + 255) / 256 * 256; }
+
+size_t parts_bytes(const AttendPlan& p, int head_dim) {
+    return sizeof(float) * 2 * (size_t)p.blocks * p.tile_rows * (head_dim + 2);
+}
+
+template <typename T>
+int launch_join(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
+    const int most = min(a.tile_rows, (a.gamma + 1) * a.group);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, (most + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attend_join<T>, a, c) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_attend_workspace_bytes(int B, int gamma, int q_heads, int kv_heads, int head_dim) {
+    if (B < 0 || B > SPEC_MAX_BATCH || gamma < 0 || gamma > SPEC_MAX_GAMMA || !heads_ok(q_heads, kv_heads) ||
+        head_dim < 8 || head_dim > SPEC_MAX_HEAD_DIM || (head_dim & 7))
+        return 0;
+    const int rows = (gamma + 1) * (q_heads / kv_heads);
+    return header_bytes() + parts_bytes(attend_simt_plan(rows, head_dim, kMostSms), head_dim);
+}
+
+int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, spec_dtype dt, int q_heads,
+                const spec_cache* cache, const int32_t* page_table, int max_pages, const int32_t* cache_len,
+                const int32_t* verify_len, const int32_t* q_row, int rows, int B, int gamma, float scale,
+                int window, int sinks, void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                spec_stream_t stream) {
+    TraceRange tr("spec_attend");
+    CacheView c;
+    int rc = cache_view(cache, c);
+    if (rc != SPEC_OK) return rc;
+    if (B < 0 || B > SPEC_MAX_BATCH || gamma < 0 || gamma > SPEC_MAX_GAMMA || !heads_ok(q_heads, c.kv_heads) ||
+        max_pages < 1 || rows < 0 || window < 0 || sinks < 0 || scale - scale != 0.0f)
+        return SPEC_ERR_SHAPE;
+    if (dt != SPEC_F32 && dt != SPEC_BF16 && dt != SPEC_F16) return SPEC_ERR_SHAPE;
+    if (cache->dt != dt && !(cache->dt == SPEC_E4M3 && dt != SPEC_F32)) return SPEC_ERR_SHAPE;
+    if (!q_row && rows < B * (gamma + 1)) return SPEC_ERR_SHAPE;
+    if (B == 0) return SPEC_OK;
+    if (!q || !out || !page_table || !cache_len || !workspace) return SPEC_ERR_NULL;
+    const long long es = dtype_size(dt);
+    if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15) return SPEC_ERR_ALIGN;
+    if (((q_row_stride | q_head_stride) * es) & 15) return SPEC_ERR_ALIGN;
+    if (((uintptr_t)page_table | (uintptr_t)cache_len | (uintptr_t)verify_len | (uintptr_t)q_row |
+         (uintptr_t)out_lse) & 3)
+        return SPEC_ERR_ALIGN;
+    if (workspace_bytes < spec_attend_workspace_bytes(B, gamma, q_heads, c.kv_heads, c.head_dim))
+        return SPEC_ERR_WORKSPACE;
+    int sms = 0;
+    if ((rc = sm_count(sms)) != SPEC_OK) return rc;
+    sms = min(sms, kMostSms);
+
+    AttendArgs a;
+    a.q = (const char*)q;
+    a.q_row = q_row_stride * es;
+    a.q_head = q_head_stride * es;
+    a.out = out;
+    a.lse = out_lse;
+    a.table = page_table;
+    a.len = cache_len;
+    a.ell = verify_len;
+    a.row = q_row;
+    a.status = (int*)workspace;
+    a.open = (int4*)((char*)workspace + 256);
+    a.parts = (float*)((char*)workspace + header_bytes());
+    a.q_heads = q_heads;
+    a.group = q_heads / c.kv_heads;
+    a.rows = rows;
+    a.B = B;
+    a.gamma = gamma;
+    a.max_pages = max_pages;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale * 1.4426950408889634f;  // log2(e)
+    a.by_group = FastDiv((uint32_t)a.group);
+    cudaStream_t st = (cudaStream_t)stream;
+
+    const AttendPlan p = attend_simt_plan((gamma + 1) * a.group, c.head_dim, sms);
+    a.tile_rows = p.tile_rows;
+    a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
+    a.least = 2;
+    if ((rc = attend_simt(a, c, dt, cache->dt, p.blocks, st)) != SPEC_OK) return rc;
+    if (dt == SPEC_F32) return launch_join<float>(a, c, p.blocks, st);
+    if (dt == SPEC_BF16) return launch_join<__nv_bfloat16>(a, c, p.blocks, st);
+    return launch_join<__half>(a, c, p.blocks, st);
+}
+
+}  // extern "C"

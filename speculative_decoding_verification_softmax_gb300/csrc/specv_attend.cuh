@@ -1,0 +1,197 @@
+// Attention over the paged cache: arguments, the split of the work over the
+// blocks, and the parts that blocks leave for the joining kernel.
+#pragma once
+
+#include "specv_cache.cuh"
+
+namespace specv {
+
+struct AttendArgs {
+    const char* q;
+    long long q_row, q_head;  // strides in bytes
+    void* out;
+    float* lse;
+    const int32_t* table;
+    const int32_t* len;
+    const int32_t* ell;
+    const int32_t* row;
+    int* status;
+    int4* open;    // [blocks]: parts, request, unit of the unit that a block left open
+    float* parts;  // [blocks][2][tile rows * (D + 2)]
+    long long part_floats;
+    int q_heads, group, rows, B, gamma, max_pages;
+    int window, sinks;
+    int tile_rows;  // rows of a unit at most
+    int least;      // tiles of a block at least
+    float scale;    // of the scores, to base 2
+    FastDiv by_group;
+};
+
+// ---------------------------------------------------------------- the work
+// Request b has (ell+1) * group query rows for each KV head.  A unit is up to
+// tile_rows of them against the request's visible keys, cut into tiles of KT
+// adjacent keys: tiles of the sinks, then tiles from the window's first key on.
+// All units' tiles, in order, are dealt to the blocks in equal runs, so that
+// ragged lengths leave no block idle; a run may end inside a unit, whose parts
+// are then joined.
+struct Request {
+    int code;      // SPEC_OK or why there is no work
+    int n, ell;    // cache length, drafts
+    int base;      // first row
+    int sink_tiles, first_tile, tiles, row_tiles, units;
+};
+
+template <int KT>
+__device__ __forceinline__ Request request_of(const AttendArgs& a, const CacheView& c, int b) {
+    Request r;
+    r.n = a.len[b];
+    r.ell = a.ell ? a.ell[b] : a.gamma;
+    r.base = a.row ? a.row[b] : b * (a.gamma + 1);
+    r.tiles = r.units = r.row_tiles = r.sink_tiles = r.first_tile = 0;
+    r.code = SPEC_OK;
+    if (r.ell < 0 || r.ell > a.gamma) r.code = SPEC_ERR_VERIFY_LEN;
+    else if (r.base < 0 || r.base > a.rows - r.ell - 1) r.code = SPEC_ERR_ROW_INDEX;
+    else if (r.n < 0 || (long long)r.n + r.ell >= min((long long)a.max_pages * c.page_size, 0x7fffffc0ll))
+        r.code = SPEC_ERR_CACHE_LEN;
+    if (r.code != SPEC_OK) return r;
+    const int last = (r.n + r.ell) / KT + 1;
+    if (a.window > 0) {
+        const int first = max(0, r.n - a.window + 1);
+        r.first_tile = first / KT;
+        r.sink_tiles = min((int)(((long long)a.sinks + KT - 1) / KT), r.first_tile);
+    }
+    r.tiles = r.sink_tiles + last - r.first_tile;
+    r.row_tiles = ((r.ell + 1) * a.group + a.tile_rows - 1) / a.tile_rows;
+    r.units = r.row_tiles * c.kv_heads;
+    return r;
+}
+
+// First key of tile t of a request.
+template <int KT>
+__device__ __forceinline__ int tile_key(const Request& r, int t) {
+    return (t < r.sink_tiles ? t : t - r.sink_tiles + r.first_tile) * KT;
+}
+
+// Whether position t is one that any row of the request sees (the rows' own
+// order, t <= p, apart), and whether the row at position p sees it.
+__device__ __forceinline__ bool any_sees(const AttendArgs& a, const Request& r, int t) {
+    return t <= r.n + r.ell && (a.window == 0 || r.n - t < a.window || t < a.sinks);
+}
+__device__ __forceinline__ bool sees(const AttendArgs& a, int p, int t) {
+    return t <= p && (a.window == 0 || p - t < a.window || t < a.sinks);
+}
+
+// True if every row of the request sees all KT keys of the tile.
+template <int KT>
+__device__ __forceinline__ bool all_see(const AttendArgs& a, const Request& r, int key) {
+    return key + KT - 1 <= r.n && (a.window == 0 || r.n + r.ell - key < a.window || key + KT <= a.sinks);
+}
+
+struct Run {
+    int b;           // request of the run's first tile
+    long long at;    // tile within the request (unit-major)
+    long long left;  // tiles of the run
+    long long step;  // tiles of every block's run
+};
+
+// The block's run.  All threads call it; s_scan [THREADS / 32 + 1] and s_run
+// are shared.
+template <int KT, int THREADS>
+__device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, long long* s_scan, Run* s_run) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + THREADS - 1) / THREADS;
+    const int b0 = tid * per, b1 = min(a.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request_of<KT>(a, c, b);
+        mine += (long long)r.units * r.tiles;
+    }
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    if (tid == 0) s_run->left = 0;
+    __syncthreads();
+    long long before = x - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const long long s = s_scan[w];
+        if (w < warp) before += s;
+        total += s;
+    }
+    const long long step = max((total + gridDim.x - 1) / gridDim.x, (long long)a.least);
+    const long long start = (long long)blockIdx.x * step;
+    if (start >= before && start < before + mine) {
+        long long at = start - before;
+        for (int b = b0; b < b1; ++b) {
+            const Request r = request_of<KT>(a, c, b);
+            const long long w = (long long)r.units * r.tiles;
+            if (at < w) {
+                s_run->b = b;
+                s_run->at = at;
+                s_run->left = min(step, total - start);
+                s_run->step = step;
+                break;
+            }
+            at -= w;
+        }
+    }
+    __syncthreads();
+    return *s_run;
+}
+
+// Where a block's part of a unit goes: slot 1 if the unit begins in the block,
+// slot 0 if it began in an earlier one.
+__device__ __forceinline__ float* part_at(const AttendArgs& a, int block, int slot) {
+    return a.parts + ((long long)block * 2 + slot) * a.part_floats;
+}
+
+// The element offset of unit row r (KV head h) in out, and its lse index.
+__device__ __forceinline__ long long out_row(const AttendArgs& a, const Request& q, int h, int r, int* token) {
+    const int j = (int)a.by_group.div((uint32_t)r);
+    *token = j;
+    return (long long)(q.base + j) * a.q_heads + h * a.group + (r - j * a.group);
+}
+
+// Byte offset of a key's first value (head 0) in the pages, or -1 if its entry
+// is no page.
+__device__ __forceinline__ long long key_at(const AttendArgs& a, const CacheView& c, const int32_t* pages, int t) {
+    const uint32_t slot = c.by_page.div((uint32_t)t);
+    const int page = pages[slot];
+    if (page < 0 || page >= c.pages) return -1;
+    return (long long)page * c.page + (long long)(t - (int)slot * c.page_size) * c.token;
+}
+
+// After its run, a block reports requests without work, and fills the rows of
+// those whose positions do not fit (blocks share the requests).
+template <typename T, int KT>
+__device__ __forceinline__ void report_requests(const AttendArgs& a, const CacheView& c) {
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const Request r = request_of<KT>(a, c, b);
+        if (r.code == SPEC_OK) continue;
+        if (threadIdx.x == 0) set_status(a.status, r.code);
+        if (r.code != SPEC_ERR_CACHE_LEN) continue;
+        const long long first = (long long)r.base * a.q_heads, n = (long long)(r.ell + 1) * a.q_heads;
+        const float nan = __int_as_float(0x7fc00000);
+        T* out = (T*)a.out + first * c.head_dim;
+        for (long long i = threadIdx.x; i < n * c.head_dim; i += blockDim.x) out[i] = from_f32<T>(nan);
+        if (a.lse)
+            for (long long i = threadIdx.x; i < n; i += blockDim.x) a.lse[first + i] = nan;
+    }
+}
+
+// ------------------------------------------------------------------ kernels
+struct AttendPlan {
+    int blocks;     // of the grid, at most
+    int tile_rows;  // rows of a unit
+};
+
+// fp32 rows: products on the CUDA cores.
+AttendPlan attend_simt_plan(int rows, int head_dim, int sms);
+int attend_simt(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype cache_dt, int blocks,
+                cudaStream_t st);
+
+}  // namespace specv

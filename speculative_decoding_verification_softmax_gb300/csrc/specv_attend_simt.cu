@@ -1,0 +1,249 @@
+// Attention over the paged cache on the CUDA cores: the path of fp32 rows,
+// whose products keep 32 bits.
+//
+// A block takes one unit at a time: 16 query rows against tiles of 64 keys.
+// One pass over the keys with the running maximum m and sum l of each row's
+// softmax, to base 2: a tile's scores s give m' = max(m, max s), p = 2^(s - m'),
+// l' = l 2^(m - m') + sum p and o' = o 2^(m - m') + p V.
+#include "specv_attend.cuh"
+
+namespace specv {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtRows = 16;
+constexpr int kSimtKeys = 64;
+constexpr int kSimtPad = 20;  // floats of a key's weights (16 rows): conflict-free 16-byte stores
+
+template <int D>
+constexpr size_t simt_smem() {
+    return sizeof(float) * (kSimtRows * D + kSimtKeys * (D + 4) + kSimtKeys * D + kSimtKeys * kSimtPad);
+}
+
+template <typename T, typename C, int D>
+__global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, CacheView c) {
+    constexpr int KT = kSimtKeys, CN = D / 64;
+    extern __shared__ float4 smem4[];
+    float* s_q = (float*)smem4;             // [16][D]
+    float* s_k = s_q + kSimtRows * D;       // [64][D + 4]
+    float* s_v = s_k + KT * (D + 4);        // [64][D]
+    float* s_p = s_v + KT * D;              // [64][20]: scores, then weights, by key
+    __shared__ float s_corr[kSimtRows], s_l[kSimtRows], s_m[kSimtRows];
+    __shared__ long long s_scan[kSimtThreads / 32 + 1];
+    __shared__ Run s_run;
+    const int tid = threadIdx.x;
+    const int col = tid & 63, rg = tid >> 6;     // products: a key or column, and 4 rows
+    const int srow = tid >> 4, slane = tid & 15;  // softmax: 16 threads a row
+
+    Run run = run_of<KT, kSimtThreads>(a, c, s_scan, &s_run);
+    int4 open = make_int4(0, 0, 0, 0);
+    const int dim = c.head_dim;
+    Request req;
+    if (run.left > 0) req = request_of<KT>(a, c, run.b);
+    while (run.left > 0) {
+        if (run.at == (long long)req.units * req.tiles) {
+            do req = request_of<KT>(a, c, ++run.b);
+            while (req.units == 0);
+            run.at = 0;
+        }
+        const int unit = (int)(run.at / req.tiles), t0 = (int)(run.at - (long long)unit * req.tiles);
+        const int nt = (int)min((long long)(req.tiles - t0), run.left);
+        const int h = unit / req.row_tiles, r0 = (unit - h * req.row_tiles) * kSimtRows;
+        const int R = min((req.ell + 1) * a.group - r0, kSimtRows);
+        const int32_t* pages = a.table + (size_t)run.b * a.max_pages;
+
+        __syncthreads();
+        for (int i = tid; i < kSimtRows * D; i += kSimtThreads) {
+            const int r = i / D, d = i - r * D;
+            float x = 0.0f;
+            if (r < R && d < dim) {
+                const int j = (int)a.by_group.div((uint32_t)(r0 + r));
+                const int head = h * a.group + (r0 + r - j * a.group);
+                x = to_f32(((const T*)(a.q + (long long)(req.base + j) * a.q_row + head * a.q_head))[d]);
+            }
+            s_q[i] = x;
+        }
+        const float scale = a.scale * (sizeof(C) == 1 && c.k_scale ? c.k_scale[h] : 1.0f);
+        float acc[4][CN];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < CN; ++n) acc[i][n] = 0.0f;
+        float m = -INFINITY, l = 0.0f;
+        bool bad = false;
+        const int myrow = r0 + srow;
+        const int mypos = req.n + (int)a.by_group.div((uint32_t)myrow);
+
+        for (int t = t0; t < t0 + nt; ++t) {
+            const int key0 = tile_key<KT>(req, t);
+            __syncthreads();
+            constexpr int E = 16 / sizeof(C);
+            for (int i = tid; i < KT * (D / E); i += kSimtThreads) {
+                const int k = i / (D / E), d = (i - k * (D / E)) * E;
+                float kx[E], vx[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) kx[e] = vx[e] = 0.0f;
+                if (d < dim && any_sees(a, req, key0 + k)) {
+                    const long long at = key_at(a, c, pages, key0 + k);
+                    if (at < 0) bad = true;
+                    else {
+                        const long long off = at + h * c.head + d * (int)sizeof(C);
+                        const Vec<C, E> kv = *(const Vec<C, E>*)(c.k + off), vv = *(const Vec<C, E>*)(c.v + off);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            kx[e] = to_f32(kv.x[e]);
+                            vx[e] = to_f32(vv.x[e]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    s_k[k * (D + 4) + d + e] = kx[e];
+                    s_v[k * D + d + e] = vx[e];
+                }
+            }
+            __syncthreads();
+            if (rg * 4 < R) {
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int d = 0; d < D; d += 4) {
+                    const float4 kk = *(const float4*)(s_k + col * (D + 4) + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 qq = *(const float4*)(s_q + (rg * 4 + i) * D + d);
+                        s[i] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[i]))));
+                    }
+                }
+                *(float4*)(s_p + col * kSimtPad + rg * 4) =
+                    make_float4(s[0] * scale, s[1] * scale, s[2] * scale, s[3] * scale);
+            }
+            __syncthreads();
+            {
+                float s[KT / 16], top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < KT / 16; ++i) {
+                    const int k = slane + 16 * i;
+                    s[i] = srow < R && sees(a, mypos, key0 + k) ? s_p[k * kSimtPad + srow] : -INFINITY;
+                    top = fmaxf(top, s[i]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, 16));
+                const float m2 = fmaxf(m, top), base = m2 == -INFINITY ? 0.0f : m2;
+                const float corr = exp2f(m - base);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < KT / 16; ++i) {
+                    const float p = exp2f(s[i] - base);
+                    sum += p;
+                    s_p[(slane + 16 * i) * kSimtPad + srow] = p;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+                l = l * corr + sum;
+                m = m2;
+                if (slane == 0) s_corr[srow] = corr;
+            }
+            __syncthreads();
+            if (rg * 4 < R) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float corr = s_corr[rg * 4 + i];
+#pragma unroll
+                    for (int n = 0; n < CN; ++n) acc[i][n] *= corr;
+                }
+                for (int k = 0; k < KT; ++k) {
+                    const float4 p = *(const float4*)(s_p + k * kSimtPad + rg * 4);
+#pragma unroll
+                    for (int n = 0; n < CN; ++n) {
+                        const float v = s_v[k * D + col + 64 * n];
+                        // a weight of zero takes nothing, whatever the value
+                        acc[0][n] = p.x == 0.0f ? acc[0][n] : fmaf(p.x, v, acc[0][n]);
+                        acc[1][n] = p.y == 0.0f ? acc[1][n] : fmaf(p.y, v, acc[1][n]);
+                        acc[2][n] = p.z == 0.0f ? acc[2][n] : fmaf(p.z, v, acc[2][n]);
+                        acc[3][n] = p.w == 0.0f ? acc[3][n] : fmaf(p.w, v, acc[3][n]);
+                    }
+                }
+            }
+        }
+        if (__syncthreads_or(bad)) {
+            l = __int_as_float(0x7fc00000);
+            if (tid == 0) set_status(a.status, SPEC_ERR_PAGE);
+        }
+        if (slane == 0) {
+            s_l[srow] = l;
+            s_m[srow] = m;
+        }
+        __syncthreads();
+        const bool whole = nt == req.tiles;
+        float* part = part_at(a, blockIdx.x, t0 == 0 ? 1 : 0);
+        const float vs = sizeof(C) == 1 && c.v_scale ? c.v_scale[h] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = rg * 4 + i;
+            if (r >= R) break;
+            if (whole) {
+                int j;
+                const long long row = out_row(a, req, h, r0 + r, &j);
+                const float inv = vs / s_l[r];
+#pragma unroll
+                for (int n = 0; n < CN; ++n)
+                    if (col + 64 * n < dim) ((T*)a.out)[row * dim + col + 64 * n] = from_f32<T>(acc[i][n] * inv);
+                if (a.lse && col == 0) a.lse[row] = (s_m[r] + log2f(s_l[r])) * 0.6931471805599453f;
+            } else {
+#pragma unroll
+                for (int n = 0; n < CN; ++n)
+                    if (col + 64 * n < dim) part[r * dim + col + 64 * n] = acc[i][n] * vs;
+                if (col == 0) {
+                    part[a.tile_rows * dim + r] = s_m[r];
+                    part[a.tile_rows * (dim + 1) + r] = s_l[r];
+                }
+            }
+        }
+        if (t0 == 0 && !whole)
+            open = make_int4(1 + (int)((req.tiles - nt + run.step - 1) / run.step), run.b, unit, 0);
+        run.at += nt;
+        run.left -= nt;
+    }
+    if (tid == 0) a.open[blockIdx.x] = open;
+    report_requests<T, KT>(a, c);
+}
+
+AttendPlan attend_simt_plan(int rows, int head_dim, int sms) {
+    (void)rows;
+    (void)head_dim;
+    AttendPlan p;
+    p.blocks = sms;
+    p.tile_rows = kSimtRows;
+    return p;
+}
+
+namespace {
+
+template <typename T, typename C, int D>
+int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
+    auto* f = k_attend_simt<T, C, D>;
+    if (cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)simt_smem<D>()) !=
+        cudaSuccess)
+        return SPEC_ERR_CUDA;
+    f<<<blocks, kSimtThreads, simt_smem<D>(), st>>>(a, c);
+    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+template <typename T, typename C>
+int launch_dim(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
+    if (c.head_dim <= 64) return launch<T, C, 64>(a, c, blocks, st);
+    if (c.head_dim <= 128) return launch<T, C, 128>(a, c, blocks, st);
+    return launch<T, C, 256>(a, c, blocks, st);
+}
+
+}  // namespace
+
+int attend_simt(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype cache_dt, int blocks,
+                cudaStream_t st) {
+    if (dt == SPEC_F32) return launch_dim<float, float>(a, c, blocks, st);
+    if (dt == SPEC_BF16)
+        return cache_dt == SPEC_E4M3 ? launch_dim<__nv_bfloat16, __nv_fp8_e4m3>(a, c, blocks, st)
+                                     : launch_dim<__nv_bfloat16, __nv_bfloat16>(a, c, blocks, st);
+    return cache_dt == SPEC_E4M3 ? launch_dim<__half, __nv_fp8_e4m3>(a, c, blocks, st)
+                                 : launch_dim<__half, __half>(a, c, blocks, st);
+}
+
+}  // namespace specv
