@@ -131,7 +131,8 @@ size_t spec_attend_workspace_bytes(int B, int gamma, int q_heads, int kv_heads, 
         head_dim < 8 || head_dim > SPEC_MAX_HEAD_DIM || (head_dim & 7))
         return 0;
     const int rows = (gamma + 1) * (q_heads / kv_heads);
-    return header_bytes() + parts_bytes(attend_simt_plan(rows, head_dim, kMostSms), head_dim);
+    return header_bytes() + max(parts_bytes(attend_simt_plan(rows, head_dim, kMostSms), head_dim),
+                                parts_bytes(attend_mma_plan(rows, head_dim, kMostSms), head_dim));
 }
 
 int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, spec_dtype dt, int q_heads,
@@ -188,11 +189,16 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
     a.by_group = FastDiv((uint32_t)a.group);
     cudaStream_t st = (cudaStream_t)stream;
 
-    const AttendPlan p = attend_simt_plan((gamma + 1) * a.group, c.head_dim, sms);
+    const int most = (gamma + 1) * a.group;
+    const AttendPlan p = dt == SPEC_F32 ? attend_simt_plan(most, c.head_dim, sms)
+                                        : attend_mma_plan(most, c.head_dim, sms);
     a.tile_rows = p.tile_rows;
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
     a.least = 2;
-    if ((rc = attend_simt(a, c, dt, cache->dt, p.blocks, st)) != SPEC_OK) return rc;
+    if (dt == SPEC_F32) rc = attend_simt(a, c, p.blocks, st);
+    else if (cache->dt == SPEC_E4M3) rc = attend_mma8(a, c, dt, p.blocks, st);
+    else rc = attend_mma16(a, c, dt, p.blocks, st);
+    if (rc != SPEC_OK) return rc;
     if (dt == SPEC_F32) return launch_join<float>(a, c, p.blocks, st);
     if (dt == SPEC_BF16) return launch_join<__nv_bfloat16>(a, c, p.blocks, st);
     return launch_join<__half>(a, c, p.blocks, st);

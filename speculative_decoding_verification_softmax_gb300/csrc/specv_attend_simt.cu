@@ -19,8 +19,9 @@ constexpr size_t simt_smem() {
     return sizeof(float) * (kSimtRows * D + kSimtKeys * (D + 4) + kSimtKeys * D + kSimtKeys * kSimtPad);
 }
 
-template <typename T, typename C, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, CacheView c) {
+    using T = float;
     constexpr int KT = kSimtKeys, CN = D / 64;
     extern __shared__ float4 smem4[];
     float* s_q = (float*)smem4;             // [16][D]
@@ -58,11 +59,11 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
             if (r < R && d < dim) {
                 const int j = (int)a.by_group.div((uint32_t)(r0 + r));
                 const int head = h * a.group + (r0 + r - j * a.group);
-                x = to_f32(((const T*)(a.q + (long long)(req.base + j) * a.q_row + head * a.q_head))[d]);
+                x = ((const T*)(a.q + (long long)(req.base + j) * a.q_row + head * a.q_head))[d];
             }
             s_q[i] = x;
         }
-        const float scale = a.scale * (sizeof(C) == 1 && c.k_scale ? c.k_scale[h] : 1.0f);
+        const float scale = a.scale;
         float acc[4][CN];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -76,30 +77,20 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
         for (int t = t0; t < t0 + nt; ++t) {
             const int key0 = tile_key<KT>(req, t);
             __syncthreads();
-            constexpr int E = 16 / sizeof(C);
-            for (int i = tid; i < KT * (D / E); i += kSimtThreads) {
-                const int k = i / (D / E), d = (i - k * (D / E)) * E;
-                float kx[E], vx[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) kx[e] = vx[e] = 0.0f;
+            for (int i = tid; i < KT * (D / 4); i += kSimtThreads) {
+                const int k = i / (D / 4), d = (i - k * (D / 4)) * 4;
+                float4 kx = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vx = kx;
                 if (d < dim && any_sees(a, req, key0 + k)) {
                     const long long at = key_at(a, c, pages, key0 + k);
-                    if (at < 0) bad = true;
-                    else {
-                        const long long off = at + h * c.head + d * (int)sizeof(C);
-                        const Vec<C, E> kv = *(const Vec<C, E>*)(c.k + off), vv = *(const Vec<C, E>*)(c.v + off);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            kx[e] = to_f32(kv.x[e]);
-                            vx[e] = to_f32(vv.x[e]);
-                        }
+                    if (at < 0) {
+                        bad = true;
+                    } else {
+                        kx = *(const float4*)(c.k + at + h * c.head + d * 4);
+                        vx = *(const float4*)(c.v + at + h * c.head + d * 4);
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    s_k[k * (D + 4) + d + e] = kx[e];
-                    s_v[k * D + d + e] = vx[e];
-                }
+                *(float4*)(s_k + k * (D + 4) + d) = kx;
+                *(float4*)(s_v + k * D + d) = vx;
             }
             __syncthreads();
             if (rg * 4 < R) {
@@ -174,7 +165,6 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
         __syncthreads();
         const bool whole = nt == req.tiles;
         float* part = part_at(a, blockIdx.x, t0 == 0 ? 1 : 0);
-        const float vs = sizeof(C) == 1 && c.v_scale ? c.v_scale[h] : 1.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = rg * 4 + i;
@@ -182,15 +172,15 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
             if (whole) {
                 int j;
                 const long long row = out_row(a, req, h, r0 + r, &j);
-                const float inv = vs / s_l[r];
+                const float inv = 1.0f / s_l[r];
 #pragma unroll
                 for (int n = 0; n < CN; ++n)
-                    if (col + 64 * n < dim) ((T*)a.out)[row * dim + col + 64 * n] = from_f32<T>(acc[i][n] * inv);
+                    if (col + 64 * n < dim) ((T*)a.out)[row * dim + col + 64 * n] = acc[i][n] * inv;
                 if (a.lse && col == 0) a.lse[row] = (s_m[r] + log2f(s_l[r])) * 0.6931471805599453f;
             } else {
 #pragma unroll
                 for (int n = 0; n < CN; ++n)
-                    if (col + 64 * n < dim) part[r * dim + col + 64 * n] = acc[i][n] * vs;
+                    if (col + 64 * n < dim) part[r * dim + col + 64 * n] = acc[i][n];
                 if (col == 0) {
                     part[a.tile_rows * dim + r] = s_m[r];
                     part[a.tile_rows * (dim + 1) + r] = s_l[r];
@@ -217,9 +207,9 @@ AttendPlan attend_simt_plan(int rows, int head_dim, int sms) {
 
 namespace {
 
-template <typename T, typename C, int D>
+template <int D>
 int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
-    auto* f = k_attend_simt<T, C, D>;
+    auto* f = k_attend_simt<D>;
     if (cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)simt_smem<D>()) !=
         cudaSuccess)
         return SPEC_ERR_CUDA;
@@ -227,23 +217,12 @@ int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st)
     return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
-template <typename T, typename C>
-int launch_dim(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
-    if (c.head_dim <= 64) return launch<T, C, 64>(a, c, blocks, st);
-    if (c.head_dim <= 128) return launch<T, C, 128>(a, c, blocks, st);
-    return launch<T, C, 256>(a, c, blocks, st);
-}
-
 }  // namespace
 
-int attend_simt(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype cache_dt, int blocks,
-                cudaStream_t st) {
-    if (dt == SPEC_F32) return launch_dim<float, float>(a, c, blocks, st);
-    if (dt == SPEC_BF16)
-        return cache_dt == SPEC_E4M3 ? launch_dim<__nv_bfloat16, __nv_fp8_e4m3>(a, c, blocks, st)
-                                     : launch_dim<__nv_bfloat16, __nv_bfloat16>(a, c, blocks, st);
-    return cache_dt == SPEC_E4M3 ? launch_dim<__half, __nv_fp8_e4m3>(a, c, blocks, st)
-                                 : launch_dim<__half, __half>(a, c, blocks, st);
+int attend_simt(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
+    if (c.head_dim <= 64) return launch<64>(a, c, blocks, st);
+    if (c.head_dim <= 128) return launch<128>(a, c, blocks, st);
+    return launch<256>(a, c, blocks, st);
 }
 
 }  // namespace specv
