@@ -20,8 +20,8 @@ _CSRC = os.path.join(_HERE, "csrc")
 LIB_PATH = os.path.join(_HERE, "libspecv.so")
 SOURCES = ["specv_verify.cu", "specv_sched.cu", "specv_api.cu", "specv_static.cu", "specv_pages.cu",
            "specv_append.cu", "specv_attend.cu", "specv_attend_simt.cu", "specv_attend_mma16.cu",
-           "specv_attend_mma8.cu"]
-HEADERS = ["specv_common.cuh", "specv_rowstats.cuh", "specv_cache.cuh", "specv_attend.cuh", "specv_attend_mma.cuh",
+           "specv_attend_mma8.cu", "specv_attend_tc.cu"]
+HEADERS = ["specv_common.cuh", "specv_rowstats.cuh", "specv_cache.cuh", "specv_attend.cuh", "specv_attend_mma.cuh", "specv_attend_tc.cuh",
            "specv_trace.h"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]

@@ -198,4 +198,9 @@ AttendPlan attend_mma_plan(int rows, int head_dim, int sms);
 int attend_mma16(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 int attend_mma8(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 
+// 16-bit rows and caches, many rows a KV head: the tensor cores.
+bool attend_tc_takes(const CacheView& c, int rows);
+AttendPlan attend_tc_plan(int sms);
+int attend_tc(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
+
 }  // namespace specv
