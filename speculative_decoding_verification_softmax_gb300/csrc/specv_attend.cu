@@ -191,7 +191,7 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
     cudaStream_t st = (cudaStream_t)stream;
 
     const int most = (gamma + 1) * a.group;
-    const bool tc = dt != SPEC_F32 && cache->dt == dt && attend_tc_takes(c, most);
+    const bool tc = dt != SPEC_F32 && attend_tc_takes(c, most);
     const AttendPlan p = dt == SPEC_F32 ? attend_simt_plan(most, c.head_dim, sms)
                          : tc           ? attend_tc_plan(sms)
                                         : attend_mma_plan(most, c.head_dim, sms);
@@ -199,7 +199,7 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
     a.least = 2;
     if (dt == SPEC_F32) rc = attend_simt(a, c, p.blocks, st);
-    else if (tc) rc = attend_tc(a, c, dt, p.blocks, st);
+    else if (tc) rc = attend_tc(a, c, dt, cache->dt, p.blocks, st);
     else if (cache->dt == SPEC_E4M3) rc = attend_mma8(a, c, dt, p.blocks, st);
     else rc = attend_mma16(a, c, dt, p.blocks, st);
     if (rc != SPEC_OK) return rc;

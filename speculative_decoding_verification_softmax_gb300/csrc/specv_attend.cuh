@@ -166,9 +166,10 @@ __device__ __forceinline__ long long key_at(const AttendArgs& a, const CacheView
 }
 
 // After its run, a block reports requests without work, and fills the rows of
-// those whose positions do not fit (blocks share the requests).
+// those whose positions do not fit (blocks share the requests).  Called by the
+// first `threads` threads of the block.
 template <typename T, int KT>
-__device__ __forceinline__ void report_requests(const AttendArgs& a, const CacheView& c) {
+__device__ __forceinline__ void report_requests(const AttendArgs& a, const CacheView& c, int threads) {
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const Request r = request_of<KT>(a, c, b);
         if (r.code == SPEC_OK) continue;
@@ -177,9 +178,9 @@ __device__ __forceinline__ void report_requests(const AttendArgs& a, const Cache
         const long long first = (long long)r.base * a.q_heads, n = (long long)(r.ell + 1) * a.q_heads;
         const float nan = __int_as_float(0x7fc00000);
         T* out = (T*)a.out + first * c.head_dim;
-        for (long long i = threadIdx.x; i < n * c.head_dim; i += blockDim.x) out[i] = from_f32<T>(nan);
+        for (long long i = threadIdx.x; i < n * c.head_dim; i += threads) out[i] = from_f32<T>(nan);
         if (a.lse)
-            for (long long i = threadIdx.x; i < n; i += blockDim.x) a.lse[first + i] = nan;
+            for (long long i = threadIdx.x; i < n; i += threads) a.lse[first + i] = nan;
     }
 }
 
@@ -198,9 +199,10 @@ AttendPlan attend_mma_plan(int rows, int head_dim, int sms);
 int attend_mma16(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 int attend_mma8(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 
-// 16-bit rows and caches, many rows a KV head: the tensor cores.
+// 16-bit rows, many of them a KV head: the tensor cores, over 16-bit and e4m3 caches.
 bool attend_tc_takes(const CacheView& c, int rows);
 AttendPlan attend_tc_plan(int sms);
-int attend_tc(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
+int attend_tc(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype cache_dt, int blocks,
+              cudaStream_t st);
 
 }  // namespace specv

@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
         run.left -= nt;
     }
     if (tid == 0) a.open[blockIdx.x] = open;
-    report_requests<O, KT>(a, c);
+    report_requests<O, KT>(a, c, THREADS);
 }
 
 // ------------------------------------------------------------------- launch

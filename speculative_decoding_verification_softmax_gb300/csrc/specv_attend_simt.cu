@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
         run.left -= nt;
     }
     if (tid == 0) a.open[blockIdx.x] = open;
-    report_requests<T, KT>(a, c);
+    report_requests<T, KT>(a, c, kSimtThreads);
 }
 
 AttendPlan attend_simt_plan(int rows, int head_dim, int sms) {

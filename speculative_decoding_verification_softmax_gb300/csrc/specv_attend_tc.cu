@@ -22,17 +22,22 @@ EncodeTiled encoder() {
     return fn;
 }
 
-// The cache as {head_dim, page_size, kv_heads, pages}, in boxes of 64 values
-// and `box` tokens; values behind head_dim read as zero.
-bool make_map(CUtensorMap& map, void* at, const CacheView& c, bool half, int box) {
+// The cache as {head_dim, page_size, kv_heads, pages}, in boxes of 64 16-bit
+// values (a swizzled panel) or of whole e4m3 rows, and `box` tokens; values
+// behind head_dim read as zero.
+bool make_map(CUtensorMap& map, void* at, const CacheView& c, spec_dtype dt, int box) {
     const EncodeTiled fn = encoder();
     if (!fn) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
                                 (cuuint64_t)c.pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c.token, (cuuint64_t)c.head, (cuuint64_t)c.page};
-    const cuuint32_t extent[4] = {64, (cuuint32_t)box, 1, 1}, step[4] = {1, 1, 1, 1};
-    return fn(&map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, at, dims, strides,
-              extent, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint32_t extent[4] = {dt == SPEC_E4M3 && c.head_dim > 64 ? 128u : 64u, (cuuint32_t)box, 1, 1}, step[4] = {1, 1, 1, 1};
+    return fn(&map,
+              dt == SPEC_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+              : dt == SPEC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              4, at, dims, strides, extent, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              dt == SPEC_E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -42,15 +47,22 @@ int box_tokens(int page_size) {
     return box;
 }
 
-template <typename T, int D>
+template <typename T, typename O, bool F8, int D>
+int launch_dim(const AttendArgs& a, const CacheView& c, const TcArgs& tc, const CUtensorMap& mk,
+               const CUtensorMap& mv, int blocks, cudaStream_t st) {
+    using Sh = TcShape<F8, D>;
+    auto* f = k_attend_tc<T, O, F8, D>;
+    if (cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    f<<<blocks, kTcThreads, Sh::kSmem, st>>>(a, c, tc, mk, mv);
+    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+template <typename T, typename O, bool F8>
 int launch(const AttendArgs& a, const CacheView& c, const TcArgs& tc, const CUtensorMap& mk, const CUtensorMap& mv,
            int blocks, cudaStream_t st) {
-    auto* f = k_attend_tc<T, D>;
-    if (cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem) !=
-        cudaSuccess)
-        return SPEC_ERR_CUDA;
-    f<<<blocks, kTcThreads, TcShape<D>::kSmem, st>>>(a, c, tc, mk, mv);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return c.head_dim <= 64 ? launch_dim<T, O, F8, 64>(a, c, tc, mk, mv, blocks, st)
+                            : launch_dim<T, O, F8, 128>(a, c, tc, mk, mv, blocks, st);
 }
 
 }  // namespace
@@ -70,19 +82,19 @@ AttendPlan attend_tc_plan(int sms) {
     return p;
 }
 
-int attend_tc(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st) {
+int attend_tc(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype cache_dt, int blocks,
+              cudaStream_t st) {
     TcArgs tc;
     tc.box = box_tokens(c.page_size);
     tc.shift = 0;
     while ((1 << tc.shift) < tc.box) ++tc.shift;
     CUtensorMap mk, mv;
-    const bool half = dt == SPEC_F16;
-    if (!make_map(mk, c.k, c, half, tc.box) || !make_map(mv, c.v, c, half, tc.box)) return SPEC_ERR_CUDA;
-    if (c.head_dim <= 64)
-        return half ? launch<__half, 64>(a, c, tc, mk, mv, blocks, st)
-                    : launch<__nv_bfloat16, 64>(a, c, tc, mk, mv, blocks, st);
-    return half ? launch<__half, 128>(a, c, tc, mk, mv, blocks, st)
-                : launch<__nv_bfloat16, 128>(a, c, tc, mk, mv, blocks, st);
+    if (!make_map(mk, c.k, c, cache_dt, tc.box) || !make_map(mv, c.v, c, cache_dt, tc.box)) return SPEC_ERR_CUDA;
+    if (cache_dt == SPEC_E4M3)
+        return dt == SPEC_F16 ? launch<__half, __half, true>(a, c, tc, mk, mv, blocks, st)
+                              : launch<__half, __nv_bfloat16, true>(a, c, tc, mk, mv, blocks, st);
+    return dt == SPEC_F16 ? launch<__half, __half, false>(a, c, tc, mk, mv, blocks, st)
+                          : launch<__nv_bfloat16, __nv_bfloat16, false>(a, c, tc, mk, mv, blocks, st);
 }
 
 }  // namespace specv

@@ -11,14 +11,17 @@
 // work for the other.  Each stream has its own S and O columns in TMEM and its
 // own running maximum and sum; the unit's end joins them.  P overlays S.
 //   warps 0-3, 4-7   softmax of the even and odd tiles, a row a thread; the
-//                    query rows' load and the unit's output
-//   warps 8-11       loads: K and V tiles, in the order of their use, through a
+//                    unit's output
+//   warps 8-11       16-bit cache: repair of V tiles that a border cuts; e4m3
+//                    cache: the widening of all tiles to fp16 (exact)
+//   warps 12-13      the next unit's query rows
+//   warp 14          K and V tiles by TMA, in the order of their use, through a
 //                    ring of shared-memory slots that runs on over the units
-//   warp 12          one thread issues all matrix instructions
-// The loads are TMA boxes of as many tokens as always lie in one page.  V rows
-// that some query row must not see (the cache's end, the window's edges) are
-// loaded by the warps themselves instead: what nobody sees becomes zero, and a
-// value that is not finite is left out and added by itself to its rows.
+//   warp 15          one thread issues all matrix instructions
+// A TMA box is as many tokens as always lie in one page.  In V tiles that some
+// query row must not see whole (the cache's end, the window's edges), rows that
+// nobody sees become zero, and a value that is not finite is taken out and added
+// by itself to the rows that see it.
 #pragma once
 
 #include <cuda.h>
@@ -31,22 +34,27 @@ namespace specv {
 
 constexpr int kTcKeys = 128;
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 13 * 32;
-constexpr int kTcUnits = 8;  // flags of units under way
+constexpr int kTcThreads = 16 * 32;
+constexpr int kTcUnits = 16;  // flags of units under way
 
 // A running maximum stays the reference until it is passed by this much (to
 // base 2): weights reach 2^8 instead of 1, exactly as well in 16 bits, and the
 // output in TMEM is scaled again a few times a unit instead of every tile.
 constexpr float kTcSlack = 8.0f;
 
-template <int D>
+// Shared memory: query rows, slots of 16-bit K or V tiles, and for an e4m3
+// cache the slots in which its tiles arrive.  The copies in flight cover HBM's
+// latency: 96 KB or more of 16-bit tiles, 64 KB or more of e4m3 ones.
+template <bool F8, int D>
 struct TcShape {
-    static constexpr int kPanel = kTcKeys * 128;       // 64 columns of a tile, 128-byte rows
-    static constexpr int kTile = kPanel * (D / 64);    // K or V of a tile
-    static constexpr int kSlots = D == 64 ? 10 : 6;
+    static constexpr int kPanel = kTcKeys * 128;     // 64 columns of a tile, 128-byte rows
+    static constexpr int kTile = kPanel * (D / 64);  // K or V of a tile
+    static constexpr int kRawTile = kTcKeys * D;
+    static constexpr int kSlots = F8 ? (D == 64 ? 6 : 3) : (D == 64 ? 12 : 6);
+    static constexpr int kRaw = F8 ? (D == 64 ? 10 : 5) : 0;
     static constexpr int kQ = kTcRows * 128 * (D / 64);
-    static constexpr int kSmem = 1024 + kQ + kSlots * kTile;
-    static constexpr int kCols = 512;                  // TMEM columns: S0, S1, O0, O1 (a power of two)
+    static constexpr int kSmem = 1024 + kQ + kSlots * kTile + kRaw * kRawTile;
+    static constexpr int kCols = 512;  // TMEM columns: S0, S1, O0, O1 (a power of two)
 };
 
 struct TcArgs {
@@ -85,19 +93,28 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
         : "memory");
 }
-// 32 columns of the warp's 32 lanes, and the wait for them.
+// 32 columns of the warp's 32 lanes; the values are there after tc_wait32.
 __device__ __forceinline__ void tc_ld32(float (&x)[32], uint32_t at) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at)
+        : "memory");
+}
+// Waits for the warp's loads; names the values, so that no use moves above it.
+__device__ __forceinline__ void tc_wait32(float (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
+          "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]),
+          "+f"(x[16]), "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]),
+          "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]), "+f"(x[30]), "+f"(x[31])
+        :
         : "memory");
 }
 __device__ __forceinline__ void tc_st32(uint32_t at, const float (&x)[32]) {
@@ -132,6 +149,15 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void tc_more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void tc_fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Operand descriptors: 128-byte swizzle, eight 128-byte rows an atom.  K-major
 // (Q, K: the columns of a product adjacent): atoms of further rows 1024 bytes on.
 // MN-major (V: a key's row is the product's N): atoms of further keys 1024 bytes
@@ -146,16 +172,33 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t panel) {
 
 // Waits for phase `parity`.  A wait that runs out of time sets `fail`, and all
 // other waits of the block then end at once: every role runs its loops to their
-// ends, without results, and the block returns.
+// ends, without results, and the block returns.  The waiting thread is suspended
+// for up to 20 us at a time and looks at the clock every 16th time only:
+// spinning on the clock slowed the softmax warps' exponentials several times over.
+__device__ __forceinline__ bool tc_try(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
+    if (tc_try(bar, parity)) return true;
+    unsigned long long t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        if (tc_try(bar, parity)) return true;
         if (*fail) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            *fail = 1;
-            return false;
+        if ((n & 15) == 0) {
+            const unsigned long long now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                *fail = 1;
+                return false;
+            }
         }
     }
 }
@@ -176,7 +219,7 @@ struct Walk {
     int b, unit, t0, nt, h, r0, R;
     long long at, left, step;
 
-    __device__ void start(const AttendArgs& a, const CacheView& c, const Run& run) {
+    __device__ __forceinline__ Walk(const AttendArgs& a, const CacheView& c, const Run& run) {
         b = run.b;
         at = run.at;
         left = run.left;
@@ -184,7 +227,7 @@ struct Walk {
         nt = 0;
         if (left > 0) req = request_of<kTcKeys>(a, c, b);
     }
-    __device__ bool next(const AttendArgs& a, const CacheView& c) {
+    __device__ __forceinline__ bool next(const AttendArgs& a, const CacheView& c) {
         at += nt;
         left -= nt;
         if (left <= 0) return false;
@@ -203,177 +246,324 @@ struct Walk {
     }
 };
 
-template <typename T, int D>
+
+// Item i of a unit of nt tiles, in the order of use: K0, K1, V0, K2, V1, ...
+__device__ __forceinline__ void item_of(int i, int nt, bool& is_v, int& t) {
+    if (i < 2 && nt > 1) {
+        is_v = false;
+        t = i;
+    } else if (nt == 1) {
+        is_v = i == 1;
+        t = 0;
+    } else {
+        const int x = i - 2, pairs = 2 * (nt - 2);
+        is_v = x >= pairs || (x & 1) == 0;
+        t = x >= pairs ? nt - 2 + (x - pairs) : is_v ? x >> 1 : (x >> 1) + 2;
+    }
+}
+
+__device__ __forceinline__ bool sees_all(const AttendArgs& a, const Request& r, int t) {
+    return t <= r.n && (a.window == 0 || r.n + r.ell - t < a.window || t < a.sinks);
+}
+
+// Bits lo .. hi - 1 of a word, for any lo and hi.
+__device__ __forceinline__ uint32_t bits_of(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 32);
+    return lo >= hi ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (32 - hi));
+}
+// Which of the 32 positions from `key` the row at position p sees.
+__device__ __forceinline__ uint32_t seen_bits(const AttendArgs& a, int p, int key) {
+    const int hi = min(p - key + 1, 32);
+    if (a.window == 0) return bits_of(0, hi);
+    // p - t < window, without an overflow for any window
+    const int lo = p >= a.window ? p - a.window + 1 - key : 0;
+    return bits_of(lo, hi) | bits_of(0, min(hi, a.sinks > key ? min(a.sinks - key, 32) : 0));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
+    uint32_t r;
+    if (std::is_same<T, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Takes the values that are not finite out of eight 16-bit ones.
+template <typename T>
+__device__ __forceinline__ bool take_out(uint4& v) {
+    uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    bool any = false;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        if (tc_nonfinite<T>(e[z], 0xffffu)) {
+            e[z] &= 0xffff0000u;
+            any = true;
+        }
+        if (tc_nonfinite<T>(e[z], 0xffff0000u)) {
+            e[z] &= 0xffffu;
+            any = true;
+        }
+    }
+    v = make_uint4(e[0], e[1], e[2], e[3]);
+    return any;
+}
+
+// Two e4m3 values to fp16 (exact).
+__device__ __forceinline__ uint32_t tc_widen(uint32_t two) {
+    uint32_t r;
+    asm("{.reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+// T: type of the products, O: type of q and out, F8: e4m3 cache.
+template <typename T, typename O, bool F8, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_attend_tc(AttendArgs a, CacheView c, TcArgs tc, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv) {
-    using Sh = TcShape<D>;
-    constexpr int KT = kTcKeys, NS = Sh::kSlots, CW = D / 8;  // chunks of a row
+    using Sh = TcShape<F8, D>;
+    constexpr int KT = kTcKeys, NS = Sh::kSlots, CW = D / 8;  // CW: 16-byte chunks of a row
+    constexpr int NR = F8 ? Sh::kRaw : NS;                    // slots that TMA fills
     extern __shared__ char smem_raw[];
-    __shared__ __align__(8) uint64_t full[NS], empty[NS], s_full[2], p_full[2], o_done[2], q_full, drain;
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[NR];
+    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail, s_flags[kTcUnits];
     __shared__ long long s_scan[kTcThreads / 32 + 1];
     __shared__ Run s_run;
     __shared__ float s_ml[2][kTcRows];
+    __shared__ float s_row[2][std::is_same<T, O>::value ? 1 : kTcRows];  // scales of two units' query rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
-    const uint32_t sq = base, ring = base + Sh::kQ;
+    const uint32_t sq = base, ring = base + Sh::kQ, raws = ring + NS * Sh::kTile;
 
-    if (warp == 12) tc_alloc(&s_tmem, Sh::kCols);
+    if (warp == 15) tc_alloc(&s_tmem, Sh::kCols);
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 4);
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(&q_full, 8);
+        mbar_init(&q_full, 2);
+        mbar_init(&q_empty, 1);
         mbar_init(&drain, 1);
         fence_mbar_init();
         s_fail = 0;
     }
     if (tid < kTcUnits) s_flags[tid] = 0;
     tc_fence_before();
-    const Run run = run_of<KT, kTcThreads>(a, c, s_scan, &s_run);  // also the barrier behind the set-up
+    run_of<KT, kTcThreads>(a, c, s_scan, &s_run);  // also the barrier behind the set-up
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     volatile int* fail = &s_fail;
-    Walk w;
-    w.start(a, c, run);
-    int4 open = make_int4(0, 0, 0, 0);
 
-    if (warp >= 8 && warp < 12) {
-        // ------------------------------------------------------------ loads
-        // Items of a unit, in the order of their use: K0, K1, V0, K2, V1, ...
-        const int lw = warp - 8, lt = tid - 8 * 32;
+    // registers: the softmax warps' shares are 168, the others' 88, together
+    // what the block was launched with (512 threads of 128).  No warp takes
+    // registers again afterwards: one that finished early could take those that
+    // the softmax warps still wait for
+    if (warp >= 8) {
+    tc_fewer_registers<88>();
+    if (warp == 14) {
+        // ------------------------------------------------------- TMA of K and V
         const int boxes = KT / tc.box;
         uint32_t item = 0, issued = 0;
         int u = 0;
+        Walk w(a, c, s_run);
         while (w.next(a, c)) {
             const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
             const int end = w.req.n + w.req.ell;
-            bool bad = false;
-            for (int i = 0; i < 2 * w.nt; ++i) {
-                // item i: K of tile i for i < 2 (or the only one), then V and K in turn
+            for (int i = 0; i < 2 * w.nt; ++i, ++item) {
                 bool is_v;
                 int t;
-                if (w.nt == 1) {
-                    is_v = i == 1;
-                    t = 0;
-                } else if (i < 2) {
-                    is_v = false;
-                    t = i;
-                } else {
-                    const int x = i - 2;
-                    if (x < 2 * (w.nt - 2)) {
-                        is_v = (x & 1) == 0;
-                        t = is_v ? x >> 1 : (x >> 1) + 2;
-                    } else {
-                        is_v = true;
-                        t = w.nt - 2 + (x - 2 * (w.nt - 2));
-                    }
-                }
+                item_of(i, w.nt, is_v, t);
                 const int key0 = tile_key<KT>(w.req, w.t0 + t);
-                const int slot = (int)(item % NS);
-                const uint32_t dst = ring + slot * Sh::kTile;
                 const bool whole = all_see<KT>(a, w.req, key0);
-                const bool by_hand = is_v && !whole;
-                // the lane's box of the tile: where it lies, looked up before the
-                // slot is free; -1 if nobody sees any of it
-                long long at = -1;
+                // the lane's box of the tile, looked up before the slot is free
                 int page = -1, token = 0;
-                if ((by_hand || lw == 0) && lane < boxes) {
-                    const int k = key0 + (lane << tc.shift);
-                    bool need = k <= end;
-                    if (need && !whole) {
-                        need = false;
-                        for (int x = 0; x < tc.box; ++x) need |= any_sees(a, w.req, k + x);
-                    }
-                    if (need) {
-                        const uint32_t place = c.by_page.div((uint32_t)k);
-                        token = k - (int)place * c.page_size;
-                        page = pages[place];
-                        if (page < 0 || page >= c.pages) {
-                            bad = true;
-                            page = -1;
-                        } else {
-                            at = (long long)page * c.page + (long long)token * c.token + w.h * c.head;
-                        }
+                const int k = key0 + (lane << tc.shift);
+                bool need = lane < boxes && k <= end;
+                if (need && !whole) {
+                    need = false;
+                    for (int x = 0; x < tc.box; ++x) need |= any_sees(a, w.req, k + x);
+                }
+                if (need) {
+                    const uint32_t place = c.by_page.div((uint32_t)k);
+                    token = k - (int)place * c.page_size;
+                    page = pages[place];
+                    if (page < 0 || page >= c.pages) {
+                        page = -1;
+                        atomicOr(&s_flags[u & (kTcUnits - 1)], 1);
                     }
                 }
-                if (bad) atomicOr(&s_flags[u & (kTcUnits - 1)], 1);
+                const int slot = (int)(item % NR);
+                uint64_t* freed = F8 ? &raw_empty[slot] : &empty[slot];
                 const bool ok =
-                    __all_sync(0xffffffffu, item < NS || tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail));
-                if (by_hand) {
-                    if (ok) {
-                        bool dirty = false;
-                        constexpr int RS = 128 / CW, BATCH = 8;  // rows of a step, steps in flight
-                        const int ch = lt % CW;
-#pragma unroll 1
-                        for (int i0 = 0; i0 < KT / RS; i0 += BATCH) {
-                            uint4 v[BATCH];
-#pragma unroll
-                            for (int q = 0; q < BATCH; ++q) {
-                                const int k = lt / CW + (i0 + q) * RS;
-                                const long long from = __shfl_sync(0xffffffffu, at, k >> tc.shift);
-                                v[q] = make_uint4(0u, 0u, 0u, 0u);
-                                if (from >= 0 && ch * 8 < c.head_dim && any_sees(a, w.req, key0 + k))
-                                    v[q] = *(const uint4*)(c.v + from + (k & (tc.box - 1)) * c.token + ch * 16);
-                            }
-#pragma unroll
-                            for (int q = 0; q < BATCH; ++q) {
-                                uint32_t e[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    if (tc_nonfinite<T>(e[z], 0xffffu)) {
-                                        e[z] &= 0xffff0000u;
-                                        dirty = true;
-                                    }
-                                    if (tc_nonfinite<T>(e[z], 0xffff0000u)) {
-                                        e[z] &= 0xffffu;
-                                        dirty = true;
-                                    }
-                                }
-                                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                                 dst + panel_at(lt / CW + (i0 + q) * RS, ch)),
-                                             "r"(e[0]), "r"(e[1]), "r"(e[2]), "r"(e[3])
-                                             : "memory");
-                            }
-                        }
-                        if (dirty) atomicOr(&s_flags[u & (kTcUnits - 1)], 2);
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[slot]);
-                } else if (lw == 0) {
-                    const bool have = ok && page >= 0;
-                    const int n = __popc(__ballot_sync(0xffffffffu, have));
-                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)n * tc.box * 128 * (D / 64));
-                    __syncwarp();
-                    if (have) {
+                    __all_sync(0xffffffffu, item < NR || tc_wait(freed, ((item / NR) & 1) ^ 1, fail));
+                // a 16-bit tile is ready when it has landed, unless it is to be repaired
+                uint64_t* bar = F8 || (is_v && !whole) ? &raw_full[slot] : &full[slot];
+                const bool have = ok && page >= 0;
+                const int n = __popc(__ballot_sync(0xffffffffu, have));
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * tc.box * (F8 ? D : 2 * D));
+                __syncwarp();
+                if (have) {
+                    const uint32_t row = (uint32_t)lane << tc.shift;
+                    if (F8) {
+                        tma_box(raws + slot * Sh::kRawTile + row * D, is_v ? &mv : &mk, 0, token, w.h, page, bar);
+                    } else {
 #pragma unroll
                         for (int p = 0; p < D / 64; ++p)
-                            tma_box(dst + p * Sh::kPanel + (lane << tc.shift) * 128, is_v ? &mv : &mk, p * 64, token, w.h,
-                                    page, &full[slot]);
+                            tma_box(ring + slot * Sh::kTile + p * Sh::kPanel + row * 128, is_v ? &mv : &mk, p * 64,
+                                    token, w.h, page, bar);
                     }
-                    if (ok) issued = item + 1;
-                } else if (lane == 0) {
-                    mbar_arrive(&full[slot]);
                 }
+                if (ok) issued = item + 1;
                 __syncwarp();
-                ++item;
             }
             ++u;
         }
-        if (*fail && warp == 8) {  // copies under way land before the block ends
-            for (uint32_t k = issued > NS ? issued - NS : 0; k < issued; ++k)
-                mbar_wait_bounded(&full[k % NS], (k / NS) & 1);
+        if (*fail) {  // copies under way land before the block ends: their time is far below the limit
+            const unsigned long long t0 = globaltimer_ns();
+            while (issued > 0 && globaltimer_ns() - t0 < 1000000ull) {}
         }
-    } else if (warp == 12) {
+    } else if (warp >= 8 && warp < 12) {
+        // ------------------------------------- repair of V, or widening of K and V
+        const int lt = tid - 8 * 32;
+        uint32_t item = 0, turns = 0;  // turns: phases of raw_full by slot (16-bit cache)
+        int u = 0;
+        Walk w(a, c, s_run);
+        while (w.next(a, c)) {
+            for (int i = 0; i < 2 * w.nt; ++i, ++item) {
+                bool is_v;
+                int t;
+                item_of(i, w.nt, is_v, t);
+                const int key0 = tile_key<KT>(w.req, w.t0 + t);
+                const bool cut = is_v && !all_see<KT>(a, w.req, key0);
+                if (!F8 && !cut) continue;
+                const int slot = (int)(item % NS);
+                const uint32_t to = ring + slot * Sh::kTile;
+                bool dirty = false;
+                if (F8) {
+                    const int rs = (int)(item % NR);
+                    tc_wait(&raw_full[rs], (item / NR) & 1, fail);
+                    if (item >= NS) tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail);
+                    const uint32_t from = raws + rs * Sh::kRawTile;
+#pragma unroll 4
+                    for (int x = lt; x < KT * (D / 16); x += 128) {
+                        const int k = x / (D / 16), ch = x - k * (D / 16);
+                        uint4 v = lds16(from + x * 16);
+                        if (cut && !any_sees(a, w.req, key0 + k)) v = make_uint4(0u, 0u, 0u, 0u);
+                        uint4 lo = make_uint4(tc_widen(v.x), tc_widen(v.x >> 16), tc_widen(v.y), tc_widen(v.y >> 16));
+                        uint4 hi = make_uint4(tc_widen(v.z), tc_widen(v.z >> 16), tc_widen(v.w), tc_widen(v.w >> 16));
+                        if (cut && !sees_all(a, w.req, key0 + k)) {
+                            dirty |= take_out<T>(lo);
+                            dirty |= take_out<T>(hi);
+                        }
+                        sts16(to + panel_at(k, 2 * ch), lo);
+                        sts16(to + panel_at(k, 2 * ch + 1), hi);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                    if (lt == 0) mbar_arrive(&raw_empty[rs]);
+                } else {
+                    tc_wait(&raw_full[slot], (turns >> slot) & 1, fail);
+                    turns ^= 1u << slot;
+                    for (int x = lt; x < KT * CW; x += 128) {
+                        const int k = x / CW, ch = x - k * CW;
+                        if (sees_all(a, w.req, key0 + k)) continue;
+                        const uint32_t at = to + panel_at(k, ch);
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (any_sees(a, w.req, key0 + k)) {
+                            v = lds16(at);
+                            if (!take_out<T>(v)) continue;
+                            dirty = true;
+                        }
+                        sts16(at, v);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                }
+                if (dirty) atomicOr(&s_flags[u & (kTcUnits - 1)], 2);
+                if (lt == 0) mbar_arrive(&full[slot]);
+            }
+            ++u;
+        }
+    } else if (warp == 12 || warp == 13) {
+        // ------------------------------------------------------------ query rows
+        constexpr int BATCH = 8;
+        const int lt = tid - 12 * 32;
+        int u = 0;
+        Walk w(a, c, s_run);
+        while (w.next(a, c)) {
+            const int all = w.R * CW;
+            // a negative scale turns the rows' signs
+            const uint32_t flip = (a.scale < 0.0f) != (F8 && c.k_scale && c.k_scale[w.h] < 0.0f) ? 0x80008000u : 0u;
+            for (int x0 = 0; x0 < all; x0 += 64 * BATCH) {
+                uint4 v[BATCH];
+#pragma unroll
+                for (int q = 0; q < BATCH; ++q) {
+                    const int x = x0 + q * 64 + lt, r = x / CW, ch = x - r * CW;
+                    v[q] = make_uint4(0u, 0u, 0u, 0u);
+                    if (x < all && ch * 8 < c.head_dim) {
+                        const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
+                        const int hq = w.h * a.group + (w.r0 + r - j * a.group);
+                        v[q] = *(const uint4*)(a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + ch * 16);
+                    }
+                }
+                // the products of the unit before are done with the query rows
+                if (x0 == 0 && u > 0) tc_wait(&q_empty, (u - 1) & 1, fail);
+#pragma unroll
+                for (int q = 0; q < BATCH; ++q) {
+                    const int x = x0 + q * 64 + lt, r = x / CW, ch = x - r * CW;
+                    if (!std::is_same<T, O>::value) {
+                        // bf16 rows under fp16 products: each row is scaled by a
+                        // power of two that brings its largest value into [1, 2),
+                        // exactly but for values 2^-14 below it, which lose bits
+                        // that are 2^-25 of it
+                        const uint32_t e[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+                        float top = 0.0f;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            top = fmaxf(top, fmaxf(fabsf(bf16_lo(e[z])), fabsf(bf16_hi(e[z]))));
+#pragma unroll
+                        for (int o = CW / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
+                        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                        uint32_t f[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) f[z] = tc_pack<__half>(bf16_lo(e[z]) * down, bf16_hi(e[z]) * down);
+                        v[q] = make_uint4(f[0], f[1], f[2], f[3]);
+                        if (x < all && ch == 0) s_row[u & 1][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+                    }
+                    if (x < all)
+                        sts16(sq + panel_at(r, ch),
+                              make_uint4(v[q].x ^ flip, v[q].y ^ flip, v[q].z ^ flip, v[q].w ^ flip));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+            ++u;
+        }
+    } else if (warp == 15) {
         // ------------------------------------------------- matrix instructions
         constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
         constexpr uint32_t head = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kTcRows >> 4) << 24);
@@ -382,6 +572,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) {
             uint32_t item = 0, pn[2] = {0, 0};
             int u = 0;
+            Walk w(a, c, s_run);
             while (w.next(a, c)) {
                 tc_wait(&q_full, u & 1, fail);
                 ++u;
@@ -396,25 +587,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const uint32_t off = (kk >> 2) * Sh::kPanel + (kk & 3) * 32;
                         tc_mma_ss(tmem + (t & 1) * KT, desc_k(sq + off), desc_k(k + off), id_s, kk > 0);
                     }
-                    tc_commit(&empty[slot]);
                     tc_commit(&s_full[t & 1]);
+                    tc_commit(&empty[slot]);
+                    if (t == w.nt - 1) tc_commit(&q_empty);
                     ++item;
                 };
                 scores(0);
                 if (w.nt > 1) scores(1);
                 for (int t = 0; t < w.nt; ++t) {
                     const int s = t & 1;
-                    tc_wait(&p_full[s], pn[s]++ & 1, fail);
                     const int slot = (int)(item % NS);
                     tc_wait(&full[slot], (item / NS) & 1, fail);
+                    tc_wait(&p_full[s], pn[s]++ & 1, fail);
                     tc_fence_after();
                     const uint32_t v = ring + slot * Sh::kTile;
 #pragma unroll
                     for (int kk = 0; kk < KT / 16; ++kk)
                         tc_mma_ts(tmem + 2 * KT + s * D, tmem + s * KT + kk * 8, desc_mn(v + kk * 2048, Sh::kPanel), id_o,
                                   t > 1 || kk > 0);
-                    tc_commit(&empty[slot]);
                     tc_commit(&o_done[s]);
+                    tc_commit(&empty[slot]);
                     ++item;
                     if (t + 2 < w.nt) scores(t + 2);
                 }
@@ -425,65 +617,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 8) {
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();  // every product and every use of TMEM is done
+    if (warp == 15) {
+        tc_fence_after();
+        tc_dealloc(tmem, Sh::kCols);
+    }
+    } else {
+        tc_more_registers<168>();
         // ------------------------------------------------- softmax and output
         const int s = warp >> 2;
         const int row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + s * KT, to = tmem + lanes + 2 * KT;
-        const float scale = fabsf(a.scale);
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        int4 open = make_int4(0, 0, 0, 0);
         uint32_t seen = 0;  // tiles of the stream so far
         int u = 0;
+        Walk w(a, c, s_run);
         while (w.next(a, c)) {
-            // query rows, 16 bytes a step
-            for (int x = tid; x < kTcRows * CW; x += 256) {
-                const int r = x / CW, ch = x - r * CW;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (r < w.R && ch * 8 < c.head_dim) {
-                    const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
-                    const int hq = w.h * a.group + (w.r0 + r - j * a.group);
-                    v = *(const uint4*)(a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + ch * 16);
-                    v.x ^= flip;
-                    v.y ^= flip;
-                    v.z ^= flip;
-                    v.w ^= flip;
-                }
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(sq + panel_at(r, ch)), "r"(v.x), "r"(v.y),
-                             "r"(v.z), "r"(v.w)
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full);
-
             const bool active = (warp & 3) * 32 < w.R;  // the warp has rows
             const int pos = w.req.n + (row < w.R ? (int)a.by_group.div((uint32_t)(w.r0 + row)) : w.req.ell);
+            float scale = fabsf(a.scale) * (F8 && c.k_scale ? fabsf(c.k_scale[w.h]) : 1.0f);
             float m = -INFINITY, l = 0.0f;
             for (int t = s; t < w.nt; t += 2) {
                 tc_wait(&s_full[s], seen & 1, fail);
+                __syncwarp();
                 tc_fence_after();
                 if (active) {
+                    if (!std::is_same<T, O>::value && t == s) scale *= s_row[u & 1][row];
                     const int key0 = tile_key<KT>(w.req, w.t0 + t);
                     const bool cut = !all_see<KT>(a, w.req, key0);
-                    float x[32], top = -INFINITY;
-                    if (!cut) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tc_ld32(x, ts + q * 32);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
-                        }
-                        top *= scale;
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tc_ld32(x, ts + q * 32);
+                    // The loops over 32 columns stay loops: the roles' code together has
+                    // to fit the instruction cache (unrolled, they were 2.5 times slower)
+                    float x[32], top = -INFINITY, top1 = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        tc_ld32(x, ts + q * 32);
+                        const uint32_t see = cut ? seen_bits(a, pos, key0 + q * 32) : 0u;
+                        tc_wait32(x);
+                        if (cut) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (sees(a, pos, key0 + q * 32 + e)) top = fmaxf(top, x[e] * scale);
+                                if (!((see >> e) & 1u)) x[e] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            top = fmaxf(top, x[e]);
+                            top1 = fmaxf(top1, x[e + 1]);
                         }
                     }
+                    top = fmaxf(top, top1);
+                    // nothing seen stays below everything, at a scale of zero too
+                    if (top != -INFINITY) top *= scale;
                     const bool up = top > m + kTcSlack;
                     if (__any_sync(0xffffffffu, up)) {
                         const float now = up ? top : m;
@@ -492,10 +679,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         m = now;
                         if (t >= 2) {
                             tc_wait(&o_done[s], (seen - 1) & 1, fail);
+                            __syncwarp();
                             tc_fence_after();
 #pragma unroll 1
                             for (int q = 0; q < D / 32; ++q) {
                                 tc_ld32(x, to + s * D + q * 32);
+                                tc_wait32(x);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) x[e] *= corr;
                                 tc_st32(to + s * D + q * 32, x);
@@ -507,26 +696,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // each at most, as much as the output's own rounding
                     const float ref = m == -INFINITY ? 0.0f : m;
                     float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         tc_ld32(x, ts + q * 32);
+                        const uint32_t see = cut ? seen_bits(a, pos, key0 + q * 32) : 0u;
+                        tc_wait32(x);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            x[e] = fmaf(x[e], scale, -ref);
-                            if (cut && !sees(a, pos, key0 + q * 32 + e)) x[e] = -INFINITY;
-                            x[e] = ex2_approx(x[e]);
-                            if (e & 1) sum1 += x[e];
-                            else sum0 += x[e];
+                        for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], scale, -ref);
+                        if (cut) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((see >> e) & 1u)) x[e] = -INFINITY;
                         }
                         uint32_t p[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            if (std::is_same<T, __half>::value)
-                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[e]) : "f"(x[2 * e + 1]), "f"(x[2 * e]));
-                            else
-                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[e]) : "f"(x[2 * e + 1]), "f"(x[2 * e]));
+                        for (int e = 0; e < 32; e += 2) {
+                            const float v0 = ex2_approx(x[e]), v1 = ex2_approx(x[e + 1]);
+                            sum0 += v0;
+                            sum1 += v1;
+                            p[e >> 1] = tc_pack<T>(v0, v1);
                         }
-                        tc_st16(ts + q * 16, p);
+                        tc_st16(ts + q * 16, p);  // columns whose scores have been read
                     }
                     l += sum0 + sum1;
                     tc_wait_st();
@@ -541,6 +731,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 s_ml[0][row] = m;
                 s_ml[1][row] = l;
             }
+            __syncwarp();
             tc_fence_before();
             asm volatile("bar.sync 1, 256;" ::: "memory");
             tc_fence_after();
@@ -559,7 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float w0 = ex2_approx(m - ref), w1 = ex2_approx(m1 - ref);
                 float L = l * w0 + s_ml[1][row] * w1;
                 if ((flags & 1) || *fail) L = __int_as_float(0x7fc00000);
-                const float inv = complete ? 1.0f / L : 1.0f;
+                const float inv = (complete ? 1.0f / L : 1.0f) * (F8 && c.v_scale ? c.v_scale[w.h] : 1.0f);
                 s_ml[0][row] = w0 * inv;
                 s_ml[1][row] = w1 * inv;
                 if (row < w.R) {
@@ -571,6 +762,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
             }
+            __syncwarp();
             asm volatile("bar.sync 1, 256;" ::: "memory");
 
             // output: stream s's warps write columns [s D/2, (s+1) D/2)
@@ -579,13 +771,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int q = 0; q < D / 64; ++q) {
                     const int col = s * (D / 2) + q * 32;
-                    float x[32];
+                    float x[32], y[32];
                     tc_ld32(x, to + col);
+                    if (w.nt > 1) tc_ld32(y, to + D + col);
+                    tc_wait32(x);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] *= w0;
                     if (w.nt > 1) {
-                        float y[32];
-                        tc_ld32(y, to + D + col);
+                        tc_wait32(y);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] = fmaf(w1, y[e], x[e]);
                     }
@@ -598,12 +791,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 if (!sees(a, pos, k)) continue;
                                 const long long at = key_at(a, c, pages, k);
                                 if (at < 0) continue;
-                                const T* v = (const T*)(c.v + at + w.h * c.head);
+                                const char* v = c.v + at + w.h * c.head;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
                                     if (col + e < c.head_dim) {
-                                        const float y = to_f32(v[col + e]);
-                                        if (!(fabsf(y) <= 3.4e38f)) x[e] += y;
+                                        const float z = F8 ? to_f32(((const __nv_fp8_e4m3*)v)[col + e])
+                                                           : to_f32(((const T*)v)[col + e]);
+                                        if (!(fabsf(z) <= 3.4e38f)) x[e] += z;
                                     }
                             }
                         }
@@ -613,17 +807,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int e = 0; e < 32; e += 8) {
                             if (col + e >= c.head_dim) break;
                             if (complete) {
-                                uint32_t o[4];
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    const float lo = x[e + 2 * z], hi = x[e + 2 * z + 1];
-                                    if (std::is_same<T, __half>::value)
-                                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[z]) : "f"(hi), "f"(lo));
-                                    else
-                                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[z]) : "f"(hi), "f"(lo));
-                                }
                                 *(uint4*)((char*)a.out + (orow * c.head_dim + col + e) * 2) =
-                                    make_uint4(o[0], o[1], o[2], o[3]);
+                                    make_uint4(tc_pack<O>(x[e], x[e + 1]), tc_pack<O>(x[e + 2], x[e + 3]),
+                                               tc_pack<O>(x[e + 4], x[e + 5]), tc_pack<O>(x[e + 6], x[e + 7]));
                             } else {
                                 float4* p = (float4*)(part + row * c.head_dim + col + e);
                                 p[0] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
@@ -636,21 +822,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (tid == 0 && (flags & 1)) set_status(a.status, SPEC_ERR_PAGE);
             if (w.t0 == 0 && !complete)
                 open = make_int4(1 + (int)((w.req.tiles - w.nt + w.step - 1) / w.step), w.b, w.unit, 0);
+            __syncwarp();
             tc_fence_before();
             asm volatile("bar.sync 1, 256;" ::: "memory");
             if (tid == 0) s_flags[u & (kTcUnits - 1)] = 0;
             ++u;
         }
         if (tid == 0) a.open[blockIdx.x] = open;
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0 && s_fail) set_status(a.status, SPEC_ERR_TIMEOUT);
+        report_requests<O, KT>(a, c, 256);
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 12) {
-        tc_fence_after();
-        tc_dealloc(tmem, Sh::kCols);
-    }
-    if (tid == 0 && s_fail) set_status(a.status, SPEC_ERR_TIMEOUT);
-    report_requests<T, KT>(a, c);
 }
 
 }  // namespace specv
