@@ -318,11 +318,11 @@ __device__ __forceinline__ bool take_out(uint4& v) {
     return any;
 }
 
-// Two e4m3 values to fp16 (exact).
-__device__ __forceinline__ uint32_t tc_widen(uint32_t two) {
-    uint32_t r;
-    asm("{.reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(two));
-    return r;
+// Four e4m3 values to fp16 (exact).
+__device__ __forceinline__ void tc_widen(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 
 // T: type of the products, O: type of q and out, F8: e4m3 cache.
@@ -464,19 +464,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_wait(&raw_full[rs], (item / NR) & 1, fail);
                     if (item >= NS) tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail);
                     const uint32_t from = raws + rs * Sh::kRawTile;
-#pragma unroll 4
-                    for (int x = lt; x < KT * (D / 16); x += 128) {
-                        const int k = x / (D / 16), ch = x - k * (D / 16);
-                        uint4 v = lds16(from + x * 16);
-                        if (cut && !any_sees(a, w.req, key0 + k)) v = make_uint4(0u, 0u, 0u, 0u);
-                        uint4 lo = make_uint4(tc_widen(v.x), tc_widen(v.x >> 16), tc_widen(v.y), tc_widen(v.y >> 16));
-                        uint4 hi = make_uint4(tc_widen(v.z), tc_widen(v.z >> 16), tc_widen(v.w), tc_widen(v.w >> 16));
-                        if (cut && !sees_all(a, w.req, key0 + k)) {
-                            dirty |= take_out<T>(lo);
-                            dirty |= take_out<T>(hi);
+                    constexpr int STEP = 128 / (D / 16), N = KT / STEP;  // rows of a step, steps
+                    const int ch = lt % (D / 16), k0 = lt / (D / 16);
+#pragma unroll 1
+                    for (int i0 = 0; i0 < N; i0 += 4) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = lds16(from + (lt + (i0 + q) * 128) * 16);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t at = to + panel_at(k0 + (i0 + q) * STEP, 2 * ch);
+                            uint4 lo, hi;
+                            tc_widen(v[q].x, lo.x, lo.y);
+                            tc_widen(v[q].y, lo.z, lo.w);
+                            tc_widen(v[q].z, hi.x, hi.y);
+                            tc_widen(v[q].w, hi.z, hi.w);
+                            sts16(at, lo);
+                            sts16(at ^ 16, hi);  // the chunk beside it, in the swizzle too
                         }
-                        sts16(to + panel_at(k, 2 * ch), lo);
-                        sts16(to + panel_at(k, 2 * ch + 1), hi);
+                    }
+                    if (cut) {  // the thread's own chunks again
+#pragma unroll 1
+                        for (int i = 0; i < 2 * N; ++i) {
+                            const int k = k0 + (i >> 1) * STEP;
+                            if (sees_all(a, w.req, key0 + k)) continue;
+                            const uint32_t at = (to + panel_at(k, 2 * ch)) ^ ((i & 1) * 16);
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (any_sees(a, w.req, key0 + k)) {
+                                v = lds16(at);
+                                if (!take_out<T>(v)) continue;
+                                dirty = true;
+                            }
+                            sts16(at, v);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -508,54 +528,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp == 12 || warp == 13) {
         // ------------------------------------------------------------ query rows
-        constexpr int BATCH = 8;
         const int lt = tid - 12 * 32;
         int u = 0;
         Walk w(a, c, s_run);
         while (w.next(a, c)) {
-            const int all = w.R * CW;
             // a negative scale turns the rows' signs
             const uint32_t flip = (a.scale < 0.0f) != (F8 && c.k_scale && c.k_scale[w.h] < 0.0f) ? 0x80008000u : 0u;
-            for (int x0 = 0; x0 < all; x0 += 64 * BATCH) {
-                uint4 v[BATCH];
-#pragma unroll
-                for (int q = 0; q < BATCH; ++q) {
-                    const int x = x0 + q * 64 + lt, r = x / CW, ch = x - r * CW;
-                    v[q] = make_uint4(0u, 0u, 0u, 0u);
-                    if (x < all && ch * 8 < c.head_dim) {
-                        const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
-                        const int hq = w.h * a.group + (w.r0 + r - j * a.group);
-                        v[q] = *(const uint4*)(a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + ch * 16);
-                    }
-                }
-                // the products of the unit before are done with the query rows
-                if (x0 == 0 && u > 0) tc_wait(&q_empty, (u - 1) & 1, fail);
-#pragma unroll
-                for (int q = 0; q < BATCH; ++q) {
-                    const int x = x0 + q * 64 + lt, r = x / CW, ch = x - r * CW;
+            // the products of the unit before are done with the query rows
+            if (u > 0) tc_wait(&q_empty, (u - 1) & 1, fail);
+            constexpr int STEP = 64 / CW;  // rows of a step
+            const int ch = lt % CW;
+            const bool inside = ch * 8 < c.head_dim;
+#pragma unroll 1
+            for (int r = lt / CW; r < w.R; r += STEP) {
+                const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
+                const int hq = w.h * a.group + (w.r0 + r - j * a.group);
+                const char* from = a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + ch * 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(r, ch)),
+                             "l"(inside ? from : a.q), "r"(inside ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (!std::is_same<T, O>::value || flip) {
+                // each thread has its own chunks again, in place
+#pragma unroll 1
+                for (int r = lt / CW; r < (w.R + STEP - 1) / STEP * STEP; r += STEP) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < w.R) v = lds16(sq + panel_at(r, ch));
                     if (!std::is_same<T, O>::value) {
-                        // bf16 rows under fp16 products: each row is scaled by a
-                        // power of two that brings its largest value into [1, 2),
-                        // exactly but for values 2^-14 below it, which lose bits
-                        // that are 2^-25 of it
-                        const uint32_t e[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-                        float top = 0.0f;
-#pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            top = fmaxf(top, fmaxf(fabsf(bf16_lo(e[z])), fabsf(bf16_hi(e[z]))));
+                        // bf16 rows under fp16 products: each row is scaled by a power
+                        // of two that brings its largest value into [1, 2), exactly but
+                        // for values 2^-14 below it, which lose bits that are 2^-25 of it
+                        float top = fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))),
+                                                fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))),
+                                          fmaxf(fmaxf(fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z))),
+                                                fmaxf(fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)))));
 #pragma unroll
                         for (int o = CW / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                         const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
                         const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                        uint32_t f[4];
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) f[z] = tc_pack<__half>(bf16_lo(e[z]) * down, bf16_hi(e[z]) * down);
-                        v[q] = make_uint4(f[0], f[1], f[2], f[3]);
-                        if (x < all && ch == 0) s_row[u & 1][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+                        v.x = tc_pack<__half>(bf16_lo(v.x) * down, bf16_hi(v.x) * down);
+                        v.y = tc_pack<__half>(bf16_lo(v.y) * down, bf16_hi(v.y) * down);
+                        v.z = tc_pack<__half>(bf16_lo(v.z) * down, bf16_hi(v.z) * down);
+                        v.w = tc_pack<__half>(bf16_lo(v.w) * down, bf16_hi(v.w) * down);
+                        if (r < w.R && ch == 0) s_row[u & 1][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
                     }
-                    if (x < all)
-                        sts16(sq + panel_at(r, ch),
-                              make_uint4(v[q].x ^ flip, v[q].y ^ flip, v[q].z ^ flip, v[q].w ^ flip));
+                    if (r < w.R) sts16(sq + panel_at(r, ch), make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
                 }
             }
             fence_proxy_async_smem();
@@ -577,38 +595,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_wait(&q_full, u & 1, fail);
                 ++u;
                 tc_fence_after();
-                auto scores = [&](int t) {
-                    const int slot = (int)(item % NS);
-                    tc_wait(&full[slot], (item / NS) & 1, fail);
-                    tc_fence_after();
-                    const uint32_t k = ring + slot * Sh::kTile;
+                // S of tile i before O of tile i - 2, in the order of the items
+                for (int i = 0; i < w.nt + 2; ++i) {
+                    if (i >= 2) {
+                        const int t = i - 2, s = t & 1, slot = (int)(item % NS);
+                        tc_wait(&full[slot], (item / NS) & 1, fail);
+                        tc_wait(&p_full[s], pn[s]++ & 1, fail);
+                        tc_fence_after();
+                        const uint32_t v = ring + slot * Sh::kTile;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * Sh::kPanel + (kk & 3) * 32;
-                        tc_mma_ss(tmem + (t & 1) * KT, desc_k(sq + off), desc_k(k + off), id_s, kk > 0);
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            tc_mma_ts(tmem + 2 * KT + s * D, tmem + s * KT + kk * 8, desc_mn(v + kk * 2048, Sh::kPanel),
+                                      id_o, t > 1 || kk > 0);
+                        tc_commit(&o_done[s]);
+                        tc_commit(&empty[slot]);
+                        ++item;
                     }
-                    tc_commit(&s_full[t & 1]);
-                    tc_commit(&empty[slot]);
-                    if (t == w.nt - 1) tc_commit(&q_empty);
-                    ++item;
-                };
-                scores(0);
-                if (w.nt > 1) scores(1);
-                for (int t = 0; t < w.nt; ++t) {
-                    const int s = t & 1;
-                    const int slot = (int)(item % NS);
-                    tc_wait(&full[slot], (item / NS) & 1, fail);
-                    tc_wait(&p_full[s], pn[s]++ & 1, fail);
-                    tc_fence_after();
-                    const uint32_t v = ring + slot * Sh::kTile;
+                    if (i < w.nt) {
+                        const int slot = (int)(item % NS);
+                        tc_wait(&full[slot], (item / NS) & 1, fail);
+                        tc_fence_after();
+                        const uint32_t k = ring + slot * Sh::kTile;
 #pragma unroll
-                    for (int kk = 0; kk < KT / 16; ++kk)
-                        tc_mma_ts(tmem + 2 * KT + s * D, tmem + s * KT + kk * 8, desc_mn(v + kk * 2048, Sh::kPanel), id_o,
-                                  t > 1 || kk > 0);
-                    tc_commit(&o_done[s]);
-                    tc_commit(&empty[slot]);
-                    ++item;
-                    if (t + 2 < w.nt) scores(t + 2);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * Sh::kPanel + (kk & 3) * 32;
+                            tc_mma_ss(tmem + (i & 1) * KT, desc_k(sq + off), desc_k(k + off), id_s, kk > 0);
+                        }
+                        tc_commit(&s_full[i & 1]);
+                        tc_commit(&empty[slot]);
+                        if (i == w.nt - 1) tc_commit(&q_empty);
+                        ++item;
+                    }
                 }
             }
             if (*fail) {
