@@ -197,6 +197,7 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
                                         : attend_mma_plan(most, c.head_dim, sms);
     a.tile_rows = p.tile_rows;
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
+    a.lead = tc ? 3 : 2;
     a.least = 2;
     if (dt == SPEC_F32) rc = attend_simt(a, c, p.blocks, st);
     else if (tc) rc = attend_tc(a, c, dt, cache->dt, p.blocks, st);

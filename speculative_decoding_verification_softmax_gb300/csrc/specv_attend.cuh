@@ -22,6 +22,7 @@ struct AttendArgs {
     int q_heads, group, rows, B, gamma, max_pages;
     int window, sinks;
     int tile_rows;  // rows of a unit at most
+    int lead;       // what a unit costs beside its tiles, in tiles
     int least;      // tiles of a block at least
     float scale;    // of the scores, to base 2
     FastDiv by_group;
@@ -33,7 +34,9 @@ struct AttendArgs {
 // adjacent keys: tiles of the sinks, then tiles from the window's first key on.
 // All units' tiles, in order, are dealt to the blocks in equal runs, so that
 // ragged lengths leave no block idle; a run may end inside a unit, whose parts
-// are then joined.
+// are then joined.  A unit counts `lead` tiles more than it has, before its
+// first: its set-up and its end take time, and runs of short requests would
+// otherwise take up to twice as long as others.
 struct Request {
     int code;      // SPEC_OK or why there is no work
     int n, ell;    // cache length, drafts
@@ -89,7 +92,7 @@ __device__ __forceinline__ bool all_see(const AttendArgs& a, const Request& r, i
 
 struct Run {
     int b;           // request of the run's first tile
-    long long at;    // tile within the request (unit-major)
+    long long at;    // tile within the request (unit-major, leads included)
     long long left;  // tiles of the run
     long long step;  // tiles of every block's run
 };
@@ -104,7 +107,7 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         const Request r = request_of<KT>(a, c, b);
-        mine += (long long)r.units * r.tiles;
+        mine += (long long)r.units * (r.tiles + a.lead);
     }
     long long x = mine;
 #pragma unroll
@@ -128,7 +131,7 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
         long long at = start - before;
         for (int b = b0; b < b1; ++b) {
             const Request r = request_of<KT>(a, c, b);
-            const long long w = (long long)r.units * r.tiles;
+            const long long w = (long long)r.units * (r.tiles + a.lead);
             if (at < w) {
                 s_run->b = b;
                 s_run->at = at;
@@ -142,6 +145,57 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
     __syncthreads();
     return *s_run;
 }
+
+// The segments of a run: tiles t0 .. t0 + nt - 1 of a unit, for the rows r0 ..
+// r0 + R - 1 of KV head h.
+template <int KT>
+struct Walk {
+    Request req;
+    int b, unit, t0, nt, h, r0, R;
+    int place;  // in the unit, leads included
+    long long left, step;
+
+    __device__ __forceinline__ Walk(const AttendArgs& a, const CacheView& c, const Run& run) {
+        b = run.b;
+        left = run.left;
+        step = run.step;
+        unit = place = 0;
+        if (left > 0) {
+            req = request_of<KT>(a, c, b);
+            unit = (int)(run.at / (req.tiles + a.lead));
+            place = (int)(run.at - (long long)unit * (req.tiles + a.lead));
+        }
+    }
+    __device__ __forceinline__ bool next(const AttendArgs& a, const CacheView& c) {
+        for (;;) {
+            if (left <= 0) return false;
+            if (place == req.tiles + a.lead) {
+                place = 0;
+                if (++unit == req.units) {
+                    unit = 0;
+                    do req = request_of<KT>(a, c, ++b);
+                    while (req.units == 0);
+                }
+            }
+            const int take = (int)min((long long)(req.tiles + a.lead - place), left);
+            t0 = max(place - a.lead, 0);
+            nt = max(place + take - a.lead, 0) - t0;
+            place += take;
+            left -= take;
+            if (nt > 0) break;
+        }
+        h = unit / req.row_tiles;
+        r0 = (unit - h * req.row_tiles) * a.tile_rows;
+        R = min((req.ell + 1) * a.group - r0, a.tile_rows);
+        return true;
+    }
+    // True if the segment is the whole unit; else its parts are joined, and the
+    // block with tile 0 says how many there are.
+    __device__ __forceinline__ bool whole() const { return nt == req.tiles; }
+    __device__ __forceinline__ int4 open() const {
+        return make_int4(1 + (int)((req.tiles - nt + step - 1) / step), b, unit, 0);
+    }
+};
 
 // Where a block's part of a unit goes: slot 1 if the unit begins in the block,
 // slot 0 if it began in an earlier one.

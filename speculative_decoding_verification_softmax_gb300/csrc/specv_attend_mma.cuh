@@ -146,24 +146,16 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
     const uint32_t sbase = smem_u32(smem);
     const int lch = tid % CH, lrow = tid / CH * RP;  // loads: chunk and first row
 
-    Run run = run_of<KT, THREADS>(a, c, s_scan, &s_run);
+    run_of<KT, THREADS>(a, c, s_scan, &s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
     const bool has_chunk = lch * 16 < dim * (F8 ? 1 : 2);
     const bool by_group = c.page_size % RP == 0;  // a thread's rows share a page
-    Request req;
-    if (run.left > 0) req = request_of<KT>(a, c, run.b);
-    while (run.left > 0) {
-        if (run.at == (long long)req.units * req.tiles) {
-            do req = request_of<KT>(a, c, ++run.b);
-            while (req.units == 0);
-            run.at = 0;
-        }
-        const int unit = (int)(run.at / req.tiles), t0 = (int)(run.at - (long long)unit * req.tiles);
-        const int nt = (int)min((long long)(req.tiles - t0), run.left);
-        const int h = unit / req.row_tiles, r0 = (unit - h * req.row_tiles) * Sh::kRows;
-        const int R = min((req.ell + 1) * a.group - r0, Sh::kRows);
-        const int32_t* pages = a.table + (size_t)run.b * a.max_pages;
+    Walk<KT> w(a, c, s_run);
+    while (w.next(a, c)) {
+        const Request& req = w.req;
+        const int t0 = w.t0, nt = w.nt, h = w.h, r0 = w.r0, R = w.R;
+        const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
         bool bad = false;
 
         // ---- loads of tile t into stage s; `page`: the group's page, fetched a tile ahead
@@ -463,18 +455,18 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 *(float2*)(so + r * (D + 4) + n * 8 + 2 * t4) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
         }
         __syncthreads();
-        const bool whole = nt == req.tiles;
+        const bool whole = w.whole();
         float* out = part_at(a, blockIdx.x, t0 == 0 ? 1 : 0);
         const float vs = F8 && c.v_scale ? c.v_scale[h] : 1.0f;
         for (int r = warp; r < R; r += THREADS / 32) {
-            float M = -INFINITY, L = 0.0f, w[WK];
+            float M = -INFINITY, L = 0.0f, part[WK];
 #pragma unroll
             for (int k = 0; k < WK; ++k) M = fmaxf(M, s_m[k][r]);
             const float base = M == -INFINITY ? 0.0f : M;
 #pragma unroll
             for (int k = 0; k < WK; ++k) {
-                w[k] = WK == 1 ? 1.0f : ex2_approx(s_m[k][r] - base);
-                L += w[k] * s_l[k][r];
+                part[k] = WK == 1 ? 1.0f : ex2_approx(s_m[k][r] - base);
+                L += part[k] * s_l[k][r];
             }
             int j;
             const long long row = out_row(a, req, h, r0 + r, &j);
@@ -484,8 +476,8 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
 #pragma unroll
                 for (int k = 0; k < WK; ++k) {
                     const float2 o = *(const float2*)((float*)smem + ((size_t)k * Sh::kRows + r) * (D + 4) + d);
-                    x += w[k] * o.x;
-                    y += w[k] * o.y;
+                    x += part[k] * o.x;
+                    y += part[k] * o.y;
                 }
                 if (whole) *(uint32_t*)((char*)a.out + (row * dim + d) * 2) = pack2<O>(x * inv, y * inv);
                 else *(float2*)(out + r * dim + d) = make_float2(x * inv, y * inv);
@@ -500,10 +492,7 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
             }
         }
         __syncthreads();  // the stages are free for the next unit
-        if (t0 == 0 && !whole)
-            open = make_int4(1 + (int)((req.tiles - nt + run.step - 1) / run.step), run.b, unit, 0);
-        run.at += nt;
-        run.left -= nt;
+        if (t0 == 0 && !whole) open = w.open();
     }
     if (tid == 0) a.open[blockIdx.x] = open;
     report_requests<O, KT>(a, c, THREADS);

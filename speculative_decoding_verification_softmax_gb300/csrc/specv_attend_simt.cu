@@ -35,22 +35,14 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
     const int col = tid & 63, rg = tid >> 6;     // products: a key or column, and 4 rows
     const int srow = tid >> 4, slane = tid & 15;  // softmax: 16 threads a row
 
-    Run run = run_of<KT, kSimtThreads>(a, c, s_scan, &s_run);
+    run_of<KT, kSimtThreads>(a, c, s_scan, &s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
-    Request req;
-    if (run.left > 0) req = request_of<KT>(a, c, run.b);
-    while (run.left > 0) {
-        if (run.at == (long long)req.units * req.tiles) {
-            do req = request_of<KT>(a, c, ++run.b);
-            while (req.units == 0);
-            run.at = 0;
-        }
-        const int unit = (int)(run.at / req.tiles), t0 = (int)(run.at - (long long)unit * req.tiles);
-        const int nt = (int)min((long long)(req.tiles - t0), run.left);
-        const int h = unit / req.row_tiles, r0 = (unit - h * req.row_tiles) * kSimtRows;
-        const int R = min((req.ell + 1) * a.group - r0, kSimtRows);
-        const int32_t* pages = a.table + (size_t)run.b * a.max_pages;
+    Walk<KT> w(a, c, s_run);
+    while (w.next(a, c)) {
+        const Request& req = w.req;
+        const int t0 = w.t0, nt = w.nt, h = w.h, r0 = w.r0, R = w.R;
+        const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
 
         __syncthreads();
         for (int i = tid; i < kSimtRows * D; i += kSimtThreads) {
@@ -163,7 +155,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
             s_m[srow] = m;
         }
         __syncthreads();
-        const bool whole = nt == req.tiles;
+        const bool whole = w.whole();
         float* part = part_at(a, blockIdx.x, t0 == 0 ? 1 : 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -187,10 +179,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
                 }
             }
         }
-        if (t0 == 0 && !whole)
-            open = make_int4(1 + (int)((req.tiles - nt + run.step - 1) / run.step), run.b, unit, 0);
-        run.at += nt;
-        run.left -= nt;
+        if (t0 == 0 && !whole) open = w.open();
     }
     if (tid == 0) a.open[blockIdx.x] = open;
     report_requests<T, KT>(a, c, kSimtThreads);

@@ -117,6 +117,17 @@ __device__ __forceinline__ void tc_wait32(float (&x)[32]) {
         :
         : "memory");
 }
+// Eight columns from each of two places, and the wait for them.
+__device__ __forceinline__ void tc_ld8(float (&x)[8], float (&y)[8], uint32_t at, uint32_t at2) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(y[0]),
+          "=f"(y[1]), "=f"(y[2]), "=f"(y[3]), "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7])
+        : "r"(at), "r"(at2)
+        : "memory");
+}
 __device__ __forceinline__ void tc_st32(uint32_t at, const float (&x)[32]) {
     const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
     asm volatile(
@@ -213,40 +224,6 @@ __device__ __forceinline__ bool tc_nonfinite(uint32_t w, uint32_t half_mask) {
     return (w & e) == e;
 }
 
-// The segments of a block's run, the same for every role.
-struct Walk {
-    Request req;
-    int b, unit, t0, nt, h, r0, R;
-    long long at, left, step;
-
-    __device__ __forceinline__ Walk(const AttendArgs& a, const CacheView& c, const Run& run) {
-        b = run.b;
-        at = run.at;
-        left = run.left;
-        step = run.step;
-        nt = 0;
-        if (left > 0) req = request_of<kTcKeys>(a, c, b);
-    }
-    __device__ __forceinline__ bool next(const AttendArgs& a, const CacheView& c) {
-        at += nt;
-        left -= nt;
-        if (left <= 0) return false;
-        if (at == (long long)req.units * req.tiles) {
-            do req = request_of<kTcKeys>(a, c, ++b);
-            while (req.units == 0);
-            at = 0;
-        }
-        unit = (int)(at / req.tiles);
-        t0 = (int)(at - (long long)unit * req.tiles);
-        nt = (int)min((long long)(req.tiles - t0), left);
-        h = unit / req.row_tiles;
-        r0 = (unit - h * req.row_tiles) * kTcRows;
-        R = min((req.ell + 1) * a.group - r0, kTcRows);
-        return true;
-    }
-};
-
-
 // Item i of a unit of nt tiles, in the order of use: K0, K1, V0, K2, V1, ...
 __device__ __forceinline__ void item_of(int i, int nt, bool& is_v, int& t) {
     if (i < 2 && nt > 1) {
@@ -325,6 +302,29 @@ __device__ __forceinline__ void tc_widen(uint32_t four, uint32_t& lo, uint32_t& 
         : "r"(four));
 }
 
+// Adds the values that are not finite, of columns col .. col + 7, of the keys
+// that the row at position p sees in the tiles of a segment that a border cuts.
+template <typename T, bool F8, int KT>
+__device__ __noinline__ void add_nonfinite(const AttendArgs& a, const CacheView& c, const Walk<KT>& w, int p, int col,
+                                           float (&x)[8]) {
+    const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
+    for (int t = 0; t < w.nt; ++t) {
+        const int key0 = tile_key<KT>(w.req, w.t0 + t);
+        if (all_see<KT>(a, w.req, key0)) continue;
+        for (int k = key0; k < key0 + KT && k <= p; ++k) {
+            if (!sees(a, p, k)) continue;
+            const long long at = key_at(a, c, pages, k);
+            if (at < 0) continue;
+            const char* v = c.v + at + w.h * c.head;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = F8 ? to_f32(((const __nv_fp8_e4m3*)v)[col + e]) : to_f32(((const T*)v)[col + e]);
+                if (!(fabsf(z) <= 3.4e38f)) x[e] += z;
+            }
+        }
+    }
+}
+
 // T: type of the products, O: type of q and out, F8: e4m3 cache.
 template <typename T, typename O, bool F8, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int boxes = KT / tc.box;
         uint32_t item = 0, issued = 0;
         int u = 0;
-        Walk w(a, c, s_run);
+        Walk<KT> w(a, c, s_run);
         while (w.next(a, c)) {
             const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
             const int end = w.req.n + w.req.ell;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int lt = tid - 8 * 32;
         uint32_t item = 0, turns = 0;  // turns: phases of raw_full by slot (16-bit cache)
         int u = 0;
-        Walk w(a, c, s_run);
+        Walk<KT> w(a, c, s_run);
         while (w.next(a, c)) {
             for (int i = 0; i < 2 * w.nt; ++i, ++item) {
                 bool is_v;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ------------------------------------------------------------ query rows
         const int lt = tid - 12 * 32;
         int u = 0;
-        Walk w(a, c, s_run);
+        Walk<KT> w(a, c, s_run);
         while (w.next(a, c)) {
             // a negative scale turns the rows' signs
             const uint32_t flip = (a.scale < 0.0f) != (F8 && c.k_scale && c.k_scale[w.h] < 0.0f) ? 0x80008000u : 0u;
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) {
             uint32_t item = 0, pn[2] = {0, 0};
             int u = 0;
-            Walk w(a, c, s_run);
+            Walk<KT> w(a, c, s_run);
             while (w.next(a, c)) {
                 tc_wait(&q_full, u & 1, fail);
                 ++u;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int4 open = make_int4(0, 0, 0, 0);
         uint32_t seen = 0;  // tiles of the stream so far
         int u = 0;
-        Walk w(a, c, s_run);
+        Walk<KT> w(a, c, s_run);
         while (w.next(a, c)) {
             const bool active = (warp & 3) * 32 < w.R;  // the warp has rows
             const int pos = w.req.n + (row < w.R ? (int)a.by_group.div((uint32_t)(w.r0 + row)) : w.req.ell);
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // the two streams' weights, for both of them; the parts' maximum and
             // sum, or the reciprocal of the sum in the weights
             const int flags = s_flags[u & (kTcUnits - 1)];
-            const bool complete = w.nt == w.req.tiles;
+            const bool complete = w.whole();
             float* part = part_at(a, blockIdx.x, w.t0 == 0 ? 1 : 0);
             int j = 0;
             long long orow = 0;
@@ -782,63 +782,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             asm volatile("bar.sync 1, 256;" ::: "memory");
 
-            // output: stream s's warps write columns [s D/2, (s+1) D/2)
+            // output: stream s's warps write columns [s D/2, (s+1) D/2), eight at a
+            // time (a short loop: this code is cold when it is reached)
             if (active) {
                 const float w0 = s_ml[0][row], w1 = s_ml[1][row];
 #pragma unroll 1
-                for (int q = 0; q < D / 64; ++q) {
-                    const int col = s * (D / 2) + q * 32;
-                    float x[32], y[32];
-                    tc_ld32(x, to + col);
-                    if (w.nt > 1) tc_ld32(y, to + D + col);
-                    tc_wait32(x);
+                for (int col = s * (D / 2); col < (s + 1) * (D / 2) && col < c.head_dim; col += 8) {
+                    float x[8], y[8];
+                    tc_ld8(x, y, to + col, to + D + col);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] *= w0;
-                    if (w.nt > 1) {
-                        tc_wait32(y);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = fmaf(w1, y[e], x[e]);
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] *= w0;
+                        // without an odd tile its columns hold anything
+                        if (w.nt > 1) x[e] = fmaf(w1, y[e], x[e]);
                     }
-                    if (flags & 2) {  // values that are not finite, by themselves
-                        const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
-                        for (int t = 0; t < w.nt; ++t) {
-                            const int key0 = tile_key<KT>(w.req, w.t0 + t);
-                            if (all_see<KT>(a, w.req, key0)) continue;
-                            for (int k = key0; k < key0 + KT && k <= pos; ++k) {
-                                if (!sees(a, pos, k)) continue;
-                                const long long at = key_at(a, c, pages, k);
-                                if (at < 0) continue;
-                                const char* v = c.v + at + w.h * c.head;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (col + e < c.head_dim) {
-                                        const float z = F8 ? to_f32(((const __nv_fp8_e4m3*)v)[col + e])
-                                                           : to_f32(((const T*)v)[col + e]);
-                                        if (!(fabsf(z) <= 3.4e38f)) x[e] += z;
-                                    }
-                            }
-                        }
-                    }
+                    if (flags & 2) add_nonfinite<T, F8, KT>(a, c, w, pos, col, x);
                     if (row < w.R) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            if (col + e >= c.head_dim) break;
-                            if (complete) {
-                                *(uint4*)((char*)a.out + (orow * c.head_dim + col + e) * 2) =
-                                    make_uint4(tc_pack<O>(x[e], x[e + 1]), tc_pack<O>(x[e + 2], x[e + 3]),
-                                               tc_pack<O>(x[e + 4], x[e + 5]), tc_pack<O>(x[e + 6], x[e + 7]));
-                            } else {
-                                float4* p = (float4*)(part + row * c.head_dim + col + e);
-                                p[0] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                                p[1] = make_float4(x[e + 4], x[e + 5], x[e + 6], x[e + 7]);
-                            }
+                        if (complete) {
+                            *(uint4*)((char*)a.out + (orow * c.head_dim + col) * 2) =
+                                make_uint4(tc_pack<O>(x[0], x[1]), tc_pack<O>(x[2], x[3]), tc_pack<O>(x[4], x[5]),
+                                           tc_pack<O>(x[6], x[7]));
+                        } else {
+                            float4* p = (float4*)(part + row * c.head_dim + col);
+                            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+                            p[1] = make_float4(x[4], x[5], x[6], x[7]);
                         }
                     }
                 }
             }
             if (tid == 0 && (flags & 1)) set_status(a.status, SPEC_ERR_PAGE);
-            if (w.t0 == 0 && !complete)
-                open = make_int4(1 + (int)((w.req.tiles - w.nt + w.step - 1) / w.step), w.b, w.unit, 0);
+            if (w.t0 == 0 && !complete) open = w.open();
             __syncwarp();
             tc_fence_before();
             asm volatile("bar.sync 1, 256;" ::: "memory");
