@@ -302,11 +302,16 @@ __device__ __forceinline__ void tc_widen(uint32_t four, uint32_t& lo, uint32_t& 
         : "r"(four));
 }
 
-// Adds the values that are not finite, of columns col .. col + 7, of the keys
-// that the row at position p sees in the tiles of a segment that a border cuts.
+struct Eight {
+    float x[8];
+};
+
+// The sums of the values that are not finite, of columns col .. col + 7, of the
+// keys that the row at position p sees in the tiles of a segment that a border
+// cuts.
 template <typename T, bool F8, int KT>
-__device__ __noinline__ void add_nonfinite(const AttendArgs& a, const CacheView& c, const Walk<KT>& w, int p, int col,
-                                           float (&x)[8]) {
+__device__ __noinline__ Eight sum_nonfinite(const AttendArgs& a, const CacheView& c, Walk<KT> w, int p, int col) {
+    Eight sum = {};
     const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
     for (int t = 0; t < w.nt; ++t) {
         const int key0 = tile_key<KT>(w.req, w.t0 + t);
@@ -319,16 +324,18 @@ __device__ __noinline__ void add_nonfinite(const AttendArgs& a, const CacheView&
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float z = F8 ? to_f32(((const __nv_fp8_e4m3*)v)[col + e]) : to_f32(((const T*)v)[col + e]);
-                if (!(fabsf(z) <= 3.4e38f)) x[e] += z;
+                if (!(fabsf(z) <= 3.4e38f)) sum.x[e] += z;
             }
         }
     }
+    return sum;
 }
 
 // T: type of the products, O: type of q and out, F8: e4m3 cache.
 template <typename T, typename O, bool F8, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    k_attend_tc(AttendArgs a, CacheView c, TcArgs tc, const __grid_constant__ CUtensorMap mk,
+    k_attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView c, TcArgs tc,
+                const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv) {
     using Sh = TcShape<F8, D>;
     constexpr int KT = kTcKeys, NS = Sh::kSlots, CW = D / 8;  // CW: 16-byte chunks of a row
@@ -382,42 +389,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fewer_registers<88>();
     if (warp == 14) {
         // ------------------------------------------------------- TMA of K and V
-        const int boxes = KT / tc.box;
+        const bool boxed = lane < KT / tc.box;  // the lane has a box of each tile
         uint32_t item = 0, issued = 0;
         int u = 0;
         Walk<KT> w(a, c, s_run);
         while (w.next(a, c)) {
             const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
             const int end = w.req.n + w.req.ell;
-            for (int i = 0; i < 2 * w.nt; ++i, ++item) {
-                bool is_v;
-                int t;
-                item_of(i, w.nt, is_v, t);
+            // the page of the lane's box of tile t; -1 if no row sees any of it
+            auto page_of = [&](int t) {
+                if (!boxed || t >= w.nt) return -1;
+                const int k = tile_key<KT>(w.req, w.t0 + t) + (lane << tc.shift);
+                const int last = min(k + tc.box - 1, end);
+                const bool need = k <= end && (a.window == 0 || w.req.n - last < a.window || k < a.sinks);
+                if (!need) return -1;
+                const int page = pages[c.by_page.div((uint32_t)k)];
+                return page < 0 || page >= c.pages ? -2 : page;
+            };
+            auto put = [&](bool is_v, int t, int page) {
                 const int key0 = tile_key<KT>(w.req, w.t0 + t);
-                const bool whole = all_see<KT>(a, w.req, key0);
-                // the lane's box of the tile, looked up before the slot is free
-                int page = -1, token = 0;
+                if (page == -2) atomicOr(&s_flags[u & (kTcUnits - 1)], 1);
                 const int k = key0 + (lane << tc.shift);
-                bool need = lane < boxes && k <= end;
-                if (need && !whole) {
-                    need = false;
-                    for (int x = 0; x < tc.box; ++x) need |= any_sees(a, w.req, k + x);
-                }
-                if (need) {
-                    const uint32_t place = c.by_page.div((uint32_t)k);
-                    token = k - (int)place * c.page_size;
-                    page = pages[place];
-                    if (page < 0 || page >= c.pages) {
-                        page = -1;
-                        atomicOr(&s_flags[u & (kTcUnits - 1)], 1);
-                    }
-                }
+                const int token = k - (int)c.by_page.div((uint32_t)k) * c.page_size;
                 const int slot = (int)(item % NR);
                 uint64_t* freed = F8 ? &raw_empty[slot] : &empty[slot];
                 const bool ok =
                     __all_sync(0xffffffffu, item < NR || tc_wait(freed, ((item / NR) & 1) ^ 1, fail));
                 // a 16-bit tile is ready when it has landed, unless it is to be repaired
-                uint64_t* bar = F8 || (is_v && !whole) ? &raw_full[slot] : &full[slot];
+                uint64_t* bar =
+                    F8 || (is_v && !all_see<KT>(a, w.req, key0)) ? &raw_full[slot] : &full[slot];
                 const bool have = ok && page >= 0;
                 const int n = __popc(__ballot_sync(0xffffffffu, have));
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * tc.box * (F8 ? D : 2 * D));
@@ -434,7 +434,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
                 if (ok) issued = item + 1;
+                ++item;
                 __syncwarp();
+            };
+            // K of tile i and V of tile i - 2, and the table three tiles ahead: its
+            // round trip would otherwise be the rate of the tiles
+            int p0 = -1, p1 = -1, p2 = page_of(0), p3 = page_of(1), p4 = page_of(2);
+#pragma unroll 1
+            for (int i = 0; i < w.nt + 2; ++i) {
+                const int p5 = page_of(i + 3);
+                if (i >= 2) put(true, i - 2, p0);
+                if (i < w.nt) put(false, i, p2);
+                p0 = p1;
+                p1 = p2;
+                p2 = p3;
+                p3 = p4;
+                p4 = p5;
             }
             ++u;
         }
@@ -796,7 +811,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // without an odd tile its columns hold anything
                         if (w.nt > 1) x[e] = fmaf(w1, y[e], x[e]);
                     }
-                    if (flags & 2) add_nonfinite<T, F8, KT>(a, c, w, pos, col, x);
+                    if (flags & 2) {
+                        const Eight more = sum_nonfinite<T, F8, KT>(a, c, w, pos, col);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] += more.x[e];
+                    }
                     if (row < w.R) {
                         if (complete) {
                             *(uint4*)((char*)a.out + (orow * c.head_dim + col) * 2) =
