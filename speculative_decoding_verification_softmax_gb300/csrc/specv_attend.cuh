@@ -105,6 +105,7 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
     const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = tid * per, b1 = min(a.B, b0 + per);
     long long mine = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const Request r = request_of<KT>(a, c, b);
         mine += (long long)r.units * (r.tiles + a.lead);
@@ -129,6 +130,7 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
     const long long start = (long long)blockIdx.x * step;
     if (start >= before && start < before + mine) {
         long long at = start - before;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const Request r = request_of<KT>(a, c, b);
             const long long w = (long long)r.units * (r.tiles + a.lead);
@@ -173,6 +175,7 @@ struct Walk {
                 place = 0;
                 if (++unit == req.units) {
                     unit = 0;
+#pragma unroll 1
                     do req = request_of<KT>(a, c, ++b);
                     while (req.units == 0);
                 }
@@ -224,6 +227,7 @@ __device__ __forceinline__ long long key_at(const AttendArgs& a, const CacheView
 // first `threads` threads of the block.
 template <typename T, int KT>
 __device__ __forceinline__ void report_requests(const AttendArgs& a, const CacheView& c, int threads) {
+#pragma unroll 1
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const Request r = request_of<KT>(a, c, b);
         if (r.code == SPEC_OK) continue;

@@ -14,7 +14,9 @@
 //                    unit's output
 //   warps 8-11       16-bit cache: repair of V tiles that a border cuts; e4m3
 //                    cache: the widening of all tiles to fp16 (exact)
-//   warps 12-13      the next unit's query rows
+//   warp 12          the next unit's query rows
+//   warp 13          the block's units, told to all others through a ring, so
+//                    that none waits for a request's lengths between two units
 //   warp 14          K and V tiles by TMA, in the order of their use, through a
 //                    ring of shared-memory slots that runs on over the units
 //   warp 15          one thread issues all matrix instructions
@@ -35,7 +37,7 @@ namespace specv {
 constexpr int kTcKeys = 128;
 constexpr int kTcRows = 128;
 constexpr int kTcThreads = 16 * 32;
-constexpr int kTcUnits = 16;  // flags of units under way
+constexpr int kTcUnits = 8;  // ring of units under way
 
 // A running maximum stays the reference until it is passed by this much (to
 // base 2): weights reach 2^8 instead of 1, exactly as well in 16 bits, and the
@@ -73,25 +75,35 @@ __device__ __forceinline__ void tc_dealloc(uint32_t base, int cols) {
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
+// Matrix instructions, called by a whole warp and issued by the one thread with
+// `issue`: the operands stay in the warp's uniform registers.
 // D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(issue)
         : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(issue)
         : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t issue, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 // 32 columns of the warp's 32 lanes; the values are there after tc_wait32.
 __device__ __forceinline__ void tc_ld32(float (&x)[32], uint32_t at) {
@@ -302,6 +314,64 @@ __device__ __forceinline__ void tc_widen(uint32_t four, uint32_t& lo, uint32_t& 
         : "r"(four));
 }
 
+// A unit (a segment of the block's run) as the roles read it; nt = 0 ends the
+// run.
+struct Unit {
+    int n, ell, base, b;
+    int sink_tiles, first_tile, t0, nt;
+    int h, r0, unit;
+    int rows_parts;  // rows R, and the parts if the unit is left open here << 8, -1 if it is whole
+
+    __device__ __forceinline__ int rows() const { return rows_parts & 255; }
+    __device__ __forceinline__ int parts() const { return rows_parts >> 8; }
+
+    __device__ __forceinline__ Request request() const {
+        Request r;
+        r.n = n;
+        r.ell = ell;
+        r.base = base;
+        r.sink_tiles = sink_tiles;
+        r.first_tile = first_tile;
+        return r;
+    }
+};
+
+// A role's view of the ring: next() waits for the next unit, done() gives the
+// last one's place back (each role's warps once).
+struct Units {
+    const Unit* ring;
+    uint64_t* full;
+    uint64_t* empty;
+    volatile int* fail;
+    int u;
+    Request req;
+    int b, t0, nt, h, r0, R;
+
+    __device__ __forceinline__ Units(const Unit* r, uint64_t* f, uint64_t* e, volatile int* x)
+        : ring(r), full(f), empty(e), fail(x), u(-1) {}
+    __device__ __forceinline__ bool next() {
+        ++u;
+        tc_wait(&full[u % kTcUnits], (u / kTcUnits) & 1, fail);
+        __syncwarp();
+        if (*fail) return false;
+        const Unit& s = ring[u % kTcUnits];
+        nt = s.nt;
+        if (nt == 0) return false;
+        req = s.request();
+        b = s.b;
+        t0 = s.t0;
+        h = s.h;
+        r0 = s.r0;
+        R = s.rows();
+        return true;
+    }
+    __device__ __forceinline__ const Unit& now() const { return ring[u % kTcUnits]; }
+    __device__ __forceinline__ void done() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[u % kTcUnits]);
+    }
+};
+
 struct Eight {
     float x[8];
 };
@@ -310,12 +380,13 @@ struct Eight {
 // keys that the row at position p sees in the tiles of a segment that a border
 // cuts.
 template <typename T, bool F8, int KT>
-__device__ __noinline__ Eight sum_nonfinite(const AttendArgs& a, const CacheView& c, Walk<KT> w, int p, int col) {
+__device__ __noinline__ Eight sum_nonfinite(const AttendArgs& a, const CacheView& c, Unit w, int p, int col) {
+    const Request req = w.request();
     Eight sum = {};
     const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
     for (int t = 0; t < w.nt; ++t) {
-        const int key0 = tile_key<KT>(w.req, w.t0 + t);
-        if (all_see<KT>(a, w.req, key0)) continue;
+        const int key0 = tile_key<KT>(req, w.t0 + t);
+        if (all_see<KT>(a, req, key0)) continue;
         for (int k = key0; k < key0 + KT && k <= p; ++k) {
             if (!sees(a, p, k)) continue;
             const long long at = key_at(a, c, pages, k);
@@ -343,6 +414,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     extern __shared__ char smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[NR];
     __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
+    __shared__ __align__(8) uint64_t unit_full[kTcUnits], unit_empty[kTcUnits];
+    __shared__ __align__(16) Unit s_units[kTcUnits];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail, s_flags[kTcUnits];
     __shared__ long long s_scan[kTcThreads / 32 + 1];
@@ -368,13 +441,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(&q_full, 2);
+        mbar_init(&q_full, 1);
+        for (int i = 0; i < kTcUnits; ++i) {
+            mbar_init(&unit_full[i], 1);
+            mbar_init(&unit_empty[i], 15);
+        }
         mbar_init(&q_empty, 1);
         mbar_init(&drain, 1);
         fence_mbar_init();
         s_fail = 0;
     }
-    if (tid < kTcUnits) s_flags[tid] = 0;
     tc_fence_before();
     run_of<KT, kTcThreads>(a, c, s_scan, &s_run);  // also the barrier behind the set-up
     tc_fence_after();
@@ -392,8 +468,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool boxed = lane < KT / tc.box;  // the lane has a box of each tile
         uint32_t item = 0, issued = 0;
         int u = 0;
-        Walk<KT> w(a, c, s_run);
-        while (w.next(a, c)) {
+        Units w(s_units, unit_full, unit_empty, fail);
+        while (w.next()) {
             const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
             const int end = w.req.n + w.req.ell;
             // the page of the lane's box of tile t; -1 if no row sees any of it
@@ -408,7 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             auto put = [&](bool is_v, int t, int page) {
                 const int key0 = tile_key<KT>(w.req, w.t0 + t);
-                if (page == -2) atomicOr(&s_flags[u & (kTcUnits - 1)], 1);
+                if (page == -2) atomicOr(&s_flags[u % kTcUnits], 1);
                 const int k = key0 + (lane << tc.shift);
                 const int token = k - (int)c.by_page.div((uint32_t)k) * c.page_size;
                 const int slot = (int)(item % NR);
@@ -452,6 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 p4 = p5;
             }
             ++u;
+            w.done();
         }
         if (*fail) {  // copies under way land before the block ends: their time is far below the limit
             const unsigned long long t0 = globaltimer_ns();
@@ -462,8 +539,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int lt = tid - 8 * 32;
         uint32_t item = 0, turns = 0;  // turns: phases of raw_full by slot (16-bit cache)
         int u = 0;
-        Walk<KT> w(a, c, s_run);
-        while (w.next(a, c)) {
+        Units w(s_units, unit_full, unit_empty, fail);
+        while (w.next()) {
             for (int i = 0; i < 2 * w.nt; ++i, ++item) {
                 bool is_v;
                 int t;
@@ -536,22 +613,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                     asm volatile("bar.sync 2, 128;" ::: "memory");
                 }
-                if (dirty) atomicOr(&s_flags[u & (kTcUnits - 1)], 2);
+                if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);
+                __syncwarp();
                 if (lt == 0) mbar_arrive(&full[slot]);
             }
             ++u;
+            w.done();
         }
-    } else if (warp == 12 || warp == 13) {
+    } else if (warp == 12) {
         // ------------------------------------------------------------ query rows
-        const int lt = tid - 12 * 32;
+        const int lt = lane;
         int u = 0;
-        Walk<KT> w(a, c, s_run);
-        while (w.next(a, c)) {
+        Units w(s_units, unit_full, unit_empty, fail);
+        while (w.next()) {
             // a negative scale turns the rows' signs
             const uint32_t flip = (a.scale < 0.0f) != (F8 && c.k_scale && c.k_scale[w.h] < 0.0f) ? 0x80008000u : 0u;
             // the products of the unit before are done with the query rows
             if (u > 0) tc_wait(&q_empty, (u - 1) & 1, fail);
-            constexpr int STEP = 64 / CW;  // rows of a step
+            constexpr int STEP = 32 / CW;  // rows of a step
             const int ch = lt % CW;
             const bool inside = ch * 8 < c.head_dim;
 #pragma unroll 1
@@ -595,6 +674,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
             ++u;
+            w.done();
+        }
+    } else if (warp == 13) {
+        // -------------------------------------------------------------- units
+        Walk<KT> w(a, c, s_run);
+        for (int u = 0;; ++u) {
+            const bool more = w.next(a, c);
+            const int at = u % kTcUnits;
+            if (u >= kTcUnits) tc_wait(&unit_empty[at], ((u / kTcUnits) & 1) ^ 1, fail);
+            __syncwarp();
+            if (lane == 0) {
+                Unit s;
+                s.nt = 0;
+                if (more) {
+                    const int4 open = w.open();
+                    s.n = w.req.n;
+                    s.ell = w.req.ell;
+                    s.base = w.req.base;
+                    s.b = w.b;
+                    s.sink_tiles = w.req.sink_tiles;
+                    s.first_tile = w.req.first_tile;
+                    s.t0 = w.t0;
+                    s.nt = w.nt;
+                    s.h = w.h;
+                    s.r0 = w.r0;
+                    s.unit = w.unit;
+                    s.rows_parts = w.R + 256 * (w.whole() ? -1 : w.t0 == 0 ? open.x : 0);
+                }
+                s_units[at] = s;
+                s_flags[at] = 0;
+                mbar_arrive(&unit_full[at]);
+            }
+            __syncwarp();
+            if (!more || *fail) break;
         }
     } else if (warp == 15) {
         // ------------------------------------------------- matrix instructions
@@ -602,53 +715,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         constexpr uint32_t head = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(kTcRows >> 4) << 24);
         constexpr uint32_t id_s = head | ((uint32_t)(KT >> 3) << 17);
         constexpr uint32_t id_o = head | ((uint32_t)(D >> 3) << 17) | (1u << 16);
-        if (lane == 0) {
-            uint32_t item = 0, pn[2] = {0, 0};
-            int u = 0;
-            Walk<KT> w(a, c, s_run);
-            while (w.next(a, c)) {
-                tc_wait(&q_full, u & 1, fail);
-                ++u;
-                tc_fence_after();
-                // S of tile i before O of tile i - 2, in the order of the items
-                for (int i = 0; i < w.nt + 2; ++i) {
-                    if (i >= 2) {
-                        const int t = i - 2, s = t & 1, slot = (int)(item % NS);
-                        tc_wait(&full[slot], (item / NS) & 1, fail);
-                        tc_wait(&p_full[s], pn[s]++ & 1, fail);
-                        tc_fence_after();
-                        const uint32_t v = ring + slot * Sh::kTile;
+        const uint32_t one = elect_one();
+        uint32_t item = 0, pn = 0;
+        Units w(s_units, unit_full, unit_empty, fail);
+        while (w.next()) {
+            tc_wait(&q_full, w.u & 1, fail);
+            __syncwarp();
+            tc_fence_after();
+            // S of tile i before O of tile i - 2, in the order of the items
+#pragma unroll 1
+            for (int i = 0; i < w.nt + 2; ++i) {
+                const uint32_t s = i & 1;
+                if (i >= 2) {
+                    const uint32_t slot = item % NS;
+                    tc_wait(&full[slot], (item / NS) & 1, fail);
+                    tc_wait(&p_full[s], (pn >> s) & 1, fail);
+                    pn ^= 1u << s;
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint64_t v = desc_mn(ring + slot * Sh::kTile, Sh::kPanel);
+                    const uint32_t from = tmem + s * KT, out = tmem + 2 * KT + s * D;
 #pragma unroll
-                        for (int kk = 0; kk < KT / 16; ++kk)
-                            tc_mma_ts(tmem + 2 * KT + s * D, tmem + s * KT + kk * 8, desc_mn(v + kk * 2048, Sh::kPanel),
-                                      id_o, t > 1 || kk > 0);
-                        tc_commit(&o_done[s]);
-                        tc_commit(&empty[slot]);
-                        ++item;
-                    }
-                    if (i < w.nt) {
-                        const int slot = (int)(item % NS);
-                        tc_wait(&full[slot], (item / NS) & 1, fail);
-                        tc_fence_after();
-                        const uint32_t k = ring + slot * Sh::kTile;
+                    for (int kk = 0; kk < KT / 16; ++kk)
+                        tc_mma_ts(one, out, from + kk * 8, v + kk * (2048 >> 4), id_o, i > 3 || kk > 0);
+                    tc_commit(one, &o_done[s]);
+                    tc_commit(one, &empty[slot]);
+                    ++item;
+                }
+                if (i < w.nt) {
+                    const uint32_t slot = item % NS;
+                    tc_wait(&full[slot], (item / NS) & 1, fail);
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint64_t q = desc_k(sq), k = desc_k(ring + slot * Sh::kTile);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * Sh::kPanel + (kk & 3) * 32;
-                            tc_mma_ss(tmem + (i & 1) * KT, desc_k(sq + off), desc_k(k + off), id_s, kk > 0);
-                        }
-                        tc_commit(&s_full[i & 1]);
-                        tc_commit(&empty[slot]);
-                        if (i == w.nt - 1) tc_commit(&q_empty);
-                        ++item;
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * Sh::kPanel + (kk & 3) * 32) >> 4;
+                        tc_mma_ss(one, tmem + s * KT, q + off, k + off, id_s, kk > 0);
                     }
+                    tc_commit(one, &s_full[s]);
+                    tc_commit(one, &empty[slot]);
+                    if (i == w.nt - 1) tc_commit(one, &q_empty);
+                    ++item;
                 }
             }
-            if (*fail) {
-                tc_commit(&drain);
-                mbar_wait_bounded(&drain, 0);
-            }
+            w.done();
         }
-        __syncwarp();
+        if (*fail) {
+            tc_commit(one, &drain);
+            mbar_wait_bounded(&drain, 0);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -667,8 +783,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int4 open = make_int4(0, 0, 0, 0);
         uint32_t seen = 0;  // tiles of the stream so far
         int u = 0;
-        Walk<KT> w(a, c, s_run);
-        while (w.next(a, c)) {
+        Units w(s_units, unit_full, unit_empty, fail);
+        while (w.next()) {
             const bool active = (warp & 3) * 32 < w.R;  // the warp has rows
             const int pos = w.req.n + (row < w.R ? (int)a.by_group.div((uint32_t)(w.r0 + row)) : w.req.ell);
             float scale = fabsf(a.scale) * (F8 && c.k_scale ? fabsf(c.k_scale[w.h]) : 1.0f);
@@ -770,8 +886,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
             // the two streams' weights, for both of them; the parts' maximum and
             // sum, or the reciprocal of the sum in the weights
-            const int flags = s_flags[u & (kTcUnits - 1)];
-            const bool complete = w.whole();
+            const int flags = s_flags[u % kTcUnits];
+            const bool complete = w.now().parts() < 0;
             float* part = part_at(a, blockIdx.x, w.t0 == 0 ? 1 : 0);
             int j = 0;
             long long orow = 0;
@@ -812,7 +928,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (w.nt > 1) x[e] = fmaf(w1, y[e], x[e]);
                     }
                     if (flags & 2) {
-                        const Eight more = sum_nonfinite<T, F8, KT>(a, c, w, pos, col);
+                        const Eight more = sum_nonfinite<T, F8, KT>(a, c, w.now(), pos, col);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] += more.x[e];
                     }
@@ -830,12 +946,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (tid == 0 && (flags & 1)) set_status(a.status, SPEC_ERR_PAGE);
-            if (w.t0 == 0 && !complete) open = w.open();
+            if (w.now().parts() > 0) open = make_int4(w.now().parts(), w.b, w.now().unit, 0);
             __syncwarp();
             tc_fence_before();
             asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (tid == 0) s_flags[u & (kTcUnits - 1)] = 0;
             ++u;
+            w.done();
         }
         if (tid == 0) a.open[blockIdx.x] = open;
         __syncwarp();
