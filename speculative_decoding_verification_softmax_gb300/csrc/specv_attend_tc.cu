@@ -31,6 +31,12 @@ bool make_map(CUtensorMap& map, void* at, const CacheView& c, spec_dtype dt, int
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
                                 (cuuint64_t)c.pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c.token, (cuuint64_t)c.head, (cuuint64_t)c.page};
+    // L2 fetches no more around a row than the row itself: other heads' values
+    // beside it are used by other units, at other times
+    const int row = c.head_dim * dtype_size(dt);
+    const CUtensorMapL2promotion fetch = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                      : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     const cuuint32_t extent[4] = {dt == SPEC_E4M3 && c.head_dim > 64 ? 128u : 64u, (cuuint32_t)box, 1, 1}, step[4] = {1, 1, 1, 1};
     return fn(&map,
               dt == SPEC_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -38,7 +44,7 @@ bool make_map(CUtensorMap& map, void* at, const CacheView& c, spec_dtype dt, int
                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
               4, at, dims, strides, extent, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
               dt == SPEC_E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int box_tokens(int page_size) {

@@ -12,13 +12,15 @@
 // own running maximum and sum; the unit's end joins them.  P overlays S.
 //   warps 0-3, 4-7   softmax of the even and odd tiles, a row a thread; the
 //                    unit's output
-//   warps 8-11       16-bit cache: repair of V tiles that a border cuts; e4m3
-//                    cache: the widening of all tiles to fp16 (exact)
-//   warp 12          the next unit's query rows
+//   warps 8-11       the next unit's query rows; 16-bit cache: repair of V tiles
+//                    that a border cuts; e4m3 cache: the widening of all tiles
+//                    to fp16 (exact)
 //   warp 13          the block's units, told to all others through a ring, so
 //                    that none waits for a request's lengths between two units
-//   warp 14          K and V tiles by TMA, in the order of their use, through a
+//   warps 14, 12     K and V tiles by TMA, in the order of their use, through a
 //                    ring of shared-memory slots that runs on over the units
+//                    (two warps: a box takes 100 cycles to issue, and a tile of
+//                    pages of 16 tokens is 8 boxes or 16)
 //   warp 15          one thread issues all matrix instructions
 // A TMA box is as many tokens as always lie in one page.  In V tiles that some
 // query row must not see whole (the cache's end, the window's edges), rows that
@@ -307,6 +309,28 @@ __device__ __forceinline__ bool take_out(uint4& v) {
     return any;
 }
 
+// The weights of 32 scores: their sums, and rounded to T into 16 columns.
+template <typename T>
+__device__ __forceinline__ void weigh(float (&x)[32], float scale, float ref, uint32_t see, bool cut, float& sum0,
+                                      float& sum1, uint32_t to) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], scale, -ref);
+    if (cut) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1u)) x[e] = -INFINITY;
+    }
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float v0 = ex2_approx(x[e]), v1 = ex2_approx(x[e + 1]);
+        sum0 += v0;
+        sum1 += v1;
+        p[e >> 1] = tc_pack<T>(v0, v1);
+    }
+    tc_st16(to, p);
+}
+
 // Four e4m3 values to fp16 (exact).
 __device__ __forceinline__ void tc_widen(uint32_t four, uint32_t& lo, uint32_t& hi) {
     asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
@@ -441,7 +465,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(&q_full, 1);
+        mbar_init(&q_full, 4);
         for (int i = 0; i < kTcUnits; ++i) {
             mbar_init(&unit_full[i], 1);
             mbar_init(&unit_empty[i], 15);
@@ -463,8 +487,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // the softmax warps still wait for
     if (warp >= 8) {
     tc_fewer_registers<88>();
-    if (warp == 14) {
-        // ------------------------------------------------------- TMA of K and V
+    if (warp == 12 || warp == 14) {
+        // --------------------------------- TMA: K by warp 14, V by warp 12
+        const bool mine_v = warp == 12;
         const bool boxed = lane < KT / tc.box;  // the lane has a box of each tile
         uint32_t item = 0, issued = 0;
         int u = 0;
@@ -510,7 +535,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
                 if (ok) issued = item + 1;
-                ++item;
                 __syncwarp();
             };
             // K of tile i and V of tile i - 2, and the table three tiles ahead: its
@@ -519,8 +543,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < w.nt + 2; ++i) {
                 const int p5 = page_of(i + 3);
-                if (i >= 2) put(true, i - 2, p0);
-                if (i < w.nt) put(false, i, p2);
+                if (i >= 2) {
+                    if (mine_v) put(true, i - 2, p0);
+                    ++item;
+                }
+                if (i < w.nt) {
+                    if (!mine_v) put(false, i, p2);
+                    ++item;
+                }
                 p0 = p1;
                 p1 = p2;
                 p2 = p3;
@@ -536,11 +566,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp >= 8 && warp < 12) {
         // ------------------------------------- repair of V, or widening of K and V
-        const int lt = tid - 8 * 32;
+        // two pairs of warps take the items in turn
+        const int pair = (warp - 8) >> 1, lt = tid & 63;
         uint32_t item = 0, turns = 0;  // turns: phases of raw_full by slot (16-bit cache)
         int u = 0;
         Units w(s_units, unit_full, unit_empty, fail);
         while (w.next()) {
+            // a negative scale turns the rows' signs
+            const uint32_t flip = (a.scale < 0.0f) != (F8 && c.k_scale && c.k_scale[w.h] < 0.0f) ? 0x80008000u : 0u;
+            // the products of the unit before are done with the query rows
+            if (u > 0) tc_wait(&q_empty, (u - 1) & 1, fail);
+            __syncwarp();
+            constexpr int QSTEP = 128 / CW;  // rows of a step
+            const int qt = tid & 127, qch = qt % CW;
+            const bool inside = qch * 8 < c.head_dim;
+#pragma unroll 1
+            for (int r = qt / CW; r < w.R; r += QSTEP) {
+                const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
+                const int hq = w.h * a.group + (w.r0 + r - j * a.group);
+                const char* from = a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + qch * 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(r, qch)),
+                             "l"(inside ? from : a.q), "r"(inside ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (!std::is_same<T, O>::value || flip) {
+                // each thread has its own chunks again, in place
+#pragma unroll 1
+                for (int r = qt / CW; r < (w.R + QSTEP - 1) / QSTEP * QSTEP; r += QSTEP) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < w.R) v = lds16(sq + panel_at(r, qch));
+                    if (!std::is_same<T, O>::value) {
+                        // bf16 rows under fp16 products: each row is scaled by a power
+                        // of two that brings its largest value into [1, 2), exactly but
+                        // for values 2^-14 below it, which lose bits that are 2^-25 of it
+                        float top = fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))),
+                                                fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))),
+                                          fmaxf(fmaxf(fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z))),
+                                                fmaxf(fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)))));
+#pragma unroll
+                        for (int o = CW / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
+                        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                        v.x = tc_pack<__half>(bf16_lo(v.x) * down, bf16_hi(v.x) * down);
+                        v.y = tc_pack<__half>(bf16_lo(v.y) * down, bf16_hi(v.y) * down);
+                        v.z = tc_pack<__half>(bf16_lo(v.z) * down, bf16_hi(v.z) * down);
+                        v.w = tc_pack<__half>(bf16_lo(v.w) * down, bf16_hi(v.w) * down);
+                        if (r < w.R && qch == 0) s_row[u & 1][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+                    }
+                    if (r < w.R) sts16(sq + panel_at(r, qch), make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+
             for (int i = 0; i < 2 * w.nt; ++i, ++item) {
                 bool is_v;
                 int t;
@@ -549,6 +629,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool cut = is_v && !all_see<KT>(a, w.req, key0);
                 if (!F8 && !cut) continue;
                 const int slot = (int)(item % NS);
+                if ((int)(item & 1) != pair) {
+                    turns ^= 1u << slot;
+                    continue;
+                }
                 const uint32_t to = ring + slot * Sh::kTile;
                 bool dirty = false;
                 if (F8) {
@@ -556,13 +640,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_wait(&raw_full[rs], (item / NR) & 1, fail);
                     if (item >= NS) tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail);
                     const uint32_t from = raws + rs * Sh::kRawTile;
-                    constexpr int STEP = 128 / (D / 16), N = KT / STEP;  // rows of a step, steps
+                    constexpr int STEP = 64 / (D / 16), N = KT / STEP;  // rows of a step, steps
                     const int ch = lt % (D / 16), k0 = lt / (D / 16);
 #pragma unroll 1
                     for (int i0 = 0; i0 < N; i0 += 4) {
                         uint4 v[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = lds16(from + (lt + (i0 + q) * 128) * 16);
+                        for (int q = 0; q < 4; ++q) v[q] = lds16(from + (lt + (i0 + q) * 64) * 16);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t at = to + panel_at(k0 + (i0 + q) * STEP, 2 * ch);
@@ -592,12 +676,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
                     if (lt == 0) mbar_arrive(&raw_empty[rs]);
                 } else {
                     tc_wait(&raw_full[slot], (turns >> slot) & 1, fail);
                     turns ^= 1u << slot;
-                    for (int x = lt; x < KT * CW; x += 128) {
+                    for (int x = lt; x < KT * CW; x += 64) {
                         const int k = x / CW, ch = x - k * CW;
                         if (sees_all(a, w.req, key0 + k)) continue;
                         const uint32_t at = to + panel_at(k, ch);
@@ -611,68 +695,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
                 }
                 if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);
                 __syncwarp();
                 if (lt == 0) mbar_arrive(&full[slot]);
             }
-            ++u;
-            w.done();
-        }
-    } else if (warp == 12) {
-        // ------------------------------------------------------------ query rows
-        const int lt = lane;
-        int u = 0;
-        Units w(s_units, unit_full, unit_empty, fail);
-        while (w.next()) {
-            // a negative scale turns the rows' signs
-            const uint32_t flip = (a.scale < 0.0f) != (F8 && c.k_scale && c.k_scale[w.h] < 0.0f) ? 0x80008000u : 0u;
-            // the products of the unit before are done with the query rows
-            if (u > 0) tc_wait(&q_empty, (u - 1) & 1, fail);
-            constexpr int STEP = 32 / CW;  // rows of a step
-            const int ch = lt % CW;
-            const bool inside = ch * 8 < c.head_dim;
-#pragma unroll 1
-            for (int r = lt / CW; r < w.R; r += STEP) {
-                const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
-                const int hq = w.h * a.group + (w.r0 + r - j * a.group);
-                const char* from = a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + ch * 16;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(r, ch)),
-                             "l"(inside ? from : a.q), "r"(inside ? 16 : 0)
-                             : "memory");
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            if (!std::is_same<T, O>::value || flip) {
-                // each thread has its own chunks again, in place
-#pragma unroll 1
-                for (int r = lt / CW; r < (w.R + STEP - 1) / STEP * STEP; r += STEP) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < w.R) v = lds16(sq + panel_at(r, ch));
-                    if (!std::is_same<T, O>::value) {
-                        // bf16 rows under fp16 products: each row is scaled by a power
-                        // of two that brings its largest value into [1, 2), exactly but
-                        // for values 2^-14 below it, which lose bits that are 2^-25 of it
-                        float top = fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))),
-                                                fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))),
-                                          fmaxf(fmaxf(fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z))),
-                                                fmaxf(fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)))));
-#pragma unroll
-                        for (int o = CW / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
-                        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                        v.x = tc_pack<__half>(bf16_lo(v.x) * down, bf16_hi(v.x) * down);
-                        v.y = tc_pack<__half>(bf16_lo(v.y) * down, bf16_hi(v.y) * down);
-                        v.z = tc_pack<__half>(bf16_lo(v.z) * down, bf16_hi(v.z) * down);
-                        v.w = tc_pack<__half>(bf16_lo(v.w) * down, bf16_hi(v.w) * down);
-                        if (r < w.R && ch == 0) s_row[u & 1][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
-                    }
-                    if (r < w.R) sts16(sq + panel_at(r, ch), make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full);
             ++u;
             w.done();
         }
@@ -799,21 +827,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const bool cut = !all_see<KT>(a, w.req, key0);
                     // The loops over 32 columns stay loops: the roles' code together has
                     // to fit the instruction cache (unrolled, they were 2.5 times slower)
-                    float x[32], top = -INFINITY, top1 = -INFINITY;
+                    float x[32], y[32], top = -INFINITY, top1 = -INFINITY;
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 4; q += 2) {
                         tc_ld32(x, ts + q * 32);
-                        const uint32_t see = cut ? seen_bits(a, pos, key0 + q * 32) : 0u;
+                        tc_ld32(y, ts + q * 32 + 32);
                         tc_wait32(x);
+                        tc_wait32(y);
                         if (cut) {
+                            const uint32_t see = seen_bits(a, pos, key0 + q * 32);
+                            const uint32_t see1 = seen_bits(a, pos, key0 + q * 32 + 32);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < 32; ++e) {
                                 if (!((see >> e) & 1u)) x[e] = -INFINITY;
+                                if (!((see1 >> e) & 1u)) y[e] = -INFINITY;
+                            }
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < 32; ++e) {
                             top = fmaxf(top, x[e]);
-                            top1 = fmaxf(top1, x[e + 1]);
+                            top1 = fmaxf(top1, y[e]);
                         }
                     }
                     top = fmaxf(top, top1);
@@ -844,27 +877,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // each at most, as much as the output's own rounding
                     const float ref = m == -INFINITY ? 0.0f : m;
                     float sum0 = 0.0f, sum1 = 0.0f;
+                    tc_ld32(x, ts);
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        tc_ld32(x, ts + q * 32);
-                        const uint32_t see = cut ? seen_bits(a, pos, key0 + q * 32) : 0u;
+                    for (int q = 0; q < 4; q += 2) {
+                        tc_ld32(y, ts + q * 32 + 32);
                         tc_wait32(x);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], scale, -ref);
-                        if (cut) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((see >> e) & 1u)) x[e] = -INFINITY;
-                        }
-                        uint32_t p[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float v0 = ex2_approx(x[e]), v1 = ex2_approx(x[e + 1]);
-                            sum0 += v0;
-                            sum1 += v1;
-                            p[e >> 1] = tc_pack<T>(v0, v1);
-                        }
-                        tc_st16(ts + q * 16, p);  // columns whose scores have been read
+                        const uint32_t see = cut ? seen_bits(a, pos, key0 + q * 32) : 0xffffffffu;
+                        weigh<T>(x, scale, ref, see, cut, sum0, sum1, ts + q * 16);
+                        tc_wait32(y);
+                        if (q == 0) tc_ld32(x, ts + 64);  // columns that the weights do not reach yet
+                        const uint32_t see1 = cut ? seen_bits(a, pos, key0 + q * 32 + 32) : 0xffffffffu;
+                        weigh<T>(y, scale, ref, see1, cut, sum0, sum1, ts + q * 16 + 16);
                     }
                     l += sum0 + sum1;
                     tc_wait_st();
