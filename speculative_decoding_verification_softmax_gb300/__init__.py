@@ -197,9 +197,15 @@ def _check(rc: int, where: str):
 
 
 # ------------------------------------------------------------ torch helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -503,70 +509,103 @@ def kernel_count(B: int, temperature: float) -> int:
 
 
 # ------------------------------------------------------- the key-value cache
-def _row_dtype(name, t) -> int:
+# These calls run many times a token (per layer), and a small batch's kernels
+# take a few microseconds: what they check is checked in one expression per
+# tensor, and the message is looked for only when it fails.
+_codes = {}
+
+
+def _dtype_codes():
     torch = _torch()
-    code = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}.get(t.dtype)
-    if code is None:
+    if not _codes:
+        _codes.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32, torch.float8_e4m3fn: E4M3})
+    return _codes
+
+
+def _row_dtype(name, t) -> int:
+    code = _dtype_codes().get(t.dtype)
+    if code is None or code == E4M3:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     return code
 
 
-def _on_device(name, t):
-    torch = _torch()
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _on_device(name, t, dev):
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
 
 
-def _cache_arg(k_cache, v_cache, k_scale, v_scale, layered=False):
+def _want(name, t, dtype, shape, dev):
+    """_check_tensor of a required tensor, the device already known."""
+    if t is not None and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return
+    _check_tensor(name, t, dtype, shape)
+
+
+def _current_device(t):
+    """The current device; a host tensor is refused later, with its name."""
+    return _torch().cuda.current_device() if t.is_cuda else 0
+
+
+def _raw_stream(stream, dev):
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cache_arg(k_cache, v_cache, k_scale, v_scale, dev, layered=False):
     """spec_cache of [pages, page_size, kv_heads, head_dim] tensors (with
     `layered` also [layers, pages, ...]) of any strides with adjacent values."""
-    torch = _torch()
-    dt = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32,
-          torch.float8_e4m3fn: E4M3}.get(k_cache.dtype)
+    dt = _dtype_codes().get(k_cache.dtype)
     if dt is None:
         raise TypeError(f"k_cache must be bfloat16, float16, float32 or float8_e4m3fn, got {k_cache.dtype}")
-    if v_cache.dtype != k_cache.dtype:
+    if v_cache.dtype is not k_cache.dtype:
         raise TypeError(f"v_cache must be {k_cache.dtype}, got {v_cache.dtype}")
     shape, strides = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 and not (layered and len(shape) == 5):
+    dims = len(shape)
+    if dims != 4 and not (layered and dims == 5):
         raise ValueError(f"k_cache must be {'[layers, ' if layered else '['}pages, page_size, kv_heads, head_dim], "
                          f"got {tuple(shape)}")
     if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("v_cache must have the shape and strides of k_cache")
-    _on_device("k_cache", k_cache)
-    _on_device("v_cache", v_cache)
-    if strides[-1] != 1 and shape[-1] != 1:
-        raise ValueError("the head_dim values of k_cache must be adjacent")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        _on_device("k_cache", k_cache, dev)
+        _on_device("v_cache", v_cache, dev)
     P, page, H, D = shape[-4:]
+    if strides[-1] != 1 and D != 1:
+        raise ValueError("the head_dim values of k_cache must be adjacent")
     # a dimension of one entry has no stride of its own
     unit = 64
-    ls = strides[0] if len(shape) == 5 and shape[0] > 1 else unit
+    ls = strides[0] if dims == 5 and shape[0] > 1 else unit
     ps, ts, hs = strides[-4] if P > 1 else unit, strides[-3] if page > 1 else unit, strides[-2] if H > 1 else unit
-    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if s is not None:
-            if dt != E4M3:
-                raise ValueError(f"{name} belongs to a float8_e4m3fn cache")
-            _check_tensor(name, s, torch.float32, (H,))
-    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), dt, shape[0] if len(shape) == 5 else 1, P, page, H, D, ls,
-                 ps, ts, hs, None if k_scale is None else k_scale.data_ptr(),
-                 None if v_scale is None else v_scale.data_ptr())
+    if k_scale is not None or v_scale is not None:
+        torch = _torch()
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if s is not None:
+                if dt != E4M3:
+                    raise ValueError(f"{name} belongs to a float8_e4m3fn cache")
+                _want(name, s, torch.float32, (H,), dev)
+    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), dt, shape[0] if dims == 5 else 1, P, page, H, D, ls,
+                 ps, ts, hs, _address(k_scale), _address(v_scale))
 
 
-def _row_strides(name, t, dtype, heads, dim, B, gamma, packed):
+def _row_strides(name, t, dtype, heads, dim, B, gamma, packed, dev):
     """(rows, row stride, head stride) of query-like rows: [B, gamma+1, heads,
     dim] (padded) or [rows, heads, dim] (packed)."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _on_device(name, t)
+    if t.get_device() != dev:
+        _on_device(name, t, dev)
     shape, s = t.shape, t.stride()
     if packed:
         if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
             raise ValueError(f"{name} must have shape [rows, {heads}, {dim}] with a row index, got {tuple(shape)}")
         rows, rs = shape[0], s[0]
     else:
-        if tuple(shape) != (B, gamma + 1, heads, dim):
+        if shape != (B, gamma + 1, heads, dim):
             raise ValueError(f"{name} must have shape {(B, gamma + 1, heads, dim)}, got {tuple(shape)}")
         rows, rs = B * (gamma + 1), s[1] if gamma > 0 else s[0]
         if gamma > 0 and B > 1 and s[0] != (gamma + 1) * s[1]:
@@ -576,20 +615,20 @@ def _row_strides(name, t, dtype, heads, dim, B, gamma, packed):
     return rows, rs if rows > 1 else heads * dim, s[-2] if heads > 1 else dim
 
 
-def _tables(page_table, cache_len, verify_len, row, B, slots):
-    torch = _torch()
-    _check_tensor("page_table", page_table, torch.int32, (B, slots))
-    _check_tensor("cache_len", cache_len, torch.int32, (B,))
-    _check_tensor("verify_len", verify_len, torch.int32, (B,), required=False)
-    _check_tensor("row", row, torch.int32, (B,), required=False)
+def _tables(page_table, cache_len, verify_len, row, dev):
+    i32 = _torch().int32
+    B, slots = page_table.shape
+    _want("page_table", page_table, i32, (B, slots), dev)
+    _want("cache_len", cache_len, i32, (B,), dev)
+    if verify_len is not None:
+        _want("verify_len", verify_len, i32, (B,), dev)
+    if row is not None:
+        _want("row", row, i32, (B,), dev)
 
 
-def _workspace(workspace, make):
-    torch = _torch()
-    if workspace is None:
-        return make()
-    _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),))
-    return workspace
+def _workspace_bytes(workspace, dev):
+    _want("workspace", workspace, _torch().uint8, (workspace.numel(),), dev)
+    return workspace.numel()
 
 
 def _gamma_of(q, row, gamma):
@@ -644,22 +683,26 @@ def attend(q, k_cache, v_cache, page_table, cache_len, verify_len=None, row=None
     torch = _torch()
     dt = _row_dtype("q", q)
     gamma = _gamma_of(q, row, gamma)
-    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale)
+    dev = _current_device(q)
+    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale, dev)
     B, slots = page_table.shape
-    heads, dim = q.shape[-2], cache.head_dim
-    rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, row is not None)
-    _tables(page_table, cache_len, verify_len, row, B, slots)
+    heads, dim = q.shape[-2], k_cache.shape[-1]
+    rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, row is not None, dev)
+    _tables(page_table, cache_len, verify_len, row, dev)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
-        _check_tensor("out", out, q.dtype, q.shape)
-    _check_tensor("out_lse", out_lse, torch.float32, q.shape[:-1], required=False)
-    workspace = _workspace(workspace, lambda: alloc_attend_workspace(B, gamma, heads, cache.kv_heads, dim, q.device))
+        _want("out", out, q.dtype, q.shape, dev)
+    if out_lse is not None:
+        _want("out_lse", out_lse, torch.float32, q.shape[:-1], dev)
+    if workspace is None:
+        workspace = alloc_attend_workspace(B, gamma, heads, k_cache.shape[-2], dim, q.device)
     rc = lib().spec_attend(q.data_ptr(), rs, hs, dt, heads, cache, page_table.data_ptr(), slots,
-                           cache_len.data_ptr(), _ptr(verify_len), _ptr(row), rows, B, gamma,
-                           dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr(out_lse),
-                           workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
-    _check(rc, "spec_attend")
+                           cache_len.data_ptr(), _address(verify_len), _address(row), rows, B, gamma,
+                           dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _address(out_lse),
+                           workspace.data_ptr(), _workspace_bytes(workspace, dev), _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_attend")
     return out, workspace
 
 
@@ -722,42 +765,49 @@ def append_kv(q, k, v, k_cache, v_cache, page_table, cache_len, verify_len=None,
     torch = _torch()
     dt = _row_dtype("q", q)
     gamma = _gamma_of(q, row, gamma)
-    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale)
+    dev = _current_device(q)
+    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale, dev)
     B, slots = page_table.shape
-    heads, dim, H = q.shape[-2], cache.head_dim, cache.kv_heads
+    heads, H, dim = q.shape[-2], k_cache.shape[-2], k_cache.shape[-1]
     packed = row is not None
-    rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, packed)
-    krows, krs, khs = _row_strides("k", k, q.dtype, H, dim, B, gamma, packed)
-    vrows, vrs, vhs = _row_strides("v", v, q.dtype, H, dim, B, gamma, packed)
+    rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, packed, dev)
+    krows, krs, khs = _row_strides("k", k, q.dtype, H, dim, B, gamma, packed, dev)
+    vrows, vrs, vhs = _row_strides("v", v, q.dtype, H, dim, B, gamma, packed, dev)
     if krows != rows or vrows != rows:
         raise ValueError(f"q, k and v must have the same rows, got {rows}, {krows} and {vrows}")
-    _tables(page_table, cache_len, verify_len, row, B, slots)
+    _tables(page_table, cache_len, verify_len, row, dev)
     n = 0
     if turns is not None:
         n = turns.numel()
-        _check_tensor("turns", turns, torch.int64, (n,))
+        _want("turns", turns, torch.int64, (n,), dev)
     if out_q is None:
         out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
-        _check_tensor("out_q", out_q, q.dtype, q.shape)
-    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, q.device))
+        _want("out_q", out_q, q.dtype, q.shape, dev)
+    if workspace is None:
+        workspace = alloc_cache_workspace(B, 0, q.device)
     rc = lib().spec_append_kv(q.data_ptr(), rs, hs, k.data_ptr(), v.data_ptr(), krs, khs, vrs, vhs, dt, heads, cache,
-                              page_table.data_ptr(), slots, cache_len.data_ptr(), _ptr(verify_len), _ptr(row), rows,
-                              B, gamma, _ptr(turns), 2 * n, 1 if interleaved else 0, mscale, out_q.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
-    _check(rc, "spec_append_kv")
+                              page_table.data_ptr(), slots, cache_len.data_ptr(), _address(verify_len), _address(row),
+                              rows, B, gamma, _address(turns), 2 * n, 1 if interleaved else 0, mscale,
+                              out_q.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace, dev),
+                              _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_append_kv")
     return out_q, workspace
 
 
 def _page_state(page_table, num_pages, ref_count, cache_len=None):
-    torch = _torch()
+    """(device, B, max_pages, pages) of tensors that belong together."""
+    i32 = _torch().int32
+    dev = _current_device(page_table)
     B, slots = page_table.shape
-    _check_tensor("page_table", page_table, torch.int32, (B, slots))
-    _check_tensor("num_pages", num_pages, torch.int32, (B,))
-    _check_tensor("ref_count", ref_count, torch.int32, (ref_count.numel(),))
+    pages = ref_count.numel()
+    _want("page_table", page_table, i32, (B, slots), dev)
+    _want("num_pages", num_pages, i32, (B,), dev)
+    _want("ref_count", ref_count, i32, (pages,), dev)
     if cache_len is not None:
-        _check_tensor("cache_len", cache_len, torch.int32, (B,))
-    return B, slots, ref_count.numel()
+        _want("cache_len", cache_len, i32, (B,), dev)
+    return dev, B, slots, pages
 
 
 def reserve_pages(page_table, num_pages, ref_count, cache_len, verify_len=None, *, gamma: int, page_size: int,
@@ -765,18 +815,22 @@ def reserve_pages(page_table, num_pages, ref_count, cache_len, verify_len=None, 
     """Run spec_reserve_pages: pages for positions cache_len[b] .. cache_len[b]
     + verify_len[b] of every request.  page_table [B, max_pages], num_pages [B]
     and ref_count [pages] are updated.  Returns (out_status [B], workspace)."""
-    torch = _torch()
-    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
-    _check_tensor("verify_len", verify_len, torch.int32, (B,), required=False)
-    _check_tensor("out_status", out_status, torch.int32, (B,), required=False)
+    i32 = _torch().int32
+    dev, B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    if verify_len is not None:
+        _want("verify_len", verify_len, i32, (B,), dev)
+    if out_status is not None:
+        _want("out_status", out_status, i32, (B,), dev)
     if out_status is None:
-        out_status = torch.empty((B,), dtype=torch.int32, device=page_table.device)
-    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+        out_status = _torch().empty((B,), dtype=i32, device=page_table.device)
+    if workspace is None:
+        workspace = alloc_cache_workspace(B, 0, page_table.device)
     rc = lib().spec_reserve_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
-                                  cache_len.data_ptr(), _ptr(verify_len), B, gamma, slots, page_size,
-                                  out_status.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                  _stream_handle(stream))
-    _check(rc, "spec_reserve_pages")
+                                  cache_len.data_ptr(), _address(verify_len), B, gamma, slots, page_size,
+                                  out_status.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace, dev),
+                                  _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_reserve_pages")
     return out_status, workspace
 
 
@@ -785,33 +839,38 @@ def commit_pages(page_table, num_pages, ref_count, cache_len, accept_len, *, pag
     """Run spec_commit_pages: cache_len + accept_len + 1 into out_cache_len (by
     default cache_len itself), and pages behind it, or left by the window, given
     back.  Returns (out_cache_len, workspace)."""
-    torch = _torch()
-    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
-    _check_tensor("accept_len", accept_len, torch.int32, (B,))
-    _check_tensor("out_cache_len", out_cache_len, torch.int32, (B,), required=False)
+    i32 = _torch().int32
+    dev, B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    _want("accept_len", accept_len, i32, (B,), dev)
+    if out_cache_len is not None:
+        _want("out_cache_len", out_cache_len, i32, (B,), dev)
     if out_cache_len is None:
         out_cache_len = cache_len
-    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+    if workspace is None:
+        workspace = alloc_cache_workspace(B, 0, page_table.device)
     rc = lib().spec_commit_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
                                  cache_len.data_ptr(), accept_len.data_ptr(), B, slots, page_size, window, sinks,
-                                 out_cache_len.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                 _stream_handle(stream))
-    _check(rc, "spec_commit_pages")
+                                 out_cache_len.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace, dev),
+                                 _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_commit_pages")
     return out_cache_len, workspace
 
 
 def free_pages(page_table, num_pages, ref_count, cache_len, requests, *, workspace=None, stream=None):
     """Run spec_free_pages: the requests named in `requests` [n] int32 end and
     give their pages back.  Returns the workspace."""
-    torch = _torch()
-    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    i32 = _torch().int32
+    dev, B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
     n = requests.numel()
-    _check_tensor("requests", requests, torch.int32, (n,))
-    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+    _want("requests", requests, i32, (n,), dev)
+    if workspace is None:
+        workspace = alloc_cache_workspace(B, 0, page_table.device)
     rc = lib().spec_free_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
                                cache_len.data_ptr(), requests.data_ptr(), n, B, slots, workspace.data_ptr(),
-                               workspace.numel(), _stream_handle(stream))
-    _check(rc, "spec_free_pages")
+                               _workspace_bytes(workspace, dev), _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_free_pages")
     return workspace
 
 
@@ -821,23 +880,26 @@ def fork_pages(page_table, num_pages, ref_count, cache_len, src, dst, k_cache, v
     dst [n] int32), sharing full pages and copying the partial last one in every
     layer of k_cache and v_cache ([layers, pages, page_size, kv_heads, head_dim],
     or without layers).  Returns (out_status [n], workspace)."""
-    torch = _torch()
-    B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    i32 = _torch().int32
+    dev, B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
     n = src.numel()
-    _check_tensor("src", src, torch.int32, (n,))
-    _check_tensor("dst", dst, torch.int32, (n,))
-    _check_tensor("out_status", out_status, torch.int32, (n,), required=False)
-    cache = _cache_arg(k_cache, v_cache, None, None, layered=True)
+    _want("src", src, i32, (n,), dev)
+    _want("dst", dst, i32, (n,), dev)
+    if out_status is not None:
+        _want("out_status", out_status, i32, (n,), dev)
+    cache = _cache_arg(k_cache, v_cache, None, None, dev, layered=True)
     if cache.pages != pages:
         raise ValueError(f"the cache has {cache.pages} pages, ref_count {pages}")
     if out_status is None:
-        out_status = torch.empty((n,), dtype=torch.int32, device=page_table.device)
-    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, 0, page_table.device))
+        out_status = _torch().empty((n,), dtype=i32, device=page_table.device)
+    if workspace is None:
+        workspace = alloc_cache_workspace(B, 0, page_table.device)
     rc = lib().spec_fork_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(),
                                cache_len.data_ptr(), src.data_ptr(), dst.data_ptr(), n, B, slots, cache,
-                               out_status.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                               _stream_handle(stream))
-    _check(rc, "spec_fork_pages")
+                               out_status.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace, dev),
+                               _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_fork_pages")
     return out_status, workspace
 
 
@@ -847,21 +909,26 @@ def compact_pages(page_table, num_pages, ref_count, k_cache, v_cache, *, out_pag
     every layer of k_cache and v_cache.  The renamed table and counts go to
     out_page_table and out_ref_count (by default the inputs themselves).
     Returns (out_total [1] = N, workspace)."""
-    torch = _torch()
-    B, slots, pages = _page_state(page_table, num_pages, ref_count)
-    _check_tensor("out_page_table", out_page_table, torch.int32, (B, slots), required=False)
-    _check_tensor("out_ref_count", out_ref_count, torch.int32, (pages,), required=False)
-    _check_tensor("out_total", out_total, torch.int32, (1,), required=False)
-    cache = _cache_arg(k_cache, v_cache, None, None, layered=True)
+    i32 = _torch().int32
+    dev, B, slots, pages = _page_state(page_table, num_pages, ref_count)
+    if out_page_table is not None:
+        _want("out_page_table", out_page_table, i32, (B, slots), dev)
+    if out_ref_count is not None:
+        _want("out_ref_count", out_ref_count, i32, (pages,), dev)
+    if out_total is not None:
+        _want("out_total", out_total, i32, (1,), dev)
+    cache = _cache_arg(k_cache, v_cache, None, None, dev, layered=True)
     if cache.pages != pages:
         raise ValueError(f"the cache has {cache.pages} pages, ref_count {pages}")
     out_page_table = page_table if out_page_table is None else out_page_table
     out_ref_count = ref_count if out_ref_count is None else out_ref_count
     if out_total is None:
-        out_total = torch.empty((1,), dtype=torch.int32, device=page_table.device)
-    workspace = _workspace(workspace, lambda: alloc_cache_workspace(B, pages, page_table.device))
+        out_total = _torch().empty((1,), dtype=i32, device=page_table.device)
+    if workspace is None:
+        workspace = alloc_cache_workspace(B, pages, page_table.device)
     rc = lib().spec_compact_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), B, slots, cache,
                                   out_page_table.data_ptr(), out_ref_count.data_ptr(), out_total.data_ptr(),
-                                  workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
-    _check(rc, "spec_compact_pages")
+                                  workspace.data_ptr(), _workspace_bytes(workspace, dev), _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_compact_pages")
     return out_total, workspace

@@ -2,6 +2,8 @@
 // blocks, and the parts that blocks leave for the joining kernel.
 #pragma once
 
+#include <atomic>
+
 #include "specv_cache.cuh"
 
 namespace specv {
@@ -240,6 +242,18 @@ __device__ __forceinline__ void report_requests(const AttendArgs& a, const Cache
         if (a.lse)
             for (long long i = threadIdx.x; i < n; i += threads) a.lse[first + i] = nan;
     }
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device (a bit
+// each in `done`, which belongs to the kernel).
+inline int allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+    if ((done.load(std::memory_order_relaxed) >> dev) & 1ull) return SPEC_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+    done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return SPEC_OK;
 }
 
 // ------------------------------------------------------------------ kernels

@@ -503,8 +503,8 @@ template <typename T, typename O, bool F8, int D, int WR, int WK>
 int mma_launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
     using Sh = MmaShape<F8, D, WR, WK>;
     auto* f = k_attend_mma<T, O, F8, D, WR, WK>;
-    if (cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
-        return SPEC_ERR_CUDA;
+    static std::atomic<unsigned long long> done{0};
+    if (const int rc = allow_smem((const void*)f, Sh::kSmem, done)) return rc;
     f<<<blocks, Sh::kThreads, Sh::kSmem, st>>>(a, c);
     return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

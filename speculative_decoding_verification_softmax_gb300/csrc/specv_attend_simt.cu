@@ -199,9 +199,8 @@ namespace {
 template <int D>
 int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
     auto* f = k_attend_simt<D>;
-    if (cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)simt_smem<D>()) !=
-        cudaSuccess)
-        return SPEC_ERR_CUDA;
+    static std::atomic<unsigned long long> done{0};
+    if (const int rc = allow_smem((const void*)f, (int)simt_smem<D>(), done)) return rc;
     f<<<blocks, kSimtThreads, simt_smem<D>(), st>>>(a, c);
     return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -58,8 +58,8 @@ int launch_dim(const AttendArgs& a, const CacheView& c, const TcArgs& tc, const 
                const CUtensorMap& mv, int blocks, cudaStream_t st) {
     using Sh = TcShape<F8, D>;
     auto* f = k_attend_tc<T, O, F8, D>;
-    if (cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
-        return SPEC_ERR_CUDA;
+    static std::atomic<unsigned long long> done{0};
+    if (const int rc = allow_smem((const void*)f, Sh::kSmem, done)) return rc;
     f<<<blocks, kTcThreads, Sh::kSmem, st>>>(a, c, tc, mk, mv);
     return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -213,7 +213,7 @@ def test_row_strides():
         # the device check is the only one that needs a GPU
         keep, sv._on_device = sv._on_device, lambda *a: None
         try:
-            return sv._row_strides("q", t, t.dtype, heads, dim, B, gamma, packed)
+            return sv._row_strides("q", t, t.dtype, heads, dim, B, gamma, packed, 0)
         finally:
             sv._on_device = keep
 
