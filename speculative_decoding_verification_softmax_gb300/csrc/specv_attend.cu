@@ -4,8 +4,6 @@
 
 #include <math.h>
 
-#include <mutex>
-
 #include "specv_trace.h"
 
 namespace specv {
@@ -19,6 +17,7 @@ constexpr int kJoinRows = kJoinThreads / 32;
 // One warp a row.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a, CacheView c) {
+    pdl_trigger();
     pdl_wait();
     const int4 open = a.open[blockIdx.x];
     if (open.x == 0) return;
@@ -79,20 +78,6 @@ using namespace specv;
 
 namespace {
 
-std::mutex g_at_mu;
-int g_at_sms[64];
-
-int sm_count(int& sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
-    std::lock_guard<std::mutex> lk(g_at_mu);
-    if (!g_at_sms[dev] &&
-        cudaDeviceGetAttribute(&g_at_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return SPEC_ERR_CUDA;
-    sms = g_at_sms[dev];
-    return SPEC_OK;
-}
-
 bool heads_ok(int q_heads, int kv_heads) {
     return q_heads >= 1 && kv_heads >= 1 && q_heads <= 65535 && q_heads % kv_heads == 0;
 }
@@ -110,16 +95,7 @@ size_t parts_bytes(const AttendPlan& p, int head_dim) {
 template <typename T>
 int launch_join(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
     const int most = min(a.tile_rows, (a.gamma + 1) * a.group);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, (most + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attend_join<T>, a, c) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(k_attend_join<T>, dim3(blocks, (most + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, st, 0, a, c);
 }
 
 }  // namespace

@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
     const uint32_t sbase = smem_u32(smem);
     const int lch = tid % CH, lrow = tid / CH * RP;  // loads: chunk and first row
 
+    pdl_trigger();
+    pdl_wait();
     run_of<KT, THREADS>(a, c, s_scan, &s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
@@ -505,8 +507,7 @@ int mma_launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t
     auto* f = k_attend_mma<T, O, F8, D, WR, WK>;
     static std::atomic<unsigned long long> done{0};
     if (const int rc = allow_smem((const void*)f, Sh::kSmem, done)) return rc;
-    f<<<blocks, Sh::kThreads, Sh::kSmem, st>>>(a, c);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(f, dim3(blocks), Sh::kThreads, Sh::kSmem, st, 0, a, c);
 }
 
 template <typename T, typename O, bool F8, int D>

@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
     const int col = tid & 63, rg = tid >> 6;     // products: a key or column, and 4 rows
     const int srow = tid >> 4, slane = tid & 15;  // softmax: 16 threads a row
 
+    pdl_trigger();
+    pdl_wait();
     run_of<KT, kSimtThreads>(a, c, s_scan, &s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
@@ -201,8 +203,7 @@ int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st)
     auto* f = k_attend_simt<D>;
     static std::atomic<unsigned long long> done{0};
     if (const int rc = allow_smem((const void*)f, (int)simt_smem<D>(), done)) return rc;
-    f<<<blocks, kSimtThreads, simt_smem<D>(), st>>>(a, c);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(f, dim3(blocks), kSimtThreads, simt_smem<D>(), st, 0, a, c);
 }
 
 }  // namespace

@@ -60,8 +60,7 @@ int launch_dim(const AttendArgs& a, const CacheView& c, const TcArgs& tc, const 
     auto* f = k_attend_tc<T, O, F8, D>;
     static std::atomic<unsigned long long> done{0};
     if (const int rc = allow_smem((const void*)f, Sh::kSmem, done)) return rc;
-    f<<<blocks, kTcThreads, Sh::kSmem, st>>>(a, c, tc, mk, mv);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(f, dim3(blocks), kTcThreads, Sh::kSmem, st, 0, a, c, tc, mk, mv);
 }
 
 template <typename T, typename O, bool F8>

@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     const uint32_t sq = base, ring = base + Sh::kQ, raws = ring + NS * Sh::kTile;
 
+    pdl_trigger();
     if (warp == 15) tc_alloc(&s_tmem, Sh::kCols);
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -476,6 +477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         s_fail = 0;
     }
     tc_fence_before();
+    pdl_wait();
     run_of<KT, kTcThreads>(a, c, s_scan, &s_run);  // also the barrier behind the set-up
     tc_fence_after();
     const uint32_t tmem = s_tmem;

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "specv_common.cuh"
 
 namespace specv {
@@ -69,6 +71,43 @@ inline int cache_view(const spec_cache* c, CacheView& o) {
     o.k_scale = c->dt == SPEC_E4M3 ? c->k_scale : nullptr;
     o.v_scale = c->dt == SPEC_E4M3 ? c->v_scale : nullptr;
     return SPEC_OK;
+}
+
+// SMs of the current device.
+inline int sm_count(int& sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+    sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SPEC_ERR_CUDA;
+        known[dev].store(sms, std::memory_order_relaxed);
+    }
+    return SPEC_OK;
+}
+
+// Launches a programmatic dependent of the kernel before it in the stream: its
+// blocks may be placed while that one drains.  Every kernel launched so waits
+// (pdl_wait) before it touches memory, and lets the next one be placed at once
+// (pdl_trigger).  `cluster` > 0: one cluster of so many blocks.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster,
+                     A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 // ------------------------------------------------------------- element types

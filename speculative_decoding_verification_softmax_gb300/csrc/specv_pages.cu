@@ -199,6 +199,8 @@ struct ReserveArgs {
 // it to the request whose range of needs holds r (a binary search in shared
 // memory).  Latency bound: 1024 requests over a pool of 250,000 pages read 1 MB.
 __global__ void __launch_bounds__(kPgThreads) k_reserve_pages(ReserveArgs a) {
+    pdl_trigger();
+    pdl_wait();
     __shared__ int s_pref[SPEC_MAX_BATCH + 1];
     __shared__ int s_num[SPEC_MAX_BATCH];
     __shared__ int s_warp[kPgWarps + 1], s_cta[2 * kPgCluster];
@@ -279,6 +281,8 @@ struct CommitArgs {
 
 // Commit: one warp a request, a lane per slot given back.
 __global__ void __launch_bounds__(256) k_commit_pages(CommitArgs a) {
+    pdl_trigger();
+    pdl_wait();
     const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (b >= a.B) return;
     const int n = a.len[b], acc = a.accept[b], held = a.num[b];
@@ -330,6 +334,8 @@ struct FreeArgs {
 // Free: one warp an entry of the list.  Each slot is exchanged for -1, so that
 // of two warps with the same request one gets its page.
 __global__ void __launch_bounds__(256) k_free_pages(FreeArgs a) {
+    pdl_trigger();
+    pdl_wait();
     const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (i >= a.n) return;
     const int b = a.requests[i];
@@ -368,6 +374,8 @@ constexpr int kForkSrc = 1 << 30;  // flag beside a request's count as a dst
 // written.  A valid fork's dst is no other fork's dst or src, so nothing that
 // is written is read by another fork.
 __global__ void __launch_bounds__(kPgThreads) k_fork_tables(ForkArgs a) {
+    pdl_trigger();
+    pdl_wait();
     __shared__ int s_pref[SPEC_MAX_BATCH + 1];
     __shared__ int s_use[SPEC_MAX_BATCH];
     __shared__ int s_warp[kPgWarps + 1], s_cta[2 * kPgCluster];
@@ -525,6 +533,8 @@ __device__ __forceinline__ void copy_vecs(const CacheView& c, const PageShape& g
 
 // Fork, the data: block (i, layer and K or V, 32 KB slice).
 __global__ void __launch_bounds__(kCopyThreads) k_fork_copy(CacheView c, PageShape g, const int32_t* list, int n) {
+    pdl_trigger();
+    pdl_wait();
     const int i = blockIdx.x;
     const int tokens = list[2 * n + i];
     const uint32_t vecs = (uint32_t)tokens * g.per_token, i0 = blockIdx.z * kCopyVecs;
@@ -555,6 +565,8 @@ struct CompactArgs {
 // hole k gets number N-h+k: one scan finds N, a second both lists, and h is
 // their length.
 __global__ void __launch_bounds__(kPgThreads) k_compact_plan(CompactArgs a) {
+    pdl_trigger();
+    pdl_wait();
     __shared__ int s_warp[kPgWarps + 1], s_cta[2 * kPgCluster], s_holes[kPgCluster];
     __shared__ int s_mine;
     cg::cluster_group cluster = cg::this_cluster();
@@ -617,6 +629,8 @@ __global__ void __launch_bounds__(kPgThreads) k_compact_plan(CompactArgs a) {
 
 // Compact, the data: first the moved pages in 32 KB items, then the tables.
 __global__ void __launch_bounds__(kCopyThreads) k_compact_move(CompactArgs a, CacheView c, PageShape g) {
+    pdl_trigger();
+    pdl_wait();
     const int h = a.status[kPgMoved], N = *a.out_total;
     const uint32_t vecs = (uint32_t)c.page_size * g.per_token;
     const int slices = (int)((vecs + kCopyVecs - 1) / kCopyVecs);
@@ -690,20 +704,13 @@ int pages_info(PagesInfo& out) {
     return SPEC_OK;
 }
 
+// One block per 16384 pages, in a cluster of a power of two: a small pool is
+// scanned by one block, without the launch and the barriers of sixteen.
 template <typename A>
-int launch_cluster(void (*kernel)(A), const A& a, int blocks, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kPgThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)blocks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+int launch_cluster(void (*kernel)(A), const A& a, int most, cudaStream_t st) {
+    int blocks = 1;
+    while (blocks < most && (long long)blocks * kPgWarps * kPgWords * 32 < a.pages) blocks *= 2;
+    return launch_dependent(kernel, dim3(blocks), kPgThreads, 0, st, blocks, a);
 }
 
 int check_tables(const int32_t* table, const int32_t* num, const int32_t* ref, int pages, int B, int max_pages,
@@ -781,8 +788,7 @@ int spec_commit_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_coun
     if (((uintptr_t)cache_len | (uintptr_t)accept_len | (uintptr_t)out_cache_len) & 3) return SPEC_ERR_ALIGN;
     const CommitArgs a{page_table, num_pages, ref_count, cache_len, accept_len, out_cache_len,
                        (int*)workspace, pages, B, max_pages, page_size, window, sinks};
-    k_commit_pages<<<(B + 7) / 8, 256, 0, (cudaStream_t)stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(k_commit_pages, dim3((B + 7) / 8), 256, 0, (cudaStream_t)stream, 0, a);
 }
 
 int spec_free_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages, int32_t* cache_len,
@@ -796,8 +802,7 @@ int spec_free_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count,
     if (rc != SPEC_OK) return rc;
     if (((uintptr_t)cache_len | (uintptr_t)requests) & 3) return SPEC_ERR_ALIGN;
     const FreeArgs a{page_table, num_pages, ref_count, cache_len, requests, (int*)workspace, pages, n, B, max_pages};
-    k_free_pages<<<(n + 7) / 8, 256, 0, (cudaStream_t)stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(k_free_pages, dim3((n + 7) / 8), 256, 0, (cudaStream_t)stream, 0, a);
 }
 
 int spec_fork_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int32_t* cache_len,
@@ -824,8 +829,8 @@ int spec_fork_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count,
     const ForkArgs a{page_table, num_pages, ref_count, cache_len, src, dst, out_status, (int*)workspace, list,
                      c.pages, n, B, max_pages, c.page_size};
     if ((rc = launch_cluster(k_fork_tables, a, d.cluster, (cudaStream_t)stream)) != SPEC_OK) return rc;
-    k_fork_copy<<<dim3(n, c.layers * 2, (unsigned)slices), kCopyThreads, 0, (cudaStream_t)stream>>>(c, g, list, n);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(k_fork_copy, dim3(n, c.layers * 2, (unsigned)slices), kCopyThreads, 0,
+                            (cudaStream_t)stream, 0, c, g, list, n);
 }
 
 int spec_compact_pages(const int32_t* page_table, const int32_t* num_pages, const int32_t* ref_count, int B,
@@ -850,8 +855,8 @@ int spec_compact_pages(const int32_t* page_table, const int32_t* num_pages, cons
     const CompactArgs a{page_table, num_pages, ref_count, out_page_table, out_ref_count, out_total, (int*)workspace,
                         lists, lists + P, lists + 2 * P, lists + 3 * P, c.pages, B, max_pages};
     if ((rc = launch_cluster(k_compact_plan, a, d.cluster, (cudaStream_t)stream)) != SPEC_OK) return rc;
-    k_compact_move<<<d.sms * 4, kCopyThreads, 0, (cudaStream_t)stream>>>(a, c, page_shape(cache));
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_dependent(k_compact_move, dim3(d.sms * 4), kCopyThreads, 0, (cudaStream_t)stream, 0, a, c,
+                            page_shape(cache));
 }
 
 }  // extern "C"
