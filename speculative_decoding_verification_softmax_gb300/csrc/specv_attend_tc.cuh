@@ -309,12 +309,25 @@ __device__ __forceinline__ bool take_out(uint4& v) {
     return any;
 }
 
+// Two fp32 operations of one instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float b, float c) {
+    asm("{.reg .b64 v, w, z; mov.b64 v, {%0, %1}; mov.b64 w, {%2, %2}; mov.b64 z, {%3, %3}; fma.rn.f32x2 v, v, w, z; "
+        "mov.b64 {%0, %1}, v;}"
+        : "+f"(x), "+f"(y)
+        : "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+    asm("{.reg .b64 v, w; mov.b64 v, {%0, %1}; mov.b64 w, {%2, %3}; add.rn.f32x2 v, v, w; mov.b64 {%0, %1}, v;}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
 // The weights of 32 scores: their sums, and rounded to T into 16 columns.
 template <typename T>
 __device__ __forceinline__ void weigh(float (&x)[32], float scale, float ref, uint32_t see, bool cut, float& sum0,
                                       float& sum1, uint32_t to) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e], scale, -ref);
+    for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], scale, -ref);
     if (cut) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
@@ -324,8 +337,7 @@ __device__ __forceinline__ void weigh(float (&x)[32], float scale, float ref, ui
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         const float v0 = ex2_approx(x[e]), v1 = ex2_approx(x[e + 1]);
-        sum0 += v0;
-        sum1 += v1;
+        add2(sum0, sum1, v0, v1);
         p[e >> 1] = tc_pack<T>(v0, v1);
     }
     tc_st16(to, p);
