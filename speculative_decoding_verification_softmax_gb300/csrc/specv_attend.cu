@@ -14,60 +14,89 @@ constexpr int kJoinRows = kJoinThreads / 32;
 // Joins the parts of the unit that block blockIdx.x left open: the block's own
 // and those of the blocks after it, in order.  With each part's maximum m_i
 // and sum l_i, M = max m_i: out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// One warp a row.
+// One warp a row; bound by its round trips, of which there are two: what is
+// open, and then the first parts' outputs together with all maxima and sums.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a, CacheView c) {
+    constexpr int NE = SPEC_MAX_HEAD_DIM / 64, FIRST = 4;  // column pairs of a lane; parts fetched ahead
     pdl_trigger();
     pdl_wait();
     const int4 open = a.open[blockIdx.x];
-    if (open.x == 0) return;
-    const Request req = request_of<64>(a, c, open.y);  // rows do not depend on the tile size
-    const int h = open.z / req.row_tiles, r0 = (open.z - h * req.row_tiles) * a.tile_rows;
-    const int R = min((req.ell + 1) * a.group - r0, a.tile_rows);
-    const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= R) return;
+    const int n = open.x, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (n == 0 || r >= (int)((uint32_t)open.w >> 16)) return;
     const int dim = c.head_dim;
     const float* first = part_at(a, blockIdx.x, 1);
     const float* rest = part_at(a, blockIdx.x + 1, 0);
     const long long hop = 2 * a.part_floats;
-    const int n = open.x;
-    // maxima and sums, a part a lane
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) {
-        const float* p = i == 0 ? first : rest + (i - 1) * hop;
-        M = fmaxf(M, p[a.tile_rows * dim + r]);
-    }
+    auto part = [&](int i) { return i == 0 ? first : rest + (i - 1) * hop; };
+    float2 o[FIRST][NE];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int i = 0; i < FIRST; ++i)
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            if (i < n && 2 * lane + 64 * e < dim) o[i][e] = *(const float2*)(part(i) + r * dim + 2 * lane + 64 * e);
+    // maxima and sums, a part a lane
+    float m0 = -INFINITY, l0 = 0.0f, M = -INFINITY;
+    if (lane < n) {
+        m0 = part(lane)[a.tile_rows * dim + r];
+        l0 = part(lane)[a.tile_rows * (dim + 1) + r];
+        M = m0;
+    }
+    for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, part(i)[a.tile_rows * dim + r]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     const float base = M == -INFINITY ? 0.0f : M;
     float L = 0.0f;
-    float acc[SPEC_MAX_HEAD_DIM / 32];
+    float2 acc[NE];
 #pragma unroll
-    for (int e = 0; e < SPEC_MAX_HEAD_DIM / 32; ++e) acc[e] = 0.0f;
+    for (int e = 0; e < NE; ++e) acc[e] = make_float2(0.0f, 0.0f);
     for (int i0 = 0; i0 < n; i0 += 32) {
         float w = 0.0f, l = 0.0f;
         if (i0 + lane < n) {
-            const float* p = i0 + lane == 0 ? first : rest + (i0 + lane - 1) * hop;
-            w = exp2f(p[a.tile_rows * dim + r] - base);
-            l = p[a.tile_rows * (dim + 1) + r] * w;
+            w = exp2f((i0 == 0 ? m0 : part(i0 + lane)[a.tile_rows * dim + r]) - base);
+            l = (i0 == 0 ? l0 : part(i0 + lane)[a.tile_rows * (dim + 1) + r]) * w;
         }
         L += warp_sum(l);
         const int m = min(32, n - i0);
+        int i = 0;
+        if (i0 == 0) {
+#pragma unroll
+            for (int f = 0; f < FIRST; ++f) {
+                const float wf = __shfl_sync(0xffffffffu, w, f);
+                if (f < n) {
+#pragma unroll
+                    for (int e = 0; e < NE; ++e)
+                        if (2 * lane + 64 * e < dim) {
+                            acc[e].x = fmaf(wf, o[f][e].x, acc[e].x);
+                            acc[e].y = fmaf(wf, o[f][e].y, acc[e].y);
+                        }
+                }
+            }
+            i = min(FIRST, m);
+        }
 #pragma unroll 4
-        for (int i = 0; i < m; ++i) {
-            const float* p = (i0 + i == 0 ? first : rest + (i0 + i - 1) * hop) + r * dim;
+        for (; i < m; ++i) {
+            const float* p = part(i0 + i) + r * dim;
             const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
-            for (int e = 0; e < SPEC_MAX_HEAD_DIM / 32; ++e)
-                if (lane + 32 * e < dim) acc[e] = fmaf(wi, p[lane + 32 * e], acc[e]);
+            for (int e = 0; e < NE; ++e)
+                if (2 * lane + 64 * e < dim) {
+                    const float2 x = *(const float2*)(p + 2 * lane + 64 * e);
+                    acc[e].x = fmaf(wi, x.x, acc[e].x);
+                    acc[e].y = fmaf(wi, x.y, acc[e].y);
+                }
         }
     }
-    int j;
-    const long long row = out_row(a, req, h, r0 + r, &j);
+    const long long row = out_row(a, open.y, open.w & 0xffff, open.z + r);
     const float inv = 1.0f / L;
 #pragma unroll
-    for (int e = 0; e < SPEC_MAX_HEAD_DIM / 32; ++e)
-        if (lane + 32 * e < dim) ((T*)a.out)[row * dim + lane + 32 * e] = from_f32<T>(acc[e] * inv);
+    for (int e = 0; e < NE; ++e)
+        if (2 * lane + 64 * e < dim) {
+            Vec<T, 2> two;
+            two.x[0] = from_f32<T>(acc[e].x * inv);
+            two.x[1] = from_f32<T>(acc[e].y * inv);
+            *(Vec<T, 2>*)((T*)a.out + row * dim + 2 * lane + 64 * e) = two;
+        }
     if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
 }
 

@@ -18,7 +18,8 @@ struct AttendArgs {
     const int32_t* ell;
     const int32_t* row;
     int* status;
-    int4* open;    // [blocks]: parts, request, unit of the unit that a block left open
+    int4* open;    // [blocks]: of the unit that a block left open its parts (0: none), first
+                   // row of q, first row of the unit, rows << 16 | KV head
     float* parts;  // [blocks][2][tile rows * (D + 2)]
     long long part_floats;
     int q_heads, group, rows, B, gamma, max_pages;
@@ -150,6 +151,10 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
     return *s_run;
 }
 
+__device__ __forceinline__ int4 open_of(int parts, int base, int r0, int R, int h) {
+    return make_int4(parts, base, r0, (int)((uint32_t)R << 16 | (uint32_t)h));
+}
+
 // The segments of a run: tiles t0 .. t0 + nt - 1 of a unit, for the rows r0 ..
 // r0 + R - 1 of KV head h.
 template <int KT>
@@ -198,7 +203,7 @@ struct Walk {
     // block with tile 0 says how many there are.
     __device__ __forceinline__ bool whole() const { return nt == req.tiles; }
     __device__ __forceinline__ int4 open() const {
-        return make_int4(1 + (int)((req.tiles - nt + step - 1) / step), b, unit, 0);
+        return open_of(1 + (int)((req.tiles - nt + step - 1) / step), req.base, r0, R, h);
     }
 };
 
@@ -208,11 +213,11 @@ __device__ __forceinline__ float* part_at(const AttendArgs& a, int block, int sl
     return a.parts + ((long long)block * 2 + slot) * a.part_floats;
 }
 
-// The element offset of unit row r (KV head h) in out, and its lse index.
-__device__ __forceinline__ long long out_row(const AttendArgs& a, const Request& q, int h, int r, int* token) {
+// The row of out (and the index of lse) of row r of KV head h of a request whose
+// first row is `base`.
+__device__ __forceinline__ long long out_row(const AttendArgs& a, int base, int h, int r) {
     const int j = (int)a.by_group.div((uint32_t)r);
-    *token = j;
-    return (long long)(q.base + j) * a.q_heads + h * a.group + (r - j * a.group);
+    return (long long)(base + j) * a.q_heads + h * a.group + (r - j * a.group);
 }
 
 // Byte offset of a key's first value (head 0) in the pages, or -1 if its entry

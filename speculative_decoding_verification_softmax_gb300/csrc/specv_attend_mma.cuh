@@ -470,8 +470,7 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 part[k] = WK == 1 ? 1.0f : ex2_approx(s_m[k][r] - base);
                 L += part[k] * s_l[k][r];
             }
-            int j;
-            const long long row = out_row(a, req, h, r0 + r, &j);
+            const long long row = out_row(a, req.base, h, r0 + r);
             const float inv = whole ? vs / L : vs;
             for (int d = 2 * lane; d < dim; d += 64) {
                 float x = 0.0f, y = 0.0f;

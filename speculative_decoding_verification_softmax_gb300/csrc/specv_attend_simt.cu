@@ -164,8 +164,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
             const int r = rg * 4 + i;
             if (r >= R) break;
             if (whole) {
-                int j;
-                const long long row = out_row(a, req, h, r0 + r, &j);
+                const long long row = out_row(a, req.base, h, r0 + r);
                 const float inv = 1.0f / s_l[r];
 #pragma unroll
                 for (int n = 0; n < CN; ++n)

@@ -355,7 +355,7 @@ __device__ __forceinline__ void tc_widen(uint32_t four, uint32_t& lo, uint32_t& 
 struct Unit {
     int n, ell, base, b;
     int sink_tiles, first_tile, t0, nt;
-    int h, r0, unit;
+    int h, r0, unused;
     int rows_parts;  // rows R, and the parts if the unit is left open here << 8, -1 if it is whole
 
     __device__ __forceinline__ int rows() const { return rows_parts & 255; }
@@ -730,7 +730,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 Unit s;
                 s.nt = 0;
                 if (more) {
-                    const int4 open = w.open();
                     s.n = w.req.n;
                     s.ell = w.req.ell;
                     s.base = w.req.base;
@@ -741,8 +740,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     s.nt = w.nt;
                     s.h = w.h;
                     s.r0 = w.r0;
-                    s.unit = w.unit;
-                    s.rows_parts = w.R + 256 * (w.whole() ? -1 : w.t0 == 0 ? open.x : 0);
+                    s.rows_parts = w.R + 256 * (w.whole() ? -1 : w.t0 == 0 ? w.open().x : 0);
                 }
                 s_units[at] = s;
                 s_flags[at] = 0;
@@ -926,9 +924,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int flags = s_flags[u % kTcUnits];
             const bool complete = w.now().parts() < 0;
             float* part = part_at(a, blockIdx.x, w.t0 == 0 ? 1 : 0);
-            int j = 0;
             long long orow = 0;
-            if (row < w.R) orow = out_row(a, w.req, w.h, w.r0 + row, &j);
+            if (row < w.R) orow = out_row(a, w.req.base, w.h, w.r0 + row);
             if (s == 0) {
                 const float m1 = s_ml[0][row];
                 const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.0f : M;
@@ -983,7 +980,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (tid == 0 && (flags & 1)) set_status(a.status, SPEC_ERR_PAGE);
-            if (w.now().parts() > 0) open = make_int4(w.now().parts(), w.b, w.now().unit, 0);
+            if (w.now().parts() > 0) open = open_of(w.now().parts(), w.req.base, w.r0, w.R, w.h);
             __syncwarp();
             tc_fence_before();
             asm volatile("bar.sync 1, 256;" ::: "memory");

@@ -705,10 +705,12 @@ int pages_info(PagesInfo& out) {
 }
 
 // One block per 16384 pages, in a cluster of a power of two: a small pool is
-// scanned by one block, without the launch and the barriers of sixteen.
+// scanned by one block, without the launch and the barriers of sixteen.  `least`
+// blocks where there is other work for them.
 template <typename A>
-int launch_cluster(void (*kernel)(A), const A& a, int most, cudaStream_t st) {
+int launch_cluster(void (*kernel)(A), const A& a, int least, int most, cudaStream_t st) {
     int blocks = 1;
+    while (blocks < least && blocks < most) blocks *= 2;
     while (blocks < most && (long long)blocks * kPgWarps * kPgWords * 32 < a.pages) blocks *= 2;
     return launch_dependent(kernel, dim3(blocks), kPgThreads, 0, st, blocks, a);
 }
@@ -772,7 +774,7 @@ int spec_reserve_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_cou
     if ((rc = pages_info(d)) != SPEC_OK) return rc;
     const ReserveArgs a{page_table, num_pages, ref_count, cache_len, verify_len, out_status,
                         (int*)workspace, pages, B, gamma, max_pages, page_size};
-    return launch_cluster(k_reserve_pages, a, d.cluster, (cudaStream_t)stream);
+    return launch_cluster(k_reserve_pages, a, 1, d.cluster, (cudaStream_t)stream);
 }
 
 int spec_commit_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages,
@@ -828,7 +830,7 @@ int spec_fork_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count,
     int32_t* list = (int32_t*)((char*)workspace + 256);
     const ForkArgs a{page_table, num_pages, ref_count, cache_len, src, dst, out_status, (int*)workspace, list,
                      c.pages, n, B, max_pages, c.page_size};
-    if ((rc = launch_cluster(k_fork_tables, a, d.cluster, (cudaStream_t)stream)) != SPEC_OK) return rc;
+    if ((rc = launch_cluster(k_fork_tables, a, (n + kPgWarps - 1) / kPgWarps, d.cluster, (cudaStream_t)stream)) != SPEC_OK) return rc;
     return launch_dependent(k_fork_copy, dim3(n, c.layers * 2, (unsigned)slices), kCopyThreads, 0,
                             (cudaStream_t)stream, 0, c, g, list, n);
 }
@@ -854,7 +856,7 @@ int spec_compact_pages(const int32_t* page_table, const int32_t* num_pages, cons
     const size_t P = (size_t)c.pages;
     const CompactArgs a{page_table, num_pages, ref_count, out_page_table, out_ref_count, out_total, (int*)workspace,
                         lists, lists + P, lists + 2 * P, lists + 3 * P, c.pages, B, max_pages};
-    if ((rc = launch_cluster(k_compact_plan, a, d.cluster, (cudaStream_t)stream)) != SPEC_OK) return rc;
+    if ((rc = launch_cluster(k_compact_plan, a, 1, d.cluster, (cudaStream_t)stream)) != SPEC_OK) return rc;
     return launch_dependent(k_compact_move, dim3(d.sms * 4), kCopyThreads, 0, (cudaStream_t)stream, 0, a, c,
                             page_shape(cache));
 }
