@@ -10,94 +10,92 @@ namespace specv {
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = kJoinThreads / 32;
+constexpr int kJoinPairs = SPEC_MAX_HEAD_DIM / 64;  // column pairs of a lane
+
+// A row's n parts: their maximum M, and sums scaled by 2^-M.
+struct Joined {
+    float M, L;
+    float2 o[kJoinPairs];
+};
+
+__device__ __forceinline__ Joined join_parts(const AttendArgs& a, int dim, int r, int n) {
+    constexpr int BATCH = 4;  // parts whose values are fetched together
+    const int lane = threadIdx.x & 31;
+    const float* own = part_at(a, blockIdx.x, 1);
+    const float* rest = part_at(a, blockIdx.x + 1, 0);
+    Joined s;
+    s.M = -INFINITY;
+    s.L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kJoinPairs; ++e) s.o[e] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+        float m[BATCH], l[BATCH];
+        float2 o[BATCH][kJoinPairs];
+#pragma unroll
+        for (int f = 0; f < BATCH; ++f) {
+            const int i = i0 + f;
+            m[f] = -INFINITY;
+            l[f] = 0.0f;
+            if (i < n) {
+                const float* p = i == 0 ? own : rest + (i - 1) * 2 * a.part_floats;
+                m[f] = p[a.tile_rows * dim + r];
+                l[f] = p[a.tile_rows * (dim + 1) + r];
+#pragma unroll
+                for (int e = 0; e < kJoinPairs; ++e)
+                    if (2 * lane + 64 * e < dim) o[f][e] = *(const float2*)(p + r * dim + 2 * lane + 64 * e);
+            }
+        }
+        const float M = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), s.M);
+        const float base = M == -INFINITY ? 0.0f : M, old = exp2f(s.M - base);
+        s.M = M;
+        s.L *= old;
+#pragma unroll
+        for (int e = 0; e < kJoinPairs; ++e) {
+            s.o[e].x *= old;
+            s.o[e].y *= old;
+        }
+#pragma unroll
+        for (int f = 0; f < BATCH; ++f)
+            if (i0 + f < n) {
+                const float w = exp2f(m[f] - base);
+                s.L = fmaf(w, l[f], s.L);
+#pragma unroll
+                for (int e = 0; e < kJoinPairs; ++e)
+                    if (2 * lane + 64 * e < dim) {
+                        s.o[e].x = fmaf(w, o[f][e].x, s.o[e].x);
+                        s.o[e].y = fmaf(w, o[f][e].y, s.o[e].y);
+                    }
+            }
+    }
+    return s;
+}
 
 // Joins the parts of the unit that block blockIdx.x left open: the block's own
-// and those of the blocks after it, in order.  With each part's maximum m_i
-// and sum l_i, M = max m_i: out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// One warp a row; bound by its round trips, of which there are two: what is
-// open, and then the first parts' outputs together with all maxima and sums.
+// and those of the blocks after it, in a fixed order.  With each part's maximum
+// m_i and sum l_i, M = max m_i: out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// Bound by its round trips: what is open, then four parts at a time.  One warp a
+// row.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendArgs a, CacheView c) {
-    constexpr int NE = SPEC_MAX_HEAD_DIM / 64, FIRST = 4;  // column pairs of a lane; parts fetched ahead
     pdl_trigger();
     pdl_wait();
     const int4 open = a.open[blockIdx.x];
     const int n = open.x, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (n == 0 || r >= (int)((uint32_t)open.w >> 16)) return;
     const int dim = c.head_dim;
-    const float* first = part_at(a, blockIdx.x, 1);
-    const float* rest = part_at(a, blockIdx.x + 1, 0);
-    const long long hop = 2 * a.part_floats;
-    auto part = [&](int i) { return i == 0 ? first : rest + (i - 1) * hop; };
-    float2 o[FIRST][NE];
-#pragma unroll
-    for (int i = 0; i < FIRST; ++i)
-#pragma unroll
-        for (int e = 0; e < NE; ++e)
-            if (i < n && 2 * lane + 64 * e < dim) o[i][e] = *(const float2*)(part(i) + r * dim + 2 * lane + 64 * e);
-    // maxima and sums, a part a lane
-    float m0 = -INFINITY, l0 = 0.0f, M = -INFINITY;
-    if (lane < n) {
-        m0 = part(lane)[a.tile_rows * dim + r];
-        l0 = part(lane)[a.tile_rows * (dim + 1) + r];
-        M = m0;
-    }
-    for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, part(i)[a.tile_rows * dim + r]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    const float base = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
-    float2 acc[NE];
-#pragma unroll
-    for (int e = 0; e < NE; ++e) acc[e] = make_float2(0.0f, 0.0f);
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        float w = 0.0f, l = 0.0f;
-        if (i0 + lane < n) {
-            w = exp2f((i0 == 0 ? m0 : part(i0 + lane)[a.tile_rows * dim + r]) - base);
-            l = (i0 == 0 ? l0 : part(i0 + lane)[a.tile_rows * (dim + 1) + r]) * w;
-        }
-        L += warp_sum(l);
-        const int m = min(32, n - i0);
-        int i = 0;
-        if (i0 == 0) {
-#pragma unroll
-            for (int f = 0; f < FIRST; ++f) {
-                const float wf = __shfl_sync(0xffffffffu, w, f);
-                if (f < n) {
-#pragma unroll
-                    for (int e = 0; e < NE; ++e)
-                        if (2 * lane + 64 * e < dim) {
-                            acc[e].x = fmaf(wf, o[f][e].x, acc[e].x);
-                            acc[e].y = fmaf(wf, o[f][e].y, acc[e].y);
-                        }
-                }
-            }
-            i = min(FIRST, m);
-        }
-#pragma unroll 4
-        for (; i < m; ++i) {
-            const float* p = part(i0 + i) + r * dim;
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-#pragma unroll
-            for (int e = 0; e < NE; ++e)
-                if (2 * lane + 64 * e < dim) {
-                    const float2 x = *(const float2*)(p + 2 * lane + 64 * e);
-                    acc[e].x = fmaf(wi, x.x, acc[e].x);
-                    acc[e].y = fmaf(wi, x.y, acc[e].y);
-                }
-        }
-    }
+    const Joined s = join_parts(a, dim, r, n);
     const long long row = out_row(a, open.y, open.w & 0xffff, open.z + r);
-    const float inv = 1.0f / L;
+    const float inv = 1.0f / s.L;
 #pragma unroll
-    for (int e = 0; e < NE; ++e)
+    for (int e = 0; e < kJoinPairs; ++e)
         if (2 * lane + 64 * e < dim) {
             Vec<T, 2> two;
-            two.x[0] = from_f32<T>(acc[e].x * inv);
-            two.x[1] = from_f32<T>(acc[e].y * inv);
+            two.x[0] = from_f32<T>(s.o[e].x * inv);
+            two.x[1] = from_f32<T>(s.o[e].y * inv);
             *(Vec<T, 2>*)((T*)a.out + row * dim + 2 * lane + 64 * e) = two;
         }
-    if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
+    if (a.lse && lane == 0) a.lse[row] = (s.M + log2f(s.L)) * 0.6931471805599453f;
 }
 
 }  // namespace specv
@@ -203,7 +201,10 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
     a.tile_rows = p.tile_rows;
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
     a.lead = tc ? 3 : 2;
-    a.least = 2;
+    // a part costs the joining kernel about 0.2 us a row, a tile its block 0.45 us
+    // (64 keys) or 1.1 us (128): a unit of t tiles in parts of sqrt(0.2 / 0.45 t)
+    // or sqrt(0.2 / 1.1 t) tiles spends as long on the one as on the other
+    a.part_cost = tc ? 0.2f / 1.1f : 0.2f / 0.45f;
     if (dt == SPEC_F32) rc = attend_simt(a, c, p.blocks, st);
     else if (tc) rc = attend_tc(a, c, dt, cache->dt, p.blocks, st);
     else if (cache->dt == SPEC_E4M3) rc = attend_mma8(a, c, dt, p.blocks, st);

@@ -24,10 +24,10 @@ struct AttendArgs {
     long long part_floats;
     int q_heads, group, rows, B, gamma, max_pages;
     int window, sinks;
-    int tile_rows;  // rows of a unit at most
-    int lead;       // what a unit costs beside its tiles, in tiles
-    int least;      // tiles of a block at least
-    float scale;    // of the scores, to base 2
+    int tile_rows;    // rows of a unit at most
+    int lead;         // what a unit costs beside its tiles, in tiles
+    float part_cost;  // of a part when joined, in tiles
+    float scale;      // of the scores, to base 2
     FastDiv by_group;
 };
 
@@ -95,6 +95,7 @@ __device__ __forceinline__ bool all_see(const AttendArgs& a, const Request& r, i
 
 struct Run {
     int b;           // request of the run's first tile
+    int longest;     // tiles of the longest unit
     long long at;    // tile within the request (unit-major, leads included)
     long long left;  // tiles of the run
     long long step;  // tiles of every block's run
@@ -108,11 +109,14 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
     const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = tid * per, b1 = min(a.B, b0 + per);
     long long mine = 0;
+    int longest = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const Request r = request_of<KT>(a, c, b);
         mine += (long long)r.units * (r.tiles + a.lead);
+        longest = max(longest, r.tiles);
     }
+    longest = (int)__reduce_max_sync(0xffffffffu, (unsigned)longest);
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -120,8 +124,12 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
         if (lane >= o) x += y;
     }
     if (lane == 31) s_scan[warp] = x;
-    if (tid == 0) s_run->left = 0;
+    if (tid == 0) {
+        s_run->left = 0;
+        s_run->longest = 0;
+    }
     __syncthreads();
+    if (lane == 0) atomicMax(&s_run->longest, longest);
     long long before = x - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
@@ -129,7 +137,11 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
         if (w < warp) before += s;
         total += s;
     }
-    const long long step = max((total + gridDim.x - 1) / gridDim.x, (long long)a.least);
+    __syncthreads();
+    // few long units are not cut into more parts than joining them is worth
+    longest = s_run->longest;
+    const int least = max(2, (int)sqrtf(a.part_cost * (float)longest));
+    const long long step = max((total + gridDim.x - 1) / gridDim.x, (long long)least);
     const long long start = (long long)blockIdx.x * step;
     if (start >= before && start < before + mine) {
         long long at = start - before;

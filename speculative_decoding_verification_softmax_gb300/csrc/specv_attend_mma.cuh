@@ -296,11 +296,17 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                                  : "r"((kv ? sv : sk) + tile_at<CH>(k, ch))
                                  : "memory");
                     const uint32_t to = wide + kv * (KT * D * 2);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + tile_at<CW>(k, 2 * ch)),
-                                 "r"(widen2(x.x)), "r"(widen2(x.x >> 16)), "r"(widen2(x.y)), "r"(widen2(x.y >> 16))
+                    const uint4 lo = make_uint4(widen2(x.x), widen2(x.x >> 16), widen2(x.y), widen2(x.y >> 16));
+                    const uint4 hi = make_uint4(widen2(x.z), widen2(x.z >> 16), widen2(x.w), widen2(x.w >> 16));
+                    // a row's second four chunks store their upper half first: eight
+                    // lanes then meet eight bank groups
+                    const bool turn = (ch & 4) != 0;
+                    const uint4 a0 = turn ? hi : lo, a1 = turn ? lo : hi;
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + tile_at<CW>(k, 2 * ch + (turn ? 1 : 0))),
+                                 "r"(a0.x), "r"(a0.y), "r"(a0.z), "r"(a0.w)
                                  : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + tile_at<CW>(k, 2 * ch + 1)),
-                                 "r"(widen2(x.z)), "r"(widen2(x.z >> 16)), "r"(widen2(x.w)), "r"(widen2(x.w >> 16))
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + tile_at<CW>(k, 2 * ch + (turn ? 0 : 1))),
+                                 "r"(a1.x), "r"(a1.y), "r"(a1.z), "r"(a1.w)
                                  : "memory");
                 }
                 __syncthreads();

@@ -14,13 +14,16 @@ constexpr int kSimtRows = 16;
 constexpr int kSimtKeys = 64;
 constexpr int kSimtPad = 20;  // floats of a key's weights (16 rows): conflict-free 16-byte stores
 
+// Blocks of an SM, by shared memory: 43, 80 and 154 KB each.
+constexpr int simt_per_sm(int dim) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
+
 template <int D>
 constexpr size_t simt_smem() {
     return sizeof(float) * (kSimtRows * D + kSimtKeys * (D + 4) + kSimtKeys * D + kSimtKeys * kSimtPad);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, CacheView c) {
+__global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(AttendArgs a, CacheView c) {
     using T = float;
     constexpr int KT = kSimtKeys, CN = D / 64;
     extern __shared__ float4 smem4[];
@@ -188,9 +191,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_attend_simt(AttendArgs a, Cach
 
 AttendPlan attend_simt_plan(int rows, int head_dim, int sms) {
     (void)rows;
-    (void)head_dim;
     AttendPlan p;
-    p.blocks = sms;
+    p.blocks = sms * simt_per_sm(head_dim);
     p.tile_rows = kSimtRows;
     return p;
 }

@@ -58,6 +58,8 @@ struct TcShape {
     static constexpr int kRaw = F8 ? (D == 64 ? 10 : 5) : 0;
     static constexpr int kQ = kTcRows * 128 * (D / 64);
     static constexpr int kSmem = 1024 + kQ + kSlots * kTile + kRaw * kRawTile;
+    // beside it, about 2 KB of barriers, units and weights have to fit 227 KB
+    static_assert(kSmem + 2048 <= 227 * 1024, "shared memory of an SM");
     static constexpr int kCols = 512;  // TMEM columns: S0, S1, O0, O1 (a power of two)
 };
 
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int KT = kTcKeys, NS = Sh::kSlots, CW = D / 8;  // CW: 16-byte chunks of a row
     constexpr int NR = F8 ? Sh::kRaw : NS;                    // slots that TMA fills
     extern __shared__ char smem_raw[];
-    __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[NR];
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[F8 ? NR : 1];
     __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
     __shared__ __align__(8) uint64_t unit_full[kTcUnits], unit_empty[kTcUnits];
     __shared__ __align__(16) Unit s_units[kTcUnits];
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < NR; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 1);
+            if (F8) mbar_init(&raw_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
