@@ -109,7 +109,8 @@ bool heads_ok(int q_heads, int kv_heads) {
     return q_heads >= 1 && kv_heads >= 1 && q_heads <= 65535 && q_heads % kv_heads == 0;
 }
 
-// The workspace's size may not depend on the GPU: it is that of the largest
+// The workspace's size may not depend on the GPU, nor on the cache's type (e4m3
+// has the most blocks): it is that of the largest
 // grid the library launches.
 constexpr int kMostSms = 160;
 
@@ -135,7 +136,7 @@ size_t spec_attend_workspace_bytes(int B, int gamma, int q_heads, int kv_heads, 
         return 0;
     const int rows = (gamma + 1) * (q_heads / kv_heads);
     return header_bytes() + max(parts_bytes(attend_simt_plan(rows, head_dim, kMostSms), head_dim),
-                                max(parts_bytes(attend_mma_plan(rows, head_dim, kMostSms), head_dim),
+                                max(parts_bytes(attend_mma_plan(rows, head_dim, true, kMostSms), head_dim),
                                     parts_bytes(attend_tc_plan(kMostSms), head_dim)));
 }
 
@@ -197,7 +198,7 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
     const bool tc = dt != SPEC_F32 && attend_tc_takes(c, most);
     const AttendPlan p = dt == SPEC_F32 ? attend_simt_plan(most, c.head_dim, sms)
                          : tc           ? attend_tc_plan(sms)
-                                        : attend_mma_plan(most, c.head_dim, sms);
+                                        : attend_mma_plan(most, c.head_dim, cache->dt == SPEC_E4M3, sms);
     a.tile_rows = p.tile_rows;
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
     a.lead = tc ? 3 : 2;

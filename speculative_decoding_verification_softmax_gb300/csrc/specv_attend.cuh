@@ -284,7 +284,7 @@ AttendPlan attend_simt_plan(int rows, int head_dim, int sms);
 int attend_simt(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st);
 
 // 16-bit rows: warp-level matrix instructions, over 16-bit and e4m3 caches.
-AttendPlan attend_mma_plan(int rows, int head_dim, int sms);
+AttendPlan attend_mma_plan(int rows, int head_dim, bool f8, int sms);
 int attend_mma16(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 int attend_mma8(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 

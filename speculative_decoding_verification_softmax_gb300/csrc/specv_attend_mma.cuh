@@ -12,7 +12,9 @@
 //     tile costs one barrier; the WK parts are joined when the unit ends;
 //   - S = Q K^T has its accumulators laid out as the next product's A operand,
 //     so the weights never leave the registers.
-// An e4m3 cache is widened once per tile to fp16 (exact) in shared memory.
+// An e4m3 cache is widened to fp16 (exact) on the way from shared memory to the
+// operands: its keys' bytes are read 16 at a time in an order that the query rows
+// share, and its values are transposed as pairs of bytes.
 #pragma once
 
 #include <type_traits>
@@ -90,25 +92,28 @@ __device__ __forceinline__ bool any_nonfinite<__half>(uint32_t w) {
     return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
 }
 
-// e4m3 pairs to fp16 pairs (exact).
-__device__ __forceinline__ uint32_t widen2(uint32_t two) {
-    uint32_t r;
-    asm("{.reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(two));
-    return r;
+// Four e4m3 values to fp16 (exact).
+__device__ __forceinline__ void widen4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 
 // Byte offset of 16-byte chunk `ch` of key row `k` in a tile with CH chunks a
 // row: the chunk is exchanged within its 128 bytes so that eight adjacent rows
-// have the same chunk in eight different bank groups.
+// have the same chunk in eight different bank groups, and (the order of the
+// exchange) two adjacent rows have four adjacent chunks in eight.
 template <int CH>
 __device__ __forceinline__ uint32_t tile_at(int k, int ch) {
-    if (CH >= 8) return (uint32_t)(k * CH + (ch ^ (k & 7))) * 16;
-    return (uint32_t)(k * CH + (ch ^ ((k / (8 / CH)) & (CH - 1)))) * 16;
+    if (CH >= 8) return (uint32_t)(k * CH + (ch ^ (((k & 1) << 2) | ((k >> 1) & 3)))) * 16;
+    return (uint32_t)(k * CH + (ch ^ ((k >> 1) & 3))) * 16;
 }
 
 // Blocks of an SM, by registers and shared memory.
-constexpr int mma_per_sm(int dim, int wr) {
-    return dim <= 64 ? (wr == 8 ? 2 : 3) : dim <= 128 ? (wr == 8 ? 1 : 2) : 1;
+constexpr int mma_per_sm(bool f8, int dim, int wr) {
+    return dim <= 64    ? (wr == 8 ? 2 : f8 ? 4 : 3)
+           : dim <= 128 ? (wr == 8 ? 1 : f8 ? 3 : 2)
+                        : (wr == 8 || !f8 ? 1 : 2);
 }
 
 template <bool F8, int D, int WR, int WK>
@@ -117,13 +122,12 @@ struct MmaShape {
     static constexpr int kRows = 16 * WR;
     static constexpr int kCh = D * (F8 ? 1 : 2) / 16;              // chunks of a cache row
     static constexpr int kStage = 2 * kMmaKeys * kCh * 16;         // K and V of a tile
-    static constexpr int kWide = F8 ? 2 * kMmaKeys * D * 2 : 0;    // the widened tile
-    static constexpr int kPerSm = mma_per_sm(D, WR);
+    static constexpr int kPerSm = mma_per_sm(F8, D, WR);
     static constexpr int kBudget = 226 * 1024 / kPerSm - 2048;
-    static constexpr int kFit = (kBudget - kWide) / kStage;
+    static constexpr int kFit = kBudget / kStage;
     static constexpr int kStages = kFit < 6 ? kFit : 6;
     static constexpr int kJoin = 4 * WK * kRows * (D + 4);         // outputs of all warps, fp32
-    static constexpr int kSmem = kStages * kStage + kWide > kJoin ? kStages * kStage + kWide : kJoin;
+    static constexpr int kSmem = kStages * kStage > kJoin ? kStages * kStage : kJoin;
     static_assert(kStages >= 2, "the ring needs two stages");
 };
 
@@ -232,7 +236,10 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
             for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int d = kk * 16 + 2 * t4 + (i >> 1) * 8;
+                    // e4m3: a thread's 16 adjacent bytes of a key are its operands of
+                    // four products, four bytes each
+                    const int d = F8 ? (kk >> 2) * 64 + t4 * 16 + (kk & 3) * 4 + (i >> 1) * 2
+                                     : kk * 16 + 2 * t4 + (i >> 1) * 8;
                     qf[kk][i] = have[i & 1] && d < dim ? *(const uint32_t*)(qp[i & 1] + d * 2) : 0u;
                 }
             rs[0] = rs[1] = a.scale * (F8 && c.k_scale ? c.k_scale[h] : 1.0f);
@@ -283,37 +290,7 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 cp_async_commit();
             }
             const int key0 = tile_key<KT>(req, t0 + t);
-            uint32_t sk = sbase + (t % NS) * Sh::kStage, sv = sk + Sh::kStage / 2;
-            if (F8) {
-                // widen to fp16: 16 values a step
-                const uint32_t wide = sbase + NS * Sh::kStage;
-                constexpr int CW = D * 2 / 16;
-                for (int i = tid; i < 2 * KT * CH; i += THREADS) {
-                    const int kv = i / (KT * CH), r = i - kv * (KT * CH), k = r / CH, ch = r - k * CH;
-                    uint4 x;
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                                 : "r"((kv ? sv : sk) + tile_at<CH>(k, ch))
-                                 : "memory");
-                    const uint32_t to = wide + kv * (KT * D * 2);
-                    const uint4 lo = make_uint4(widen2(x.x), widen2(x.x >> 16), widen2(x.y), widen2(x.y >> 16));
-                    const uint4 hi = make_uint4(widen2(x.z), widen2(x.z >> 16), widen2(x.w), widen2(x.w >> 16));
-                    // a row's second four chunks store their upper half first: eight
-                    // lanes then meet eight bank groups
-                    const bool turn = (ch & 4) != 0;
-                    const uint4 a0 = turn ? hi : lo, a1 = turn ? lo : hi;
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + tile_at<CW>(k, 2 * ch + (turn ? 1 : 0))),
-                                 "r"(a0.x), "r"(a0.y), "r"(a0.z), "r"(a0.w)
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + tile_at<CW>(k, 2 * ch + (turn ? 0 : 1))),
-                                 "r"(a1.x), "r"(a1.y), "r"(a1.z), "r"(a1.w)
-                                 : "memory");
-                }
-                __syncthreads();
-                sk = wide;
-                sv = wide + KT * D * 2;
-            }
-            constexpr int CW = D * 2 / 16;  // chunks of a 16-bit row
+            const uint32_t sk = sbase + (t % NS) * Sh::kStage, sv = sk + Sh::kStage / 2;
 
             const bool part = !all_see<KT>(a, req, key0);
             bool dirty = false;
@@ -321,9 +298,9 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 // values that are not finite, at keys that only some rows see,
                 // must not meet a weight of zero: they are taken out of the
                 // product and added by themselves to the rows that see them
-                for (int i = tid; i < KT * CW; i += THREADS) {
+                for (int i = tid; i < KT * CH; i += THREADS) {
                     uint32_t x[4];
-                    const uint32_t at = sv + tile_at<CW>(i / CW, i % CW);
+                    const uint32_t at = sv + tile_at<CH>(i / CH, i % CH);
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                                  : "r"(at)
@@ -331,7 +308,11 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                     bool any = false;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (any_nonfinite<T>(x[e])) {
+                        if (F8) {  // the bytes 7f and ff
+                            const uint32_t nan = ((x[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                            any |= nan != 0;
+                            x[e] &= ~((nan >> 7) * 0xffu);
+                        } else if (any_nonfinite<T>(x[e])) {
                             any = true;
                             if (any_nonfinite<T>(x[e] & 0xffffu)) x[e] &= 0xffff0000u;
                             if (any_nonfinite<T>(x[e] & 0xffff0000u)) x[e] &= 0xffffu;
@@ -354,16 +335,35 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 for (int n = 0; n < CK / 8; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
+                if (F8) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
+                    for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-                    for (int n = 0; n < CK / 16; ++n) {
-                        uint32_t b[4];
-                        const int i = lane >> 3;
-                        ldsm4(b, sk + tile_at<CW>(k0 + n * 16 + (i >> 1) * 8 + (lane & 7), kk * 2 + (i & 1)));
-                        mma16816<T>(s[2 * n], qf[kk], b[0], b[1]);
-                        mma16816<T>(s[2 * n + 1], qf[kk], b[2], b[3]);
-                    }
+                        for (int n = 0; n < CK / 8; ++n) {
+                            uint32_t x[4];
+                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                         : "r"(sk + tile_at<CH>(k0 + n * 8 + g, 4 * j + t4))
+                                         : "memory");
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t b0, b1;
+                                widen4(x[q], b0, b1);
+                                mma16816<T>(s[n], qf[4 * j + q], b0, b1);
+                            }
+                        }
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                        for (int n = 0; n < CK / 16; ++n) {
+                            uint32_t b[4];
+                            const int i = lane >> 3;
+                            ldsm4(b, sk + tile_at<CH>(k0 + n * 16 + (i >> 1) * 8 + (lane & 7), kk * 2 + (i & 1)));
+                            mma16816<T>(s[2 * n], qf[kk], b[0], b[1]);
+                            mma16816<T>(s[2 * n + 1], qf[kk], b[2], b[3]);
+                        }
+                }
                 // scores to base 2, masked where the tile is cut by a border
                 float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -412,13 +412,29 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                     const uint32_t p[4] = {pack2<T>(s[2 * n][0], s[2 * n][1]), pack2<T>(s[2 * n][2], s[2 * n][3]),
                                            pack2<T>(s[2 * n + 1][0], s[2 * n + 1][1]),
                                            pack2<T>(s[2 * n + 1][2], s[2 * n + 1][3])};
+                    const int i = lane >> 3, row = k0 + n * 16 + (i & 1) * 8 + (lane & 7);
+                    if (F8) {
+                        // pairs of bytes transposed: a register has two keys' values of
+                        // two adjacent columns, which go to two products
 #pragma unroll
-                    for (int dt = 0; dt < D / 16; ++dt) {
-                        uint32_t b[4];
-                        const int i = lane >> 3;
-                        ldsm4_t(b, sv + tile_at<CW>(k0 + n * 16 + (i & 1) * 8 + (lane & 7), dt * 2 + (i >> 1)));
-                        mma16816<T>(acc[2 * dt], p, b[0], b[1]);
-                        mma16816<T>(acc[2 * dt + 1], p, b[2], b[3]);
+                        for (int dt = 0; dt < D / 32; ++dt) {
+                            uint32_t b[4], even[4], odd[4];
+                            ldsm4_t(b, sv + tile_at<CH>(row, dt * 2 + (i >> 1)));
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) widen4(__byte_perm(b[q], 0, 0x3120), even[q], odd[q]);
+                            mma16816<T>(acc[4 * dt], p, even[0], even[1]);
+                            mma16816<T>(acc[4 * dt + 1], p, odd[0], odd[1]);
+                            mma16816<T>(acc[4 * dt + 2], p, even[2], even[3]);
+                            mma16816<T>(acc[4 * dt + 3], p, odd[2], odd[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; ++dt) {
+                            uint32_t b[4];
+                            ldsm4_t(b, sv + tile_at<CH>(row, dt * 2 + (i >> 1)));
+                            mma16816<T>(acc[2 * dt], p, b[0], b[1]);
+                            mma16816<T>(acc[2 * dt + 1], p, b[2], b[3]);
+                        }
                     }
                 }
                 if (dirty) {
@@ -432,7 +448,8 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                         for (int n = 0; n < D / 8; ++n)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const int d = n * 8 + 2 * t4 + (i & 1);
+                                const int d = F8 ? (n >> 1) * 16 + 4 * t4 + 2 * (i & 1) + (n & 1)
+                                                 : n * 8 + 2 * t4 + (i & 1);
                                 if (d >= dim || !sees(a, pos[i >> 1], key)) continue;
                                 const float x = F8 ? to_f32(((const __nv_fp8_e4m3*)v)[d]) : to_f32(((const T*)v)[d]);
                                 if (!(fabsf(x) <= 3.4e38f)) acc[n][i] += x;
@@ -458,9 +475,16 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 s_m[wk][r] = m[i];
                 s_l[wk][r] = l[i];
             }
+            if (F8) {
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-                *(float2*)(so + r * (D + 4) + n * 8 + 2 * t4) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+                for (int n = 0; n < D / 8; n += 2)
+                    *(float4*)(so + r * (D + 4) + n * 8 + 4 * t4) =
+                        make_float4(acc[n][2 * i], acc[n + 1][2 * i], acc[n][2 * i + 1], acc[n + 1][2 * i + 1]);
+            } else {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *(float2*)(so + r * (D + 4) + n * 8 + 2 * t4) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+            }
         }
         __syncthreads();
         const bool whole = w.whole();

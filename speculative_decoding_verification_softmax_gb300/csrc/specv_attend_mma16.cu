@@ -4,10 +4,10 @@
 namespace specv {
 
 // Rows of a unit: 16 for each of the warps that split them.
-AttendPlan attend_mma_plan(int rows, int head_dim, int sms) {
+AttendPlan attend_mma_plan(int rows, int head_dim, bool f8, int sms) {
     const int wr = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8;
     AttendPlan p;
-    p.blocks = sms * mma_per_sm(head_dim, wr);
+    p.blocks = sms * mma_per_sm(f8, head_dim, wr);
     p.tile_rows = 16 * wr;
     return p;
 }
