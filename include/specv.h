@@ -339,7 +339,8 @@ size_t spec_attend_workspace_bytes(int B, int gamma, int q_heads, int kv_heads, 
  *                request with another value has no rows (SPEC_ERR_VERIFY_LEN).
  *   cache        dt equal to q's, or SPEC_E4M3 under SPEC_BF16 / SPEC_F16 rows.
  *                Positions cache_len[b] .. cache_len[b] + ell_b must have been
- *                appended.  Entries that no row sees are not read.
+ *                appended.  Entries that no row sees have no influence, whatever
+ *                they hold; pages that no row sees any position of may be missing.
  *   scale        finite; normally 1 / sqrt(head_dim).
  *   window       0: all earlier positions; else the last `window` positions,
  *                the token's own included.  sinks: first positions that stay
@@ -349,7 +350,7 @@ size_t spec_attend_workspace_bytes(int B, int gamma, int q_heads, int kv_heads, 
  *   out_lse      [rows, q_heads] fp32 or NULL: log sum_t w_t.
  * A request whose positions do not fit its page table (SPEC_ERR_CACHE_LEN), or
  * with a needed entry that is not a page (SPEC_ERR_PAGE), gets NaN rows.  A
- * value that is not finite reaches only the rows that see it.
+ * value that is not finite reaches only the rows that see it.  Two launches.
  * Numbers: scores, running maximum and sum, and the output are fp32; with
  * 16-bit rows the weights are rounded to that type (to fp16 under a SPEC_E4M3
  * cache) for the product with v.  Bit-reproducible for given arguments; how a
@@ -370,8 +371,8 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
  *   (x, y) -> mscale * (x cos - y sin, x sin + y cos),
  * pair i = values (i, i + rotary_dim/2), or (2i, 2i+1) if `interleaved`; the
  * other values pass unchanged.  The turned k and v go to the request's pages
- * (divided by their scales, clamped to +-448 and rounded to nearest even for
- * SPEC_E4M3), the turned q to out_q.
+ * (times the reciprocal of their scales, clamped to +-448 and rounded to nearest
+ * even for SPEC_E4M3), the turned q to out_q.
  *   q, k, v      device, dt, row r and head h at r * row_stride + h * head_stride
  *                elements (16-byte multiples).
  *   row, rows    as q_row and rows of spec_attend.

@@ -556,6 +556,15 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+def _made_on(stream, make, *args, **kw):
+    """make(*args) on the stream that the call runs on: what is allocated, zeroed
+    and later freed there is in order with the call's kernels."""
+    if stream is None:
+        return make(*args, **kw)
+    with _torch().cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _cache_arg(k_cache, v_cache, k_scale, v_scale, dev, layered=False):
     """spec_cache of [pages, page_size, kv_heads, head_dim] tensors (with
     `layered` also [layers, pages, ...]) of any strides with adjacent values."""
@@ -690,13 +699,13 @@ def attend(q, k_cache, v_cache, page_table, cache_len, verify_len=None, row=None
     rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, row is not None, dev)
     _tables(page_table, cache_len, verify_len, row, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _made_on(stream, torch.empty, q.shape, dtype=q.dtype, device=q.device)
     else:
         _want("out", out, q.dtype, q.shape, dev)
     if out_lse is not None:
         _want("out_lse", out_lse, torch.float32, q.shape[:-1], dev)
     if workspace is None:
-        workspace = alloc_attend_workspace(B, gamma, heads, k_cache.shape[-2], dim, q.device)
+        workspace = _made_on(stream, alloc_attend_workspace, B, gamma, heads, k_cache.shape[-2], dim, q.device)
     rc = lib().spec_attend(q.data_ptr(), rs, hs, dt, heads, cache, page_table.data_ptr(), slots,
                            cache_len.data_ptr(), _address(verify_len), _address(row), rows, B, gamma,
                            dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _address(out_lse),
@@ -781,11 +790,11 @@ def append_kv(q, k, v, k_cache, v_cache, page_table, cache_len, verify_len=None,
         n = turns.numel()
         _want("turns", turns, torch.int64, (n,), dev)
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out_q = _made_on(stream, torch.empty, q.shape, dtype=q.dtype, device=q.device)
     else:
         _want("out_q", out_q, q.dtype, q.shape, dev)
     if workspace is None:
-        workspace = alloc_cache_workspace(B, 0, q.device)
+        workspace = _made_on(stream, alloc_cache_workspace, B, 0, q.device)
     rc = lib().spec_append_kv(q.data_ptr(), rs, hs, k.data_ptr(), v.data_ptr(), krs, khs, vrs, vhs, dt, heads, cache,
                               page_table.data_ptr(), slots, cache_len.data_ptr(), _address(verify_len), _address(row),
                               rows, B, gamma, _address(turns), 2 * n, 1 if interleaved else 0, mscale,
@@ -822,9 +831,9 @@ def reserve_pages(page_table, num_pages, ref_count, cache_len, verify_len=None, 
     if out_status is not None:
         _want("out_status", out_status, i32, (B,), dev)
     if out_status is None:
-        out_status = _torch().empty((B,), dtype=i32, device=page_table.device)
+        out_status = _made_on(stream, _torch().empty, (B,), dtype=i32, device=page_table.device)
     if workspace is None:
-        workspace = alloc_cache_workspace(B, 0, page_table.device)
+        workspace = _made_on(stream, alloc_cache_workspace, B, 0, page_table.device)
     rc = lib().spec_reserve_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
                                   cache_len.data_ptr(), _address(verify_len), B, gamma, slots, page_size,
                                   out_status.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace, dev),
@@ -847,7 +856,7 @@ def commit_pages(page_table, num_pages, ref_count, cache_len, accept_len, *, pag
     if out_cache_len is None:
         out_cache_len = cache_len
     if workspace is None:
-        workspace = alloc_cache_workspace(B, 0, page_table.device)
+        workspace = _made_on(stream, alloc_cache_workspace, B, 0, page_table.device)
     rc = lib().spec_commit_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
                                  cache_len.data_ptr(), accept_len.data_ptr(), B, slots, page_size, window, sinks,
                                  out_cache_len.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace, dev),
@@ -865,7 +874,7 @@ def free_pages(page_table, num_pages, ref_count, cache_len, requests, *, workspa
     n = requests.numel()
     _want("requests", requests, i32, (n,), dev)
     if workspace is None:
-        workspace = alloc_cache_workspace(B, 0, page_table.device)
+        workspace = _made_on(stream, alloc_cache_workspace, B, 0, page_table.device)
     rc = lib().spec_free_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
                                cache_len.data_ptr(), requests.data_ptr(), n, B, slots, workspace.data_ptr(),
                                _workspace_bytes(workspace, dev), _raw_stream(stream, dev))
@@ -891,9 +900,9 @@ def fork_pages(page_table, num_pages, ref_count, cache_len, src, dst, k_cache, v
     if cache.pages != pages:
         raise ValueError(f"the cache has {cache.pages} pages, ref_count {pages}")
     if out_status is None:
-        out_status = _torch().empty((n,), dtype=i32, device=page_table.device)
+        out_status = _made_on(stream, _torch().empty, (n,), dtype=i32, device=page_table.device)
     if workspace is None:
-        workspace = alloc_cache_workspace(B, 0, page_table.device)
+        workspace = _made_on(stream, alloc_cache_workspace, B, 0, page_table.device)
     rc = lib().spec_fork_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(),
                                cache_len.data_ptr(), src.data_ptr(), dst.data_ptr(), n, B, slots, cache,
                                out_status.data_ptr(), workspace.data_ptr(), _workspace_bytes(workspace, dev),
@@ -923,9 +932,9 @@ def compact_pages(page_table, num_pages, ref_count, k_cache, v_cache, *, out_pag
     out_page_table = page_table if out_page_table is None else out_page_table
     out_ref_count = ref_count if out_ref_count is None else out_ref_count
     if out_total is None:
-        out_total = _torch().empty((1,), dtype=i32, device=page_table.device)
+        out_total = _made_on(stream, _torch().empty, (1,), dtype=i32, device=page_table.device)
     if workspace is None:
-        workspace = alloc_cache_workspace(B, pages, page_table.device)
+        workspace = _made_on(stream, alloc_cache_workspace, B, pages, page_table.device)
     rc = lib().spec_compact_pages(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), B, slots, cache,
                                   out_page_table.data_ptr(), out_ref_count.data_ptr(), out_total.data_ptr(),
                                   workspace.data_ptr(), _workspace_bytes(workspace, dev), _raw_stream(stream, dev))

@@ -179,8 +179,8 @@ __device__ __forceinline__ void put_item(const AppendArgs& a, const CacheView& c
 // A block has RB adjacent rows of one request: a thread works its items' places
 // out once and takes them in every row, all rows' loads in flight together.  One
 // row a block (RB = 1) is for batches that would not fill the GPU otherwise; a
-// large batch with one row a block was bound by instructions (33 us against HERE
-// for 4,600 rows of 40 + 8 heads of 128).  A block's first loads are on their way
+// large batch with one row a block was bound by instructions (33 us against
+// 26 for 4,600 rows of 40 + 8 heads of 128).  A block's first loads are on their way
 // before the angles and the pages are known.
 template <typename T, typename C, bool INTERLEAVED, int E, int RB>
 __global__ void __launch_bounds__(RB == 1 ? kAppendMost : kAppendFour) k_append(AppendArgs a, CacheView c) {

@@ -374,8 +374,22 @@ struct Unit {
     }
 };
 
+// True in all `threads` threads of named barrier `id` if it is in each: roles of
+// several warps that meet at barriers go on to the next unit, or end, together.
+__device__ __forceinline__ bool all_agree(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
 // A role's view of the ring: next() waits for the next unit, done() gives the
-// last one's place back (each role's warps once).
+// last one's place back (each role's warps once).  After a wait that ran out of
+// time there is no next unit.
 struct Units {
     const Unit* ring;
     uint64_t* full;
@@ -389,9 +403,7 @@ struct Units {
         : ring(r), full(f), empty(e), fail(x), u(-1) {}
     __device__ __forceinline__ bool next() {
         ++u;
-        tc_wait(&full[u % kTcUnits], (u / kTcUnits) & 1, fail);
-        __syncwarp();
-        if (*fail) return false;
+        if (!__all_sync(0xffffffffu, tc_wait(&full[u % kTcUnits], (u / kTcUnits) & 1, fail))) return false;
         const Unit& s = ring[u % kTcUnits];
         nt = s.nt;
         if (nt == 0) return false;
@@ -587,7 +599,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t item = 0, turns = 0;  // turns: phases of raw_full by slot (16-bit cache)
         int u = 0;
         Units w(s_units, unit_full, unit_empty, fail);
-        while (w.next()) {
+        while (all_agree(2, 128, w.next())) {
             // a negative scale turns the rows' signs
             const uint32_t flip = (a.scale < 0.0f) != (F8 && c.k_scale && c.k_scale[w.h] < 0.0f) ? 0x80008000u : 0u;
             // the products of the unit before are done with the query rows
@@ -692,7 +704,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
                     if (lt == 0) mbar_arrive(&raw_empty[rs]);
                 } else {
                     tc_wait(&raw_full[slot], (turns >> slot) & 1, fail);
@@ -711,7 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
                 }
                 if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);
                 __syncwarp();
@@ -726,8 +738,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int u = 0;; ++u) {
             const bool more = w.next(a, c);
             const int at = u % kTcUnits;
-            if (u >= kTcUnits) tc_wait(&unit_empty[at], ((u / kTcUnits) & 1) ^ 1, fail);
-            __syncwarp();
+            // a place that is not given back in time is not written over
+            if (!__all_sync(0xffffffffu,
+                            u < kTcUnits || tc_wait(&unit_empty[at], ((u / kTcUnits) & 1) ^ 1, fail)))
+                break;
             if (lane == 0) {
                 Unit s;
                 s.nt = 0;
@@ -749,7 +763,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_arrive(&unit_full[at]);
             }
             __syncwarp();
-            if (!more || *fail) break;
+            if (!more) break;
         }
     } else if (warp == 15) {
         // ------------------------------------------------- matrix instructions
@@ -826,7 +840,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t seen = 0;  // tiles of the stream so far
         int u = 0;
         Units w(s_units, unit_full, unit_empty, fail);
-        while (w.next()) {
+        while (all_agree(1, 256, w.next())) {
             const bool active = (warp & 3) * 32 < w.R;  // the warp has rows
             const int pos = w.req.n + (row < w.R ? (int)a.by_group.div((uint32_t)(w.r0 + row)) : w.req.ell);
             float scale = fabsf(a.scale) * (F8 && c.k_scale ? fabsf(c.k_scale[w.h]) : 1.0f);
@@ -984,8 +998,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (tid == 0 && (flags & 1)) set_status(a.status, SPEC_ERR_PAGE);
             if (w.now().parts() > 0) open = open_of(w.now().parts(), w.req.base, w.r0, w.R, w.h);
             __syncwarp();
-            tc_fence_before();
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            tc_fence_before();  // the barrier on the way to the next unit: both halves are written
             ++u;
             w.done();
         }

@@ -206,6 +206,35 @@ def test_scale(sv):
     case.check(zero, scale=0.0)
 
 
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("gamma", [0, 16])
+def test_negative_scales(sv, dtype, cache, gamma):
+    case = Case(lens=[150, 9], ell=[gamma, gamma // 2], gamma=gamma, heads=8, kv_heads=2, dtype=dtype, cache=cache, seed=20)
+    if case.k_scale is not None:
+        case.k_scale[0] *= -1
+        case.v_scale[1] *= -1
+    out, ws = case.call(sv, scale=-0.2, out=torch.zeros(case.q.shape, dtype=case.q.dtype, device="cuda"))
+    assert sv.read_status(ws) == 0
+    case.check(out, scale=-0.2)
+
+
+@pytest.mark.parametrize("gamma", [0, 16])
+def test_on_a_given_stream(sv, gamma):
+    """Outputs and workspace made by the call belong to its stream."""
+    case = Case(lens=[700, 33], ell=[gamma, gamma], gamma=gamma, heads=8, kv_heads=2, dim=128, seed=21)
+    caches, q = case.caches(), case.q.cuda()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                   # the current stream is far behind
+    out, ws = case.call(sv, q=q, caches=caches, stream=s)
+    s.synchronize()
+    with torch.cuda.stream(s):
+        got = out.cpu()
+    assert sv.read_status(ws, stream=s) == 0
+    torch.cuda.synchronize()
+    case.check(got)
+
+
 def test_many_requests(sv):
     """More requests than threads of a block, most of them short."""
     B = 700

@@ -291,6 +291,40 @@ def test_append(sv, dtype, cache, dim, rotary, interleaved, packed):
     assert np.array_equal(kc[~touched], before[0][~touched]) and np.array_equal(vc[~touched], before[1][~touched])
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("packed", [False, True])
+def test_append_a_large_batch(sv, cache, interleaved, packed):
+    """Batches that take several rows a block are turned like small ones, bit for bit."""
+    B, gamma, heads, H, dim, page = 200, 14, 6, 2, 64, 16
+    g = torch.Generator().manual_seed(8)
+    ell = torch.randint(-1, gamma + 1, (B,), generator=g).to(torch.int32)
+    lens = torch.randint(0, 3 * page, (B,), generator=g).to(torch.int32)
+    slots = 5
+    table = torch.randperm(B * slots, generator=g).to(torch.int32).view(B, slots).cuda()
+    n = (ell + 1).clamp(min=0)
+    row = (torch.cumsum(n, 0) - n).to(torch.int32).cuda() if packed else None
+    rows = (int(n.sum()),) if packed else (B, gamma + 1)
+    q, k, v = (torch.randn(rows + (h, dim), generator=g).bfloat16().cuda() for h in (heads, H, H))
+    scales = [torch.rand(H, generator=g).cuda() + 0.1 for _ in range(2)] if cache == "e4m3" else [None, None]
+    turns = sv.rope_table(sv.rope_frequencies(dim))
+    kw = dict(gamma=gamma, turns=turns, interleaved=interleaved, k_scale=scales[0], v_scale=scales[1])
+    K = torch.zeros(B * slots, page, H, dim, device="cuda").to(TYPES[cache])
+    V, K1, V1 = K.clone(), K.clone(), K.clone()
+    out, out1 = torch.zeros_like(q), torch.zeros_like(q)
+    ell, lens = ell.cuda(), lens.cuda()
+    _, ws = sv.append_kv(q, k, v, K, V, table, lens, ell, row, out_q=out, **kw)
+    assert sv.read_status(ws) == sv.ERR_VERIFY_LEN
+    for b in range(0, B, 20):
+        s = slice(b, b + 20)
+        at = (slice(None),) if packed else (s,)
+        sv.append_kv(q[at], k[at], v[at], K1, V1, table[s].contiguous(), lens[s].contiguous(), ell[s].contiguous(),
+                     None if row is None else row[s].contiguous(), out_q=out1[at], **kw)
+    raw = (lambda x: x.view(torch.uint8)) if cache == "e4m3" else (lambda x: x)
+    assert torch.equal(out, out1) and torch.equal(raw(K), raw(K1)) and torch.equal(raw(V), raw(V1))
+    assert float(out.float().abs().sum()) > 0 and float(K.float().abs().sum()) > 0
+
+
 def test_append_in_place_and_clamped(sv):
     """out_q = q; values beyond the 8-bit range are clamped."""
     q = torch.randn(1, 2, 2, 64, device="cuda", dtype=torch.bfloat16)
