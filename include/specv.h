@@ -449,6 +449,8 @@ int spec_fork_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count,
  * Compaction: the N referenced pages move to the ids 0..N-1.  Pages below N
  * stay; the k-th lowest referenced page from N on goes to the k-th lowest free
  * one, with its tokens of all layers, and the tables and counts are renamed.
+ * Table entries behind num_pages[b] become -1.  Whoever else keeps a page's id has
+ * to keep it in a table too: a referenced page moves whether an entry names it or not.
  *   out_page_table [B, max_pages], out_ref_count [pages]: may be page_table and
  *   ref_count.  out_total [1] int32: N.
  */

@@ -476,8 +476,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     const uint32_t sq = base, ring = base + Sh::kQ, raws = ring + NS * Sh::kTile;
 
-    pdl_trigger();
-    if (warp == 15) tc_alloc(&s_tmem, Sh::kCols);
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
@@ -502,10 +500,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_mbar_init();
         s_fail = 0;
     }
-    tc_fence_before();
+    // TMEM is taken behind the wait, and the next kernel may be placed only then:
+    // kernels beside one another, of which one waits for the other, could each
+    // hold columns that the other needs
     pdl_wait();
+    if (warp == 15) tc_alloc(&s_tmem, Sh::kCols);
+    tc_fence_before();
     run_of<KT, kTcThreads>(a, c, s_scan, &s_run);  // also the barrier behind the set-up
     tc_fence_after();
+    pdl_trigger();
     const uint32_t tmem = s_tmem;
     volatile int* fail = &s_fail;
 
