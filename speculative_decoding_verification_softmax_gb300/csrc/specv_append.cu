@@ -37,7 +37,7 @@ struct AppendArgs {
 };
 
 // Threads of a block: with one row, two items each where 128 to 512 of them do.
-constexpr int kAppendLeast = 128, kAppendMost = 512, kAppendFour = 256;
+constexpr int kAppendLeast = 128, kAppendMost = 512, kAppendTwo = 128;
 
 // One work item of a row: vector `at` of a q, k or v head, and its partner in a
 // half layout.
@@ -179,11 +179,12 @@ __device__ __forceinline__ void put_item(const AppendArgs& a, const CacheView& c
 // A block has RB adjacent rows of one request: a thread works its items' places
 // out once and takes them in every row, all rows' loads in flight together.  One
 // row a block (RB = 1) is for batches that would not fill the GPU otherwise; a
-// large batch with one row a block was bound by instructions (33 us against
-// 26 for 4,600 rows of 40 + 8 heads of 128).  A block's first loads are on their way
-// before the angles and the pages are known.
+// large batch with one row a block was bound by instructions.  4,600 rows of 40 + 8
+// heads of 128, 103 MB: one row 31 us, two rows 25 us (12 blocks of 128 threads an
+// SM; 26 us with 8), four rows 27 to 38 us (their registers leave fewer warps).  A
+// block's first loads are on their way before the angles and the pages are known.
 template <typename T, typename C, bool INTERLEAVED, int E, int RB>
-__global__ void __launch_bounds__(RB == 1 ? kAppendMost : kAppendFour) k_append(AppendArgs a, CacheView c) {
+__global__ void __launch_bounds__(RB == 1 ? kAppendMost : kAppendTwo, RB == 1 ? 1 : 12) k_append(AppendArgs a, CacheView c) {
     __shared__ __align__(16) float s_cos[RB][SPEC_MAX_HEAD_DIM / 2], s_sin[RB][SPEC_MAX_HEAD_DIM / 2];
     __shared__ long long s_entry[RB];
     pdl_trigger();
@@ -269,13 +270,13 @@ int launch_vectors(AppendArgs a, const CacheView& c, cudaStream_t st) {
     a.by_items = FastDiv((uint32_t)a.items);
     a.by_head = FastDiv((uint32_t)per_head);
     a.by_half = FastDiv((uint32_t)max(a.half, 1));
-    // four rows a block where the blocks still fill the GPU twice over
+    // two rows a block where the blocks still fill the GPU four times over
     int sms = 0;
     if (const int rc = sm_count(sms)) return rc;
-    const int four = (a.gamma + 4) / 4;
-    if ((long long)a.B * four >= 4ll * sms) {
-        a.by_blocks = FastDiv((uint32_t)four);
-        return launch_dependent(k_append<T, C, INTERLEAVED, E, 4>, dim3(a.B * four), kAppendFour, 0, st, 0, a, c);
+    const int two = (a.gamma + 2) / 2;
+    if ((long long)a.B * two >= 4ll * sms) {
+        a.by_blocks = FastDiv((uint32_t)two);
+        return launch_dependent(k_append<T, C, INTERLEAVED, E, 2>, dim3(a.B * two), kAppendTwo, 0, st, 0, a, c);
     }
     a.by_blocks = FastDiv((uint32_t)a.gamma + 1);
     const int threads = min(kAppendMost, max(kAppendLeast, (a.all + 63) / 64 * 32));
