@@ -60,7 +60,13 @@ struct TcShape {
     static constexpr int kSmem = 1024 + kQ + kSlots * kTile + kRaw * kRawTile;
     // beside it, about 2 KB of barriers, units and weights have to fit 227 KB
     static_assert(kSmem + 2048 <= 227 * 1024, "shared memory of an SM");
-    static constexpr int kCols = 512;  // TMEM columns: S0, S1, O0, O1 (a power of two)
+    // Tiles whose scores are under way, each in TMEM columns of its own: the scores
+    // of tile i are taken before the products with V of tile i - kAhead.  A third
+    // one, for which heads of 64 leave room, lets a stream find its next scores
+    // ready when it has handed over its weights.
+    static constexpr int kAhead = D == 64 ? 3 : 2;
+    static constexpr int kCols = 512;  // TMEM columns: scores, O0, O1 (a power of two)
+    static_assert(kAhead * kTcKeys + 2 * D <= kCols, "columns of TMEM");
 };
 
 struct TcArgs {
@@ -240,19 +246,13 @@ __device__ __forceinline__ bool tc_nonfinite(uint32_t w, uint32_t half_mask) {
     return (w & e) == e;
 }
 
-// Item i of a unit of nt tiles, in the order of use: K0, K1, V0, K2, V1, ...
+// Item i of a unit of nt tiles, in the order of use: K0, K1, V0, K2, V1, ... where
+// K is two tiles ahead.
+template <int AHEAD>
 __device__ __forceinline__ void item_of(int i, int nt, bool& is_v, int& t) {
-    if (i < 2 && nt > 1) {
-        is_v = false;
-        t = i;
-    } else if (nt == 1) {
-        is_v = i == 1;
-        t = 0;
-    } else {
-        const int x = i - 2, pairs = 2 * (nt - 2);
-        is_v = x >= pairs || (x & 1) == 0;
-        t = x >= pairs ? nt - 2 + (x - pairs) : is_v ? x >> 1 : (x >> 1) + 2;
-    }
+    const int first = min(AHEAD, nt), x = i - first, pairs = 2 * (nt - first);
+    is_v = x >= pairs || (x >= 0 && (x & 1) == 0);
+    t = x < 0 ? i : x >= pairs ? nt - first + (x - pairs) : is_v ? x >> 1 : (x >> 1) + first;
 }
 
 __device__ __forceinline__ bool sees_all(const AttendArgs& a, const Request& r, int t) {
@@ -459,11 +459,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv) {
     using Sh = TcShape<F8, D>;
-    constexpr int KT = kTcKeys, NS = Sh::kSlots, CW = D / 8;  // CW: 16-byte chunks of a row
+    constexpr int KT = kTcKeys, NS = Sh::kSlots, NB = Sh::kAhead, CW = D / 8;  // CW: 16-byte chunks of a row
     constexpr int NR = F8 ? Sh::kRaw : NS;                    // slots that TMA fills
     extern __shared__ char smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[F8 ? NR : 1];
-    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
+    __shared__ __align__(8) uint64_t s_full[NB], p_full[NB], o_done[2], q_full, q_empty, drain;
     __shared__ __align__(8) uint64_t unit_full[kTcUnits], unit_empty[kTcUnits];
     __shared__ __align__(16) Unit s_units[kTcUnits];
     __shared__ uint32_t s_tmem;
@@ -485,11 +485,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&raw_full[i], 1);
             if (F8) mbar_init(&raw_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
-            mbar_init(&o_done[i], 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
         mbar_init(&q_full, 4);
         for (int i = 0; i < kTcUnits; ++i) {
             mbar_init(&unit_full[i], 1);
@@ -520,75 +520,73 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fewer_registers<88>();
     if (warp == 12 || warp == 14) {
         // --------------------------------- TMA: K by warp 14, V by warp 12
-        const bool mine_v = warp == 12;
-        const bool boxed = lane < KT / tc.box;  // the lane has a box of each tile
-        uint32_t item = 0, issued = 0;
-        int u = 0;
+        // The warp's lanes are the boxes of a group of tiles, whose pages are read
+        // while those of the group before are used: the table's round trip would
+        // otherwise be the rate of the tiles.
+        const bool is_v = warp == 12;
+        const int boxes = KT >> tc.shift, group = 32 / boxes;  // boxes of a tile, tiles of a group
+        const int of = lane / boxes, row = (lane & (boxes - 1)) << tc.shift;  // the lane's tile and first row
+        const CUtensorMap* map = is_v ? &mv : &mk;
+        uint32_t before = 0, issued = 0;  // items of the units before, items issued
         Units w(s_units, unit_full, unit_empty, fail);
         while (w.next()) {
             const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
-            const int end = w.req.n + w.req.ell;
-            // the page of the lane's box of tile t; -1 if no row sees any of it
-            auto page_of = [&](int t) {
-                if (!boxed || t >= w.nt) return -1;
-                const int k = tile_key<KT>(w.req, w.t0 + t) + (lane << tc.shift);
+            const int end = w.req.n + w.req.ell, first = min(NB, w.nt);
+            int page = 0, token = 0, page1 = 0, token1 = 0;
+            bool need = false, need1 = false;  // some row sees some of the box
+            auto fetch = [&](int t) {
+                need1 = t < w.nt;
+                if (!need1) return;
+                const int k = tile_key<KT>(w.req, w.t0 + t) + row;
                 const int last = min(k + tc.box - 1, end);
-                const bool need = k <= end && (a.window == 0 || w.req.n - last < a.window || k < a.sinks);
-                if (!need) return -1;
-                const int page = pages[c.by_page.div((uint32_t)k)];
-                return page < 0 || page >= c.pages ? -2 : page;
+                need1 = k <= end && (a.window == 0 || w.req.n - last < a.window || k < a.sinks);
+                if (!need1) return;
+                const int p = (int)c.by_page.div((uint32_t)k);
+                token1 = k - p * c.page_size;
+                page1 = pages[p];
             };
-            auto put = [&](bool is_v, int t, int page) {
-                const int key0 = tile_key<KT>(w.req, w.t0 + t);
-                if (page == -2) atomicOr(&s_flags[u % kTcUnits], 1);
-                const int k = key0 + (lane << tc.shift);
-                const int token = k - (int)c.by_page.div((uint32_t)k) * c.page_size;
+            fetch(of);
+#pragma unroll 1
+            for (int t = 0; t < w.nt; ++t) {
+                if ((t & (group - 1)) == 0) {
+                    page = page1;
+                    token = token1;
+                    need = need1;
+                    fetch(t + group + of);
+                }
+                // the tile's place in the order of the items
+                const uint32_t item =
+                    before + (is_v ? t < w.nt - first ? first + 2 * t : w.nt + t : t < first ? t : 2 * t - first + 1);
                 const int slot = (int)(item % NR);
+                bool have = need && of == (t & (group - 1));
+                if (have && (uint32_t)page >= (uint32_t)c.pages) {
+                    atomicOr(&s_flags[w.u % kTcUnits], 1);
+                    have = false;
+                }
                 uint64_t* freed = F8 ? &raw_empty[slot] : &empty[slot];
-                const bool ok =
-                    __all_sync(0xffffffffu, item < NR || tc_wait(freed, ((item / NR) & 1) ^ 1, fail));
+                const bool ok = __all_sync(0xffffffffu, item < NR || tc_wait(freed, ((item / NR) & 1) ^ 1, fail));
                 // a 16-bit tile is ready when it has landed, unless it is to be repaired
-                uint64_t* bar =
-                    F8 || (is_v && !all_see<KT>(a, w.req, key0)) ? &raw_full[slot] : &full[slot];
-                const bool have = ok && page >= 0;
+                uint64_t* bar = F8 || (is_v && !all_see<KT>(a, w.req, tile_key<KT>(w.req, w.t0 + t)))
+                                    ? &raw_full[slot]
+                                    : &full[slot];
+                have = have && ok;
                 const int n = __popc(__ballot_sync(0xffffffffu, have));
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * tc.box * (F8 ? D : 2 * D));
                 __syncwarp();
                 if (have) {
-                    const uint32_t row = (uint32_t)lane << tc.shift;
                     if (F8) {
-                        tma_box(raws + slot * Sh::kRawTile + row * D, is_v ? &mv : &mk, 0, token, w.h, page, bar);
+                        tma_box(raws + slot * Sh::kRawTile + row * D, map, 0, token, w.h, page, bar);
                     } else {
 #pragma unroll
                         for (int p = 0; p < D / 64; ++p)
-                            tma_box(ring + slot * Sh::kTile + p * Sh::kPanel + row * 128, is_v ? &mv : &mk, p * 64,
-                                    token, w.h, page, bar);
+                            tma_box(ring + slot * Sh::kTile + p * Sh::kPanel + row * 128, map, p * 64, token, w.h,
+                                    page, bar);
                     }
                 }
                 if (ok) issued = item + 1;
                 __syncwarp();
-            };
-            // K of tile i and V of tile i - 2, and the table three tiles ahead: its
-            // round trip would otherwise be the rate of the tiles
-            int p0 = -1, p1 = -1, p2 = page_of(0), p3 = page_of(1), p4 = page_of(2);
-#pragma unroll 1
-            for (int i = 0; i < w.nt + 2; ++i) {
-                const int p5 = page_of(i + 3);
-                if (i >= 2) {
-                    if (mine_v) put(true, i - 2, p0);
-                    ++item;
-                }
-                if (i < w.nt) {
-                    if (!mine_v) put(false, i, p2);
-                    ++item;
-                }
-                p0 = p1;
-                p1 = p2;
-                p2 = p3;
-                p3 = p4;
-                p4 = p5;
             }
-            ++u;
+            before += 2 * w.nt;
             w.done();
         }
         if (*fail) {  // copies under way land before the block ends: their time is far below the limit
@@ -655,7 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int i = 0; i < 2 * w.nt; ++i, ++item) {
                 bool is_v;
                 int t;
-                item_of(i, w.nt, is_v, t);
+                item_of<NB>(i, w.nt, is_v, t);
                 const int key0 = tile_key<KT>(w.req, w.t0 + t);
                 const bool cut = is_v && !all_see<KT>(a, w.req, key0);
                 if (!F8 && !cut) continue;
@@ -775,34 +773,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         constexpr uint32_t id_s = head | ((uint32_t)(KT >> 3) << 17);
         constexpr uint32_t id_o = head | ((uint32_t)(D >> 3) << 17) | (1u << 16);
         const uint32_t one = elect_one();
-        uint32_t item = 0, pn = 0;
+        uint32_t item = 0, first = 0;  // first: tiles of the units before
         Units w(s_units, unit_full, unit_empty, fail);
         while (w.next()) {
             tc_wait(&q_full, w.u & 1, fail);
             __syncwarp();
             tc_fence_after();
-            // S of tile i before O of tile i - 2, in the order of the items
+            // O of tile i - NB, then S of tile i in the columns that its weights leave
 #pragma unroll 1
-            for (int i = 0; i < w.nt + 2; ++i) {
-                const uint32_t s = i & 1;
-                if (i >= 2) {
-                    const uint32_t slot = item % NS;
+            for (int i = 0; i < w.nt + NB; ++i) {
+                if (i >= NB) {
+                    const uint32_t slot = item % NS, g = first + i - NB, s = (i - NB) & 1;
                     tc_wait(&full[slot], (item / NS) & 1, fail);
-                    tc_wait(&p_full[s], (pn >> s) & 1, fail);
-                    pn ^= 1u << s;
+                    tc_wait(&p_full[g % NB], (g / NB) & 1, fail);
                     __syncwarp();
                     tc_fence_after();
                     const uint64_t v = desc_mn(ring + slot * Sh::kTile, Sh::kPanel);
-                    const uint32_t from = tmem + s * KT, out = tmem + 2 * KT + s * D;
+                    const uint32_t from = tmem + (g % NB) * KT, out = tmem + NB * KT + s * D;
 #pragma unroll
                     for (int kk = 0; kk < KT / 16; ++kk)
-                        tc_mma_ts(one, out, from + kk * 8, v + kk * (2048 >> 4), id_o, i > 3 || kk > 0);
+                        tc_mma_ts(one, out, from + kk * 8, v + kk * (2048 >> 4), id_o, i >= NB + 2 || kk > 0);
                     tc_commit(one, &o_done[s]);
                     tc_commit(one, &empty[slot]);
                     ++item;
                 }
                 if (i < w.nt) {
-                    const uint32_t slot = item % NS;
+                    const uint32_t slot = item % NS, at = (first + i) % NB;
                     tc_wait(&full[slot], (item / NS) & 1, fail);
                     __syncwarp();
                     tc_fence_after();
@@ -810,14 +806,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * Sh::kPanel + (kk & 3) * 32) >> 4;
-                        tc_mma_ss(one, tmem + s * KT, q + off, k + off, id_s, kk > 0);
+                        tc_mma_ss(one, tmem + at * KT, q + off, k + off, id_s, kk > 0);
                     }
-                    tc_commit(one, &s_full[s]);
+                    tc_commit(one, &s_full[at]);
                     tc_commit(one, &empty[slot]);
                     if (i == w.nt - 1) tc_commit(one, &q_empty);
                     ++item;
                 }
             }
+            first += w.nt;
             w.done();
         }
         if (*fail) {
@@ -838,9 +835,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int s = warp >> 2;
         const int row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + s * KT, to = tmem + lanes + 2 * KT;
+        const uint32_t to = tmem + lanes + NB * KT;
         int4 open = make_int4(0, 0, 0, 0);
-        uint32_t seen = 0;  // tiles of the stream so far
+        uint32_t seen = 0, first = 0;  // tiles of the stream so far, tiles of the units before
         int u = 0;
         Units w(s_units, unit_full, unit_empty, fail);
         while (all_agree(1, 256, w.next())) {
@@ -849,7 +846,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float scale = fabsf(a.scale) * (F8 && c.k_scale ? fabsf(c.k_scale[w.h]) : 1.0f);
             float m = -INFINITY, l = 0.0f;
             for (int t = s; t < w.nt; t += 2) {
-                tc_wait(&s_full[s], seen & 1, fail);
+                const uint32_t g = first + t, ts = tmem + lanes + (g % NB) * KT;
+                tc_wait(&s_full[g % NB], (g / NB) & 1, fail);
                 __syncwarp();
                 tc_fence_after();
                 if (active) {
@@ -925,9 +923,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[s]);
+                if (lane == 0) mbar_arrive(&p_full[g % NB]);
                 ++seen;
             }
+            first += w.nt;
             if (s < w.nt) tc_wait(&o_done[s], (seen - 1) & 1, fail);
             if (s == 1) {
                 s_ml[0][row] = m;
