@@ -57,6 +57,9 @@ struct TcShape {
     static constexpr int kSlots = F8 ? (D == 64 ? 6 : 3) : (D == 64 ? 12 : 6);
     static constexpr int kRaw = F8 ? (D == 64 ? 10 : 5) : 0;
     static constexpr int kQ = kTcRows * 128 * (D / 64);
+    // threads that widen or repair a tile: with slots enough for four tiles under
+    // way, each warp has its own
+    static constexpr int kWideners = F8 && kSlots >= 6 ? 32 : 64;
     static constexpr int kSmem = 1024 + kQ + kSlots * kTile + kRaw * kRawTile;
     // beside it, about 2 KB of barriers, units and weights have to fit 227 KB
     static_assert(kSmem + 2048 <= 227 * 1024, "shared memory of an SM");
@@ -240,12 +243,6 @@ __device__ __forceinline__ uint32_t panel_at(int row, int chunk) {  // byte of a
     return (uint32_t)((chunk >> 3) * (128 * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-template <typename T>
-__device__ __forceinline__ bool tc_nonfinite(uint32_t w, uint32_t half_mask) {
-    const uint32_t e = (std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u) & half_mask;
-    return (w & e) == e;
-}
-
 // Item i of a unit of nt tiles, in the order of use: K0, K1, V0, K2, V1, ... where
 // K is two tiles ahead.
 template <int AHEAD>
@@ -291,24 +288,45 @@ __device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Takes the values that are not finite out of eight 16-bit ones.
-template <typename T>
-__device__ __forceinline__ bool take_out(uint4& v) {
-    uint32_t e[4] = {v.x, v.y, v.z, v.w};
-    bool any = false;
+// Sets the values of a word that are not finite (two 16-bit or four e4m3 ones: all
+// bits of the exponent, or of all but the sign, set) to zero.  Adding the lowest of
+// these bits carries into the sign's place, and no further.
+template <typename T, bool F8>
+__device__ __forceinline__ uint32_t finite_of(uint32_t w) {
+    constexpr uint32_t bits = F8 ? 0x7f7f7f7fu : std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    constexpr uint32_t low = F8 ? 0x01010101u : std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+    const uint32_t m = ((w & bits) + low) & (F8 ? 0x80808080u : 0x80008000u);
+    return w & ~(F8 ? (m >> 7) * 0xffu : (m >> 15) * 0xffffu);
+}
+
+// Rows of a V tile in shared memory, `n` 16-byte chunks of this thread: chunk i is
+// of key key0 + row(i), at at(i).  What no query row sees becomes zero, and so do
+// values that are not finite where not every query row sees them; true if there
+// were such.
+template <typename T, bool F8, typename Row, typename At>
+__device__ __forceinline__ bool repair(const AttendArgs& a, const Request& req, int key0, int n, Row row, At at) {
+    bool dirty = false;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 4) {
+        uint4 v[4];
 #pragma unroll
-    for (int z = 0; z < 4; ++z) {
-        if (tc_nonfinite<T>(e[z], 0xffffu)) {
-            e[z] &= 0xffff0000u;
-            any = true;
-        }
-        if (tc_nonfinite<T>(e[z], 0xffff0000u)) {
-            e[z] &= 0xffffu;
-            any = true;
+        for (int q = 0; q < 4; ++q) v[q] = lds16(at(i0 + q));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int t = key0 + row(i0 + q);
+            const bool some = any_sees(a, req, t);
+            uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            if (some)
+                z = make_uint4(finite_of<T, F8>(v[q].x), finite_of<T, F8>(v[q].y), finite_of<T, F8>(v[q].z),
+                               finite_of<T, F8>(v[q].w));
+            const bool other = z.x != v[q].x || z.y != v[q].y || z.z != v[q].z || z.w != v[q].w;
+            if (other && !sees_all(a, req, t)) {
+                sts16(at(i0 + q), z);
+                dirty = dirty || some;
+            }
         }
     }
-    v = make_uint4(e[0], e[1], e[2], e[3]);
-    return any;
+    return dirty;
 }
 
 // Two fp32 operations of one instruction.
@@ -595,8 +613,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp >= 8 && warp < 12) {
         // ------------------------------------- repair of V, or widening of K and V
-        // two pairs of warps take the items in turn
-        const int pair = (warp - 8) >> 1, lt = tid & 63;
+        // warps, or pairs of warps, take the items in turn
+        constexpr int WT = Sh::kWideners, TEAMS = 128 / WT;
+        const int team = (tid & 127) / WT, lt = tid % WT;
+        auto meet = [&] {
+            __syncwarp();
+            if (WT > 32) asm volatile("bar.sync %0, 64;" ::"r"(3 + team) : "memory");
+        };
         uint32_t item = 0, turns = 0;  // turns: phases of raw_full by slot (16-bit cache)
         int u = 0;
         Units w(s_units, unit_full, unit_empty, fail);
@@ -658,7 +681,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool cut = is_v && !all_see<KT>(a, w.req, key0);
                 if (!F8 && !cut) continue;
                 const int slot = (int)(item % NS);
-                if ((int)(item & 1) != pair) {
+                if ((int)(item % TEAMS) != team) {
                     turns ^= 1u << slot;
                     continue;
                 }
@@ -667,17 +690,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (F8) {
                     const int rs = (int)(item % NR);
                     tc_wait(&raw_full[rs], (item / NR) & 1, fail);
-                    if (item >= NS) tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail);
                     const uint32_t from = raws + rs * Sh::kRawTile;
-                    constexpr int STEP = 64 / (D / 16), N = KT / STEP;  // rows of a step, steps
+                    constexpr int STEP = WT / (D / 16), N = KT / STEP, IN = 8;  // rows of a step, steps, loads in flight
+                    if (cut)  // each thread's own chunks, as below
+                        dirty = repair<T, true>(
+                            a, w.req, key0, N, [&](int i) { return lt / (D / 16) + i * STEP; },
+                            [&](int i) { return from + (lt + i * WT) * 16; });
+                    if (item >= NS) tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail);
                     const int ch = lt % (D / 16), k0 = lt / (D / 16);
 #pragma unroll 1
-                    for (int i0 = 0; i0 < N; i0 += 4) {
-                        uint4 v[4];
+                    for (int i0 = 0; i0 < N; i0 += IN) {
+                        uint4 v[IN];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = lds16(from + (lt + (i0 + q) * 64) * 16);
+                        for (int q = 0; q < IN; ++q) v[q] = lds16(from + (lt + (i0 + q) * WT) * 16);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < IN; ++q) {
                             const uint32_t at = to + panel_at(k0 + (i0 + q) * STEP, 2 * ch);
                             uint4 lo, hi;
                             tc_widen(v[q].x, lo.x, lo.y);
@@ -688,43 +715,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             sts16(at ^ 16, hi);  // the chunk beside it, in the swizzle too
                         }
                     }
-                    if (cut) {  // the thread's own chunks again
-#pragma unroll 1
-                        for (int i = 0; i < 2 * N; ++i) {
-                            const int k = k0 + (i >> 1) * STEP;
-                            if (sees_all(a, w.req, key0 + k)) continue;
-                            const uint32_t at = (to + panel_at(k, 2 * ch)) ^ ((i & 1) * 16);
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (any_sees(a, w.req, key0 + k)) {
-                                v = lds16(at);
-                                if (!take_out<T>(v)) continue;
-                                dirty = true;
-                            }
-                            sts16(at, v);
-                        }
-                    }
                     fence_proxy_async_smem();
-                    __syncwarp();
-                    asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
+                    meet();
                     if (lt == 0) mbar_arrive(&raw_empty[rs]);
                 } else {
                     tc_wait(&raw_full[slot], (turns >> slot) & 1, fail);
                     turns ^= 1u << slot;
-                    for (int x = lt; x < KT * CW; x += 64) {
-                        const int k = x / CW, ch = x - k * CW;
-                        if (sees_all(a, w.req, key0 + k)) continue;
-                        const uint32_t at = to + panel_at(k, ch);
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (any_sees(a, w.req, key0 + k)) {
-                            v = lds16(at);
-                            if (!take_out<T>(v)) continue;
-                            dirty = true;
-                        }
-                        sts16(at, v);
-                    }
+                    constexpr int STEP = WT / CW;
+                    const int k0 = lt / CW, ch = lt % CW;
+                    dirty = repair<T, false>(
+                        a, w.req, key0, KT / STEP, [&](int i) { return k0 + i * STEP; },
+                        [&](int i) { return to + panel_at(k0 + i * STEP, ch); });
                     fence_proxy_async_smem();
-                    __syncwarp();
-                    asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
+                    meet();
                 }
                 if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);
                 __syncwarp();
