@@ -330,34 +330,44 @@ __device__ __forceinline__ bool repair(const AttendArgs& a, const Request& req, 
 }
 
 // Two fp32 operations of one instruction.
-__device__ __forceinline__ void fma2(float& x, float& y, float b, float c) {
-    asm("{.reg .b64 v, w, z; mov.b64 v, {%0, %1}; mov.b64 w, {%2, %2}; mov.b64 z, {%3, %3}; fma.rn.f32x2 v, v, w, z; "
-        "mov.b64 {%0, %1}, v;}"
-        : "+f"(x), "+f"(y)
-        : "f"(b), "f"(c));
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-    asm("{.reg .b64 v, w; mov.b64 v, {%0, %1}; mov.b64 w, {%2, %3}; add.rn.f32x2 v, v, w; mov.b64 {%0, %1}, v;}"
-        : "+f"(x), "+f"(y)
-        : "f"(a), "f"(b));
+__device__ __forceinline__ float2 of_two(Two v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
-// The weights of 32 scores: their sums, and rounded to T into 16 columns.
+// The weights of 32 scores: their sums (four, so that few additions wait for one
+// another), and rounded to T into 16 columns.
 template <typename T>
-__device__ __forceinline__ void weigh(float (&x)[32], float scale, float ref, uint32_t see, bool cut, float& sum0,
-                                      float& sum1, uint32_t to) {
+__device__ __forceinline__ void weigh(float (&x)[32], Two scale, Two ref, Two& sum0, Two& sum1, uint32_t to) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], scale, -ref);
-    if (cut) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (!((see >> e) & 1u)) x[e] = -INFINITY;
+    for (int e = 0; e < 32; e += 2) {
+        const float2 v = of_two(fma2(two(x[e], x[e + 1]), scale, ref));
+        x[e] = v.x;
+        x[e + 1] = v.y;
     }
     uint32_t p[16];
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         const float v0 = ex2_approx(x[e]), v1 = ex2_approx(x[e + 1]);
-        add2(sum0, sum1, v0, v1);
+        Two& sum = e & 2 ? sum1 : sum0;
+        sum = add2(sum, two(v0, v1));
         p[e >> 1] = tc_pack<T>(v0, v1);
     }
     tc_st16(to, p);
@@ -856,34 +866,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (active) {
                     if (!std::is_same<T, O>::value && t == s) scale *= s_row[u & 1][row];
                     const int key0 = tile_key<KT>(w.req, w.t0 + t);
-                    const bool cut = !all_see<KT>(a, w.req, key0);
+                    float by = scale;
                     // The loops over 32 columns stay loops: the roles' code together has
                     // to fit the instruction cache (unrolled, they were 2.5 times slower)
                     float x[32], y[32], top = -INFINITY, top1 = -INFINITY;
+                    if (!all_see<KT>(a, w.req, key0)) {
+                        // scores that the row does not see, in a pass of its own: a tile
+                        // that a border cuts is rare, and this code cold.  The others are
+                        // scaled here (at a scale of zero, infinity times it is no number)
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            tc_ld32(x, ts + q * 32);
+                            tc_wait32(x);
+                            const uint32_t see = seen_bits(a, pos, key0 + q * 32);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = (see >> e) & 1u ? x[e] * scale : -INFINITY;
+                            tc_st32(ts + q * 32, x);
+                        }
+                        tc_wait_st();
+                        by = 1.0f;
+                    }
 #pragma unroll 1
                     for (int q = 0; q < 4; q += 2) {
                         tc_ld32(x, ts + q * 32);
                         tc_ld32(y, ts + q * 32 + 32);
                         tc_wait32(x);
                         tc_wait32(y);
-                        if (cut) {
-                            const uint32_t see = seen_bits(a, pos, key0 + q * 32);
-                            const uint32_t see1 = seen_bits(a, pos, key0 + q * 32 + 32);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (!((see >> e) & 1u)) x[e] = -INFINITY;
-                                if (!((see1 >> e) & 1u)) y[e] = -INFINITY;
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            top = fmaxf(top, x[e]);
-                            top1 = fmaxf(top1, y[e]);
+                        for (int e = 0; e < 32; e += 2) {
+                            top = fmaxf(top, fmaxf(x[e], x[e + 1]));
+                            top1 = fmaxf(top1, fmaxf(y[e], y[e + 1]));
                         }
                     }
                     top = fmaxf(top, top1);
                     // nothing seen stays below everything, at a scale of zero too
-                    if (top != -INFINITY) top *= scale;
+                    if (top != -INFINITY) top *= by;
                     const bool up = top > m + kTcSlack;
                     if (__any_sync(0xffffffffu, up)) {
                         const float now = up ? top : m;
@@ -908,20 +925,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // product they are rounded to T, 2^-9 (bf16) or 2^-12 of
                     // each at most, as much as the output's own rounding
                     const float ref = m == -INFINITY ? 0.0f : m;
-                    float sum0 = 0.0f, sum1 = 0.0f;
+                    const Two by2 = two(by, by), ref2 = two(-ref, -ref);
+                    Two sum0 = two(0.0f, 0.0f), sum1 = sum0;
                     tc_ld32(x, ts);
 #pragma unroll 1
                     for (int q = 0; q < 4; q += 2) {
                         tc_ld32(y, ts + q * 32 + 32);
                         tc_wait32(x);
-                        const uint32_t see = cut ? seen_bits(a, pos, key0 + q * 32) : 0xffffffffu;
-                        weigh<T>(x, scale, ref, see, cut, sum0, sum1, ts + q * 16);
+                        weigh<T>(x, by2, ref2, sum0, sum1, ts + q * 16);
                         tc_wait32(y);
                         if (q == 0) tc_ld32(x, ts + 64);  // columns that the weights do not reach yet
-                        const uint32_t see1 = cut ? seen_bits(a, pos, key0 + q * 32 + 32) : 0xffffffffu;
-                        weigh<T>(y, scale, ref, see1, cut, sum0, sum1, ts + q * 16 + 16);
+                        weigh<T>(y, by2, ref2, sum0, sum1, ts + q * 16 + 16);
                     }
-                    l += sum0 + sum1;
+                    const float2 sums = of_two(add2(sum0, sum1));
+                    l += sums.x + sums.y;
                     tc_wait_st();
                 }
                 tc_fence_before();
