@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 #include "specv_trace.h"
 
 namespace specv {
@@ -188,6 +190,7 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
     a.B = B;
     a.gamma = gamma;
     a.max_pages = max_pages;
+    a.limit = (int)std::min((long long)max_pages * c.page_size, 0x7fffffc0ll);
     a.window = window;
     a.sinks = sinks;
     a.scale = scale * 1.4426950408889634f;  // log2(e)
@@ -200,6 +203,8 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
                          : tc           ? attend_tc_plan(sms)
                                         : attend_mma_plan(most, c.head_dim, cache->dt == SPEC_E4M3, sms);
     a.tile_rows = p.tile_rows;
+    a.tile_shift = 0;
+    while ((1 << a.tile_shift) < p.tile_rows) ++a.tile_shift;
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
     a.lead = tc ? 3 : 2;
     // a part costs the joining kernel about 0.2 us a row, a tile its block 0.45 us

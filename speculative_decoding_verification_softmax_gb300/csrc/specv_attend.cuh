@@ -24,7 +24,9 @@ struct AttendArgs {
     long long part_floats;
     int q_heads, group, rows, B, gamma, max_pages;
     int window, sinks;
-    int tile_rows;    // rows of a unit at most
+    int tile_rows;    // rows of a unit at most, 2^tile_shift
+    int tile_shift;
+    int limit;        // positions of a request: pages of the table, and below 2^31
     int lead;         // what a unit costs beside its tiles, in tiles
     float part_cost;  // of a part when joined, in tiles
     float scale;      // of the scores, to base 2
@@ -57,17 +59,17 @@ __device__ __forceinline__ Request request_of(const AttendArgs& a, const CacheVi
     r.code = SPEC_OK;
     if (r.ell < 0 || r.ell > a.gamma) r.code = SPEC_ERR_VERIFY_LEN;
     else if (r.base < 0 || r.base > a.rows - r.ell - 1) r.code = SPEC_ERR_ROW_INDEX;
-    else if (r.n < 0 || (long long)r.n + r.ell >= min((long long)a.max_pages * c.page_size, 0x7fffffc0ll))
+    else if (r.n < 0 || r.n >= a.limit - r.ell)
         r.code = SPEC_ERR_CACHE_LEN;
     if (r.code != SPEC_OK) return r;
-    const int last = (r.n + r.ell) / KT + 1;
+    const int last = (int)((uint32_t)(r.n + r.ell) / KT) + 1;
     if (a.window > 0) {
         const int first = max(0, r.n - a.window + 1);
-        r.first_tile = first / KT;
-        r.sink_tiles = min((int)(((long long)a.sinks + KT - 1) / KT), r.first_tile);
+        r.first_tile = (int)((uint32_t)first / KT);
+        r.sink_tiles = min((int)(((uint32_t)a.sinks + KT - 1) / KT), r.first_tile);
     }
     r.tiles = r.sink_tiles + last - r.first_tile;
-    r.row_tiles = ((r.ell + 1) * a.group + a.tile_rows - 1) / a.tile_rows;
+    r.row_tiles = ((r.ell + 1) * a.group + a.tile_rows - 1) >> a.tile_shift;
     r.units = r.row_tiles * c.kv_heads;
     return r;
 }
@@ -94,25 +96,37 @@ __device__ __forceinline__ bool all_see(const AttendArgs& a, const Request& r, i
 }
 
 struct Run {
-    int b;           // request of the run's first tile
-    int longest;     // tiles of the longest unit
+    Request req;     // of the run's first tile
+    int b;
     long long at;    // tile within the request (unit-major, leads included)
     long long left;  // tiles of the run
     long long step;  // tiles of every block's run
 };
 
-// The block's run.  All threads call it; s_scan [THREADS / 32 + 1] and s_run
-// are shared.
+template <int THREADS>
+struct RunShared {
+    long long sum[THREADS / 32];
+    int longest[THREADS / 32];
+    Run run;
+};
+
+// n / d; the 64-bit division is long, and its case rare.
+__device__ __forceinline__ long long quotient(long long n, uint32_t d) {
+    return n >> 32 ? n / (long long)d : (long long)((uint32_t)n / d);
+}
+
+// The block's run, in s.run.  All threads call it.
 template <int KT, int THREADS>
-__device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, long long* s_scan, Run* s_run) {
+__device__ __forceinline__ void run_of(const AttendArgs& a, const CacheView& c, RunShared<THREADS>& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = tid * per, b1 = min(a.B, b0 + per);
     long long mine = 0;
     int longest = 0;
+    Request r = {};
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-        const Request r = request_of<KT>(a, c, b);
+        r = request_of<KT>(a, c, b);
         mine += (long long)r.units * (r.tiles + a.lead);
         longest = max(longest, r.tiles);
     }
@@ -123,44 +137,43 @@ __device__ __forceinline__ Run run_of(const AttendArgs& a, const CacheView& c, l
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) s_scan[warp] = x;
-    if (tid == 0) {
-        s_run->left = 0;
-        s_run->longest = 0;
+    if (lane == 31) {
+        s.sum[warp] = x;
+        s.longest[warp] = longest;
     }
+    if (tid == 0) s.run.left = 0;
     __syncthreads();
-    if (lane == 0) atomicMax(&s_run->longest, longest);
     long long before = x - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        const long long s = s_scan[w];
-        if (w < warp) before += s;
-        total += s;
+        const long long y = s.sum[w];
+        if (w < warp) before += y;
+        total += y;
+        longest = max(longest, s.longest[w]);
     }
-    __syncthreads();
     // few long units are not cut into more parts than joining them is worth
-    longest = s_run->longest;
     const int least = max(2, (int)sqrtf(a.part_cost * (float)longest));
-    const long long step = max((total + gridDim.x - 1) / gridDim.x, (long long)least);
+    const long long step = max(quotient(total + gridDim.x - 1, gridDim.x), (long long)least);
     const long long start = (long long)blockIdx.x * step;
     if (start >= before && start < before + mine) {
         long long at = start - before;
+        int b = b0;
+        if (per > 1) {
 #pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const Request r = request_of<KT>(a, c, b);
-            const long long w = (long long)r.units * (r.tiles + a.lead);
-            if (at < w) {
-                s_run->b = b;
-                s_run->at = at;
-                s_run->left = min(step, total - start);
-                s_run->step = step;
-                break;
+            for (;; ++b) {
+                r = request_of<KT>(a, c, b);
+                const long long w = (long long)r.units * (r.tiles + a.lead);
+                if (at < w) break;
+                at -= w;
             }
-            at -= w;
         }
+        s.run.req = r;
+        s.run.b = b;
+        s.run.at = at;
+        s.run.left = min(step, total - start);
+        s.run.step = step;
     }
     __syncthreads();
-    return *s_run;
 }
 
 __device__ __forceinline__ int4 open_of(int parts, int base, int r0, int R, int h) {
@@ -182,8 +195,8 @@ struct Walk {
         step = run.step;
         unit = place = 0;
         if (left > 0) {
-            req = request_of<KT>(a, c, b);
-            unit = (int)(run.at / (req.tiles + a.lead));
+            req = run.req;
+            unit = (int)quotient(run.at, (uint32_t)(req.tiles + a.lead));
             place = (int)(run.at - (long long)unit * (req.tiles + a.lead));
         }
     }
@@ -215,7 +228,9 @@ struct Walk {
     // block with tile 0 says how many there are.
     __device__ __forceinline__ bool whole() const { return nt == req.tiles; }
     __device__ __forceinline__ int4 open() const {
-        return open_of(1 + (int)((req.tiles - nt + step - 1) / step), req.base, r0, R, h);
+        const int rest = req.tiles - nt;
+        const int parts = rest <= step ? rest > 0 : (int)((uint32_t)(rest - 1) / (uint32_t)step) + 1;
+        return open_of(1 + parts, req.base, r0, R, h);
     }
 };
 

@@ -141,8 +141,7 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
     constexpr int CK = KW < 32 ? KW : 32;     // keys of a softmax step
     constexpr int RG = THREADS / CH, RP = KT / RG;  // loads: row groups, adjacent rows of a thread
     extern __shared__ __align__(128) char smem[];
-    __shared__ long long s_scan[THREADS / 32 + 1];
-    __shared__ Run s_run;
+    __shared__ RunShared<THREADS> s_run;
     __shared__ float s_m[WK][Sh::kRows], s_l[WK][Sh::kRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wr = warp % WR, wk = warp / WR;
@@ -152,12 +151,12 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
 
     pdl_trigger();
     pdl_wait();
-    run_of<KT, THREADS>(a, c, s_scan, &s_run);
+    run_of<KT>(a, c, s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
     const bool has_chunk = lch * 16 < dim * (F8 ? 1 : 2);
     const bool by_group = c.page_size % RP == 0;  // a thread's rows share a page
-    Walk<KT> w(a, c, s_run);
+    Walk<KT> w(a, c, s_run.run);
     while (w.next(a, c)) {
         const Request& req = w.req;
         const int t0 = w.t0, nt = w.nt, h = w.h, r0 = w.r0, R = w.R;

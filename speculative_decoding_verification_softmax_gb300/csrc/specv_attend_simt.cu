@@ -32,18 +32,17 @@ __global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(At
     float* s_v = s_k + KT * (D + 4);        // [64][D]
     float* s_p = s_v + KT * D;              // [64][20]: scores, then weights, by key
     __shared__ float s_corr[kSimtRows], s_l[kSimtRows], s_m[kSimtRows];
-    __shared__ long long s_scan[kSimtThreads / 32 + 1];
-    __shared__ Run s_run;
+    __shared__ RunShared<kSimtThreads> s_run;
     const int tid = threadIdx.x;
     const int col = tid & 63, rg = tid >> 6;     // products: a key or column, and 4 rows
     const int srow = tid >> 4, slane = tid & 15;  // softmax: 16 threads a row
 
     pdl_trigger();
     pdl_wait();
-    run_of<KT, kSimtThreads>(a, c, s_scan, &s_run);
+    run_of<KT>(a, c, s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
-    Walk<KT> w(a, c, s_run);
+    Walk<KT> w(a, c, s_run.run);
     while (w.next(a, c)) {
         const Request& req = w.req;
         const int t0 = w.t0, nt = w.nt, h = w.h, r0 = w.r0, R = w.R;

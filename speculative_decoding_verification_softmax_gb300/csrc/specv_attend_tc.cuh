@@ -252,10 +252,6 @@ __device__ __forceinline__ void item_of(int i, int nt, bool& is_v, int& t) {
     t = x < 0 ? i : x >= pairs ? nt - first + (x - pairs) : is_v ? x >> 1 : (x >> 1) + first;
 }
 
-__device__ __forceinline__ bool sees_all(const AttendArgs& a, const Request& r, int t) {
-    return t <= r.n && (a.window == 0 || r.n + r.ell - t < a.window || t < a.sinks);
-}
-
 // Bits lo .. hi - 1 of a word, for any lo and hi.
 __device__ __forceinline__ uint32_t bits_of(int lo, int hi) {
     lo = max(lo, 0);
@@ -299,31 +295,41 @@ __device__ __forceinline__ uint32_t finite_of(uint32_t w) {
     return w & ~(F8 ? (m >> 7) * 0xffu : (m >> 15) * 0xffffu);
 }
 
-// Rows of a V tile in shared memory, `n` 16-byte chunks of this thread: chunk i is
-// of key key0 + row(i), at at(i).  What no query row sees becomes zero, and so do
-// values that are not finite where not every query row sees them; true if there
-// were such.
-template <typename T, bool F8, typename Row, typename At>
-__device__ __forceinline__ bool repair(const AttendArgs& a, const Request& req, int key0, int n, Row row, At at) {
+// The part of a V tile from key key0 on that a thread has in shared memory: of the
+// rows k, k + STEP, ... 16 bytes each, at at(row).  What no query row sees becomes
+// zero, and so do values that are not finite where only some see them; true if
+// there were such.  Short loops over just these rows: the tile waits for them.
+template <typename T, bool F8, int KT, int STEP, typename At>
+__device__ __forceinline__ bool repair(const AttendArgs& a, const Request& req, int key0, int k, At at) {
+    const int end = req.n + req.ell;
     bool dirty = false;
+    // behind the end, and between the sinks and the window; then what only some of
+    // the rows see: their own positions, and the first ones of their windows
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 4) {
-        uint4 v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = lds16(at(i0 + q));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int t = key0 + row(i0 + q);
-            const bool some = any_sees(a, req, t);
+    for (int i = 0; i < (a.window > 0 ? 4 : 2); ++i) {
+        const bool some = i & 1;
+        int from, to;  // in the tile
+        if (i < 2) {
+            from = (some ? req.n : end) + 1 - key0;
+            to = some ? end + 1 - key0 : KT;
+        } else {
+            from = max(a.sinks, some ? req.n - a.window + 1 : 0) - key0;
+            to = max((some ? end : req.n) - a.window + 1, 0) - key0;
+        }
+        from = max(from, 0);
+        to = min(to, KT);
+        from += (k - from) & (STEP - 1);  // the thread's first row from there on
+#pragma unroll 1
+        for (int r = from; r < to; r += STEP) {
             uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            if (some)
-                z = make_uint4(finite_of<T, F8>(v[q].x), finite_of<T, F8>(v[q].y), finite_of<T, F8>(v[q].z),
-                               finite_of<T, F8>(v[q].w));
-            const bool other = z.x != v[q].x || z.y != v[q].y || z.z != v[q].z || z.w != v[q].w;
-            if (other && !sees_all(a, req, t)) {
-                sts16(at(i0 + q), z);
-                dirty = dirty || some;
+            if (some) {
+                const uint4 v = lds16(at(r));
+                z = make_uint4(finite_of<T, F8>(v.x), finite_of<T, F8>(v.y), finite_of<T, F8>(v.z),
+                               finite_of<T, F8>(v.w));
+                if (z.x == v.x && z.y == v.y && z.z == v.z && z.w == v.w) continue;
+                dirty = true;
             }
+            sts16(at(r), z);
         }
     }
     return dirty;
@@ -496,9 +502,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __shared__ __align__(16) Unit s_units[kTcUnits];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail, s_flags[kTcUnits];
-    __shared__ long long s_scan[kTcThreads / 32 + 1];
-    __shared__ Run s_run;
-    __shared__ float s_ml[2][kTcRows];
+    // the run, until warp 13 has read it; then (a unit has come from it and ended)
+    // the second stream's maxima and sums, the streams' weights
+    __shared__ union {
+        RunShared<kTcThreads> run;
+        float ml[2][kTcRows];
+    } s_of;
+    auto& s_ml = s_of.ml;
     __shared__ float s_row[2][std::is_same<T, O>::value ? 1 : kTcRows];  // scales of two units' query rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
@@ -534,7 +544,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_wait();
     if (warp == 15) tc_alloc(&s_tmem, Sh::kCols);
     tc_fence_before();
-    run_of<KT, kTcThreads>(a, c, s_scan, &s_run);  // also the barrier behind the set-up
+    run_of<KT>(a, c, s_of.run);  // also the barrier behind the set-up
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = s_tmem;
@@ -703,9 +713,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t from = raws + rs * Sh::kRawTile;
                     constexpr int STEP = WT / (D / 16), N = KT / STEP, IN = 8;  // rows of a step, steps, loads in flight
                     if (cut)  // each thread's own chunks, as below
-                        dirty = repair<T, true>(
-                            a, w.req, key0, N, [&](int i) { return lt / (D / 16) + i * STEP; },
-                            [&](int i) { return from + (lt + i * WT) * 16; });
+                        dirty = repair<T, true, KT, STEP>(a, w.req, key0, lt / (D / 16), [&](int r) {
+                            return from + (uint32_t)(r * D + lt % (D / 16) * 16);
+                        });
                     if (item >= NS) tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail);
                     const int ch = lt % (D / 16), k0 = lt / (D / 16);
 #pragma unroll 1
@@ -732,10 +742,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_wait(&raw_full[slot], (turns >> slot) & 1, fail);
                     turns ^= 1u << slot;
                     constexpr int STEP = WT / CW;
-                    const int k0 = lt / CW, ch = lt % CW;
-                    dirty = repair<T, false>(
-                        a, w.req, key0, KT / STEP, [&](int i) { return k0 + i * STEP; },
-                        [&](int i) { return to + panel_at(k0 + i * STEP, ch); });
+                    dirty = repair<T, false, KT, STEP>(a, w.req, key0, lt / CW,
+                                                       [&](int r) { return to + panel_at(r, lt % CW); });
                     fence_proxy_async_smem();
                     meet();
                 }
@@ -748,7 +756,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp == 13) {
         // -------------------------------------------------------------- units
-        Walk<KT> w(a, c, s_run);
+        Walk<KT> w(a, c, s_of.run.run);
         for (int u = 0;; ++u) {
             const bool more = w.next(a, c);
             const int at = u % kTcUnits;
@@ -927,15 +935,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float ref = m == -INFINITY ? 0.0f : m;
                     const Two by2 = two(by, by), ref2 = two(-ref, -ref);
                     Two sum0 = two(0.0f, 0.0f), sum1 = sum0;
-                    tc_ld32(x, ts);
 #pragma unroll 1
-                    for (int q = 0; q < 4; q += 2) {
-                        tc_ld32(y, ts + q * 32 + 32);
+                    for (int q = 0; q < 4; ++q) {
+                        tc_ld32(x, ts + q * 32);
                         tc_wait32(x);
                         weigh<T>(x, by2, ref2, sum0, sum1, ts + q * 16);
-                        tc_wait32(y);
-                        if (q == 0) tc_ld32(x, ts + 64);  // columns that the weights do not reach yet
-                        weigh<T>(y, by2, ref2, sum0, sum1, ts + q * 16 + 16);
                     }
                     const float2 sums = of_two(add2(sum0, sum1));
                     l += sums.x + sums.y;
