@@ -60,6 +60,7 @@ struct TcShape {
     // threads that widen or repair a tile: with slots enough for four tiles under
     // way, each warp has its own
     static constexpr int kWideners = F8 && kSlots >= 6 ? 32 : 64;
+    static constexpr int kTeams = 128 / kWideners;
     static constexpr int kSmem = 1024 + kQ + kSlots * kTile + kRaw * kRawTile;
     // beside it, about 2 KB of barriers, units and weights have to fit 227 KB
     static_assert(kSmem + 2048 <= 227 * 1024, "shared memory of an SM");
@@ -68,6 +69,16 @@ struct TcShape {
     // one, for which heads of 64 leave room, lets a stream find its next scores
     // ready when it has handed over its weights.
     static constexpr int kAhead = D == 64 ? 3 : 2;
+    // A wait on a slot's parity passes at once while the slot is two uses behind, so
+    // whoever waits has to know that the use before is over.  A team of wideners
+    // knows it of items kSlots before its last one (the products take items in order),
+    // which is enough if there are no more teams than slots; a loader of what the
+    // wideners gave back before its own last item, which is up to kAhead + 1 items
+    // ago (2 within a unit): with two teams, its slot's own team among them.
+    static_assert(!F8 || kTeams <= kSlots, "slots of the wideners");
+    static_assert(F8 || kAhead + 1 <= kSlots, "slots of the loaders");
+    static_assert(!F8 || kRaw >= kSlots + kAhead + 1 || (kTeams == 2 && kAhead == 2 && kRaw >= kSlots + 2),
+                  "slots of the loaders");
     static constexpr int kCols = 512;  // TMEM columns: scores, O0, O1 (a power of two)
     static_assert(kAhead * kTcKeys + 2 * D <= kCols, "columns of TMEM");
 };
@@ -634,7 +645,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp >= 8 && warp < 12) {
         // ------------------------------------- repair of V, or widening of K and V
         // warps, or pairs of warps, take the items in turn
-        constexpr int WT = Sh::kWideners, TEAMS = 128 / WT;
+        constexpr int WT = Sh::kWideners, TEAMS = Sh::kTeams;
         const int team = (tid & 127) / WT, lt = tid % WT;
         auto meet = [&] {
             __syncwarp();
