@@ -294,3 +294,51 @@ def test_offsets_beyond_32_bits(sv):
     out, ws = sv.attend(case.q.cuda(), K, V, table.cuda(), torch.tensor(case.lens, dtype=torch.int32).cuda())
     assert sv.read_status(ws) == 0
     case.check(out)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp16", "e4m3"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 3)])
+def test_blocks_with_many_units_of_few_tiles(sv, dim, dtype, cache, window, sinks):
+    """Units of one to four tiles, several in a block, of 9 to 85 rows."""
+    B, gamma = 170, 16
+    lens = [(37 * i) % 131 + 128 * (i % 4) for i in range(B)]
+    ell = [(5 * i) % (gamma + 1) for i in range(B)]
+    _run(sv, Case(lens=lens, ell=ell, gamma=gamma, heads=10, kv_heads=2, dim=dim, dtype=dtype, cache=cache, page=16,
+                  window=window, sinks=sinks, packed=True, seed=31))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gamma", [4, 16])
+def test_e4m3_values_that_are_no_numbers_reach_only_the_rows_that_see_them(sv, dim, gamma):
+    base = dict(lens=[130, 9], ell=[gamma, gamma], gamma=gamma, heads=8, kv_heads=1, dim=dim, dtype="bf16", cache="e4m3",
+                page=16, window=40, sinks=2, seed=8)
+    clean, dirty = Case(**base), Case(**base)
+    nan = torch.tensor(float("nan")).to(torch.float8_e4m3fn)
+
+    def put(t, d):
+        dirty.v[int(dirty.table[0, t // 16]), t % 16, 0, d] = nan
+
+    put(130 + 2, 3)             # rows 0 and 1 do not see it
+    put(130 - 40 + 2, dim - 1)  # rows 0 and 1 alone see it
+    put(1, 20)                  # a sink: all rows see it
+    a, b = (x.call(sv)[0].float().cpu() for x in (clean, dirty))
+    assert torch.equal(a[1], b[1])
+    for j in range(gamma + 1):
+        hit = {20, 3} if j >= 2 else {20, dim - 1}
+        for d in range(dim):
+            if d in hit:
+                assert torch.isnan(b[0, j, :, d]).all(), (j, d)
+            else:
+                assert torch.equal(a[0, j, :, d], b[0, j, :, d]), (j, d)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scale_of_zero_and_masks(sv, cache, dim):
+    """All seen keys weigh the same, those that a border hides nothing."""
+    case = Case(lens=[300, 0, 126], ell=[16, 9, 3], gamma=16, heads=8, kv_heads=2, dim=dim, cache=cache, window=90, sinks=5,
+                seed=12)
+    out, ws = case.call(sv, scale=0.0, out=torch.zeros(case.q.shape, dtype=case.q.dtype, device="cuda"))
+    assert sv.read_status(ws) == 0
+    case.check(out, scale=0.0)
