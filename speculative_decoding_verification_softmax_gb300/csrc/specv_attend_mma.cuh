@@ -15,6 +15,12 @@
 // An e4m3 cache is widened to fp16 (exact) on the way from shared memory to the
 // operands: its keys' bytes are read 16 at a time in an order that the query rows
 // share, and its values are transposed as pairs of bytes.
+//
+// Measured: one token of 32 requests of 4096 to 32768 positions, 32/8 heads of 128,
+// bf16: 357 us for 2.40 GB, 6.7 TB/s (HBM).  Up to 16384 positions: bf16 212 us,
+// 6.5 TB/s; e4m3 126 us, 4.5 TB/s, where the widening's instructions are the bound;
+// heads of 256 579 us, 4.5 TB/s (one block an SM).  The tensor-core kernel takes 217
+// and 150 us for the first two of these.
 #pragma once
 
 #include <type_traits>

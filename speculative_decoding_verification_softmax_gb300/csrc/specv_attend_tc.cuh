@@ -8,13 +8,15 @@
 //
 // Two streams of key tiles (even and odd) run against one another: while the
 // four warps of one stream take the softmax of their scores, the tensor cores
-// work for the other.  Each stream has its own S and O columns in TMEM and its
-// own running maximum and sum; the unit's end joins them.  P overlays S.
+// work for the other.  Each stream has its own O columns in TMEM and its own
+// running maximum and sum; the unit's end joins them.  Scores have two places (three
+// for heads of 64, for which TMEM has room), taken by the tiles in turn; P overlays S.
 //   warps 0-3, 4-7   softmax of the even and odd tiles, a row a thread; the
 //                    unit's output
 //   warps 8-11       the next unit's query rows; 16-bit cache: repair of V tiles
 //                    that a border cuts; e4m3 cache: the widening of all tiles
-//                    to fp16 (exact)
+//                    to fp16 (exact; an item takes 700 to 1500 cycles, mostly latency,
+//                    so two pairs or four warps have one each under way)
 //   warp 13          the block's units, told to all others through a ring, so
 //                    that none waits for a request's lengths between two units
 //   warps 14, 12     K and V tiles by TMA, in the order of their use, through a
@@ -26,6 +28,13 @@
 // query row must not see whole (the cache's end, the window's edges), rows that
 // nobody sees become zero, and a value that is not finite is taken out and added
 // by itself to the rows that see it.
+//
+// Measured: 64 requests of 500 to 8192 positions, blocks of 16 drafts, 32/8 heads
+// of 128, bf16: 201 us for 1.22 GB, 6.1 TB/s (HBM; 10% go to the switches between
+// units).  19 requests of 16384 positions: 192 us, 6.7 TB/s; heads of 64 101 us,
+// 6.3 TB/s (127 with two places for scores).  e4m3 is bound by the softmax and the
+// widening instead: 105 us (heads of 64) and 142 us (128) there; ragged windows of
+// 4000, 28/4 heads of 64, pages of 16: 60 us for 116 MB.
 #pragma once
 
 #include <cuda.h>

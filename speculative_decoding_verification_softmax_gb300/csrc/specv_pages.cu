@@ -5,6 +5,12 @@
 // counts, so a result depends on the state alone (a stack of free pages would
 // be in the order in which blocks happened to push) and the pool stays dense
 // at its lower end.  The scan is 4 bytes a page: 1 MB for 262144 pages.
+//
+// Small calls are bound by their launches and chains of round trips: reserve and
+// commit for 1024 requests over 250,000 pages take 20 us together, for 16 requests
+// 11 us; a fork of 64 requests 20 us for the tables and 17 us for 122 MB of copied
+// tokens (7.2 TB/s, partly from L2).  Large copies are bound by HBM: compact moves
+// 0.6 GB of pages, 1.19 GB read and written, in 197 us, 6.0 TB/s.
 #include <cooperative_groups.h>
 
 #include <mutex>
