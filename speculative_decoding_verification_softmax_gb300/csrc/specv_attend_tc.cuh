@@ -629,7 +629,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     : &full[slot];
                 have = have && ok;
                 const int n = __popc(__ballot_sync(0xffffffffu, have));
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * tc.box * (F8 ? D : 2 * D));
+                // without its slot a tile is left out: an arrival on a barrier that waits for
+                // an earlier copy would be one too many
+                if (lane == 0 && ok) mbar_arrive_expect_tx(bar, (uint32_t)n * tc.box * (F8 ? D : 2 * D));
                 __syncwarp();
                 if (have) {
                     if (F8) {
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);
                 __syncwarp();
-                if (lt == 0) mbar_arrive(&full[slot]);
+                if (lt == 0 && (F8 || !*fail)) mbar_arrive(&full[slot]);  // 16 bits: see the loaders
             }
             ++u;
             w.done();
