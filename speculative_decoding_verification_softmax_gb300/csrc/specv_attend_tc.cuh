@@ -84,6 +84,10 @@ struct TcShape {
     // which is enough if there are no more teams than slots; a loader of what the
     // wideners gave back before its own last item, which is up to kAhead + 1 items
     // ago (2 within a unit): with two teams, its slot's own team among them.
+    // The same holds for o_done: a stream that scales its output at tile t waits for
+    // its product of tile t - 2, and knows that of t - 4 to be over from the scores of
+    // t, which follow the product of t - kAhead, or from the end of the unit before.
+    static_assert(kAhead <= 4, "phases of o_done");
     static_assert(!F8 || kTeams <= kSlots, "slots of the wideners");
     static_assert(F8 || kAhead + 1 <= kSlots, "slots of the loaders");
     static_assert(!F8 || kRaw >= kSlots + kAhead + 1 || (kTeams == 2 && kAhead == 2 && kRaw >= kSlots + 2),
@@ -517,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int NR = F8 ? Sh::kRaw : NS;                    // slots that TMA fills
     extern __shared__ char smem_raw[];
     __shared__ __align__(8) uint64_t full[NS], empty[NS], raw_full[NR], raw_empty[F8 ? NR : 1];
-    __shared__ __align__(8) uint64_t s_full[NB], p_full[NB], o_done[2], q_full, q_empty, drain;
+    __shared__ __align__(8) uint64_t s_full[NB], p_full[NB], o_done[2], o_all, q_full, q_empty, drain;
     __shared__ __align__(8) uint64_t unit_full[kTcUnits], unit_empty[kTcUnits];
     __shared__ __align__(16) Unit s_units[kTcUnits];
     __shared__ uint32_t s_tmem;
@@ -548,6 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&p_full[i], 4);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
+        mbar_init(&o_all, 1);
         mbar_init(&q_full, 4);
         for (int i = 0; i < kTcUnits; ++i) {
             mbar_init(&unit_full[i], 1);
@@ -857,6 +862,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ++item;
                 }
             }
+            tc_commit(one, &o_all);
             first += w.nt;
             w.done();
         }
@@ -937,7 +943,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const float corr = up ? ex2_approx(m - now) : 1.0f;
                         l *= corr;
                         m = now;
-                        if (t >= 2) {
+                        if (t >= 2) {  // see TcShape
                             tc_wait(&o_done[s], (seen - 1) & 1, fail);
                             __syncwarp();
                             tc_fence_after();
@@ -973,7 +979,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ++seen;
             }
             first += w.nt;
-            if (s < w.nt) tc_wait(&o_done[s], (seen - 1) & 1, fail);
+            // all products of the unit, by a barrier with one phase a unit.  The
+            // stream's own o_done would not do: three tiles ahead, the scores of its
+            // last tile say nothing of its product before, and while that one is not
+            // over the wait for the last one's parity passes at once
+            tc_wait(&o_all, u & 1, fail);
             if (s == 1) {
                 s_ml[0][row] = m;
                 s_ml[1][row] = l;
