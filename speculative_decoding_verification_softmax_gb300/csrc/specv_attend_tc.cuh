@@ -743,6 +743,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         dirty = repair<T, true, KT, STEP>(a, w.req, key0, lt / (D / 16), [&](int r) {
                             return from + (uint32_t)(r * D + lt % (D / 16) * 16);
                         });
+                    if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);  // before the team meets
                     if (item >= NS) tc_wait(&empty[slot], ((item / NS) & 1) ^ 1, fail);
                     const int ch = lt % (D / 16), k0 = lt / (D / 16);
 #pragma unroll 1
@@ -771,11 +772,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     constexpr int STEP = WT / CW;
                     dirty = repair<T, false, KT, STEP>(a, w.req, key0, lt / CW,
                                                        [&](int r) { return to + panel_at(r, lt % CW); });
+                    if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);
                     fence_proxy_async_smem();
                     meet();
                 }
-                if (dirty) atomicOr(&s_flags[u % kTcUnits], 2);
-                __syncwarp();
                 if (lt == 0 && (F8 || !*fail)) mbar_arrive(&full[slot]);  // 16 bits: see the loaders
             }
             ++u;

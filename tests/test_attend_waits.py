@@ -144,3 +144,14 @@ def test_the_model_finds_early_reads():
     assert ("end", 0, 0) in early_reads((3,), 3, "stream")
     assert early_reads((5,), 2, "stream") == set()
     assert early_reads((2,), 3, "stream") == set()
+
+
+def test_repaired_values_are_told_before_the_tile_is_handed_on():
+    """What was taken out of a V tile has to be known to the softmax warps: each
+    warp of a team says so before the team's barrier, behind which one thread
+    hands the tile on."""
+    text = source()
+    loop = text[text.index("for (int i = 0; i < 2 * w.nt; ++i, ++item)"):]
+    loop = loop[:loop.index("mbar_arrive(&full[slot])")]
+    steps = re.findall(r"repair<|s_flags\[u % kTcUnits\], 2\)|meet\(\);", loop)
+    assert steps == ["repair<", "s_flags[u % kTcUnits], 2)", "meet();"] * 2
