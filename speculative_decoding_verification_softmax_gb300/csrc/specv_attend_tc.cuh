@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     : &full[slot];
                 have = have && ok;
                 const int n = __popc(__ballot_sync(0xffffffffu, have));
+                __syncwarp();  // what the lanes said of their pages is known before the tile is there
                 // without its slot a tile is left out: an arrival on a barrier that waits for
                 // an earlier copy would be one too many
                 if (lane == 0 && ok) mbar_arrive_expect_tx(bar, (uint32_t)n * tc.box * (F8 ? D : 2 * D));

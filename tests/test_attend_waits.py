@@ -155,3 +155,12 @@ def test_repaired_values_are_told_before_the_tile_is_handed_on():
     loop = loop[:loop.index("mbar_arrive(&full[slot])")]
     steps = re.findall(r"repair<|s_flags\[u % kTcUnits\], 2\)|meet\(\);", loop)
     assert steps == ["repair<", "s_flags[u % kTcUnits], 2)", "meet();"] * 2
+
+
+def test_missing_pages_are_told_before_the_tile_is_handed_on():
+    """The lanes of a loading warp that find no page say so before lane 0 arrives
+    for the tile; votes among them order no memory."""
+    text = source()
+    loop = text[text.index("s_flags[w.u % kTcUnits], 1)"):]
+    loop = loop[:loop.index("mbar_arrive_expect_tx(bar")]
+    assert loop.count("__syncwarp();") == 1
