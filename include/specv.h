@@ -353,7 +353,8 @@ size_t spec_attend_workspace_bytes(int B, int gamma, int q_heads, int kv_heads, 
  * value that is not finite reaches only the rows that see it.  Two launches.
  * Numbers: scores, running maximum and sum, and the output are fp32; with
  * 16-bit rows the weights are rounded to that type (to fp16 under a SPEC_E4M3
- * cache) for the product with v.  Bit-reproducible for given arguments; how a
+ * cache) for the product with v.  fp16 weights are scaled to its upper end: what
+ * is below 2^-25 of the largest is held to 2^-36 of that.  Bit-reproducible for given arguments; how a
  * long cache is split depends on the whole batch's lengths, so a request's
  * last bits may change with its company.  Two calls that share a workspace
  * must be ordered on one stream.

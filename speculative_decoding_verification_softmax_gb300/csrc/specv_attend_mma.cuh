@@ -98,6 +98,17 @@ __device__ __forceinline__ bool any_nonfinite<__half>(uint32_t w) {
     return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
 }
 
+// Weights are rounded to T for the product with V.  fp16 has a least step of 2^-24:
+// the weights are taken times 2^15 (the largest, 1, stays below its 65504), so that
+// those down to 2^-29 are rounded to 2^-11 of their own, and the sums of all smaller
+// ones are off by 2^-40 of the largest for each.  A long rest far below a few
+// dominant keys would be lost otherwise, in the product but not in the sum.  bf16
+// has fp32's exponents.  Times a power of two, all else stays exact.
+template <typename T>
+constexpr float kWeightsUp = std::is_same<T, __half>::value ? 15.0f : 0.0f;
+template <typename T>
+constexpr float kWeightsDown = std::is_same<T, __half>::value ? 1.0f / 32768.0f : 1.0f;
+
 // Four e4m3 values to fp16 (exact).
 __device__ __forceinline__ void widen4(uint32_t four, uint32_t& lo, uint32_t& hi) {
     asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
@@ -402,9 +413,11 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                         }
                     }
                 }
-                // weights; their sum is of the unrounded ones.  For the product
-                // they are rounded to T: 2^-9 (bf16) or 2^-12 of each at most,
-                // as much as the output's own rounding
+                // weights (see kWeightsUp); their sum is of the unrounded ones.  For
+                // the product they are rounded to T: 2^-8 (bf16) or 2^-11 of each at
+                // most, as much as the output's own rounding
+                base[0] -= kWeightsUp<T>;
+                base[1] -= kWeightsUp<T>;
 #pragma unroll
                 for (int n = 0; n < CK / 8; ++n)
 #pragma unroll
@@ -505,8 +518,9 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 part[k] = WK == 1 ? 1.0f : ex2_approx(s_m[k][r] - base);
                 L += part[k] * s_l[k][r];
             }
+            L *= kWeightsDown<T>;
             const long long row = out_row(a, req.base, h, r0 + r);
-            const float inv = whole ? vs / L : vs;
+            const float inv = (whole ? vs / L : vs) * kWeightsDown<T>;
             for (int d = 2 * lane; d < dim; d += 64) {
                 float x = 0.0f, y = 0.0f;
 #pragma unroll

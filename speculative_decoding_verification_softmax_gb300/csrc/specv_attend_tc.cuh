@@ -50,10 +50,19 @@ constexpr int kTcRows = 128;
 constexpr int kTcThreads = 16 * 32;
 constexpr int kTcUnits = 8;  // ring of units under way
 
-// A running maximum stays the reference until it is passed by this much (to
-// base 2): weights reach 2^8 instead of 1, exactly as well in 16 bits, and the
-// output in TMEM is scaled again a few times a unit instead of every tile.
-constexpr float kTcSlack = 8.0f;
+// A running maximum stays the reference until it is passed by this much (to base 2):
+// weights reach 2^kTcSlack instead of 1, exactly as well in 16 bits, and the output
+// in TMEM is scaled again a few times a unit instead of every tile.  fp16 weights
+// (the least step is 2^-24) are taken times 2^kTcUp besides, to 2^15 in all: those
+// down to 2^-25 of the reference are rounded to 2^-11 of their own, smaller ones to
+// 2^-36 of the reference.  Without it a long rest far below a few dominant keys was
+// lost, in the product but not in the sum.
+template <typename T>
+constexpr float kTcSlack = std::is_same<T, __half>::value ? 4.0f : 8.0f;
+template <typename T>
+constexpr float kTcUp = std::is_same<T, __half>::value ? 11.0f : 0.0f;
+template <typename T>
+constexpr float kTcDown = std::is_same<T, __half>::value ? 1.0f / 2048.0f : 1.0f;
 
 // Shared memory: query rows, slots of 16-bit K or V tiles, and for an e4m3
 // cache the slots in which its tiles arrive.  The copies in flight cover HBM's
@@ -938,7 +947,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     top = fmaxf(top, top1);
                     // nothing seen stays below everything, at a scale of zero too
                     if (top != -INFINITY) top *= by;
-                    const bool up = top > m + kTcSlack;
+                    const bool up = top > m + kTcSlack<T>;
                     if (__any_sync(0xffffffffu, up)) {
                         const float now = up ? top : m;
                         const float corr = up ? ex2_approx(m - now) : 1.0f;
@@ -959,9 +968,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     // weights: their sum is of the unrounded ones; for the
-                    // product they are rounded to T, 2^-9 (bf16) or 2^-12 of
+                    // product they are rounded to T, 2^-8 (bf16) or 2^-11 of
                     // each at most, as much as the output's own rounding
-                    const float ref = m == -INFINITY ? 0.0f : m;
+                    const float ref = (m == -INFINITY ? 0.0f : m) - kTcUp<T>;
                     const Two by2 = two(by, by), ref2 = two(-ref, -ref);
                     Two sum0 = two(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll 1
@@ -1005,9 +1014,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float m1 = s_ml[0][row];
                 const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.0f : M;
                 const float w0 = ex2_approx(m - ref), w1 = ex2_approx(m1 - ref);
-                float L = l * w0 + s_ml[1][row] * w1;
+                float L = (l * w0 + s_ml[1][row] * w1) * kTcDown<T>;
                 if ((flags & 1) || *fail) L = __int_as_float(0x7fc00000);
-                const float inv = (complete ? 1.0f / L : 1.0f) * (F8 && c.v_scale ? c.v_scale[w.h] : 1.0f);
+                const float inv = (complete ? kTcDown<T> / L : kTcDown<T>) * (F8 && c.v_scale ? c.v_scale[w.h] : 1.0f);
                 s_ml[0][row] = w0 * inv;
                 s_ml[1][row] = w1 * inv;
                 if (row < w.R) {
