@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kPgThreads) k_reserve_pages(ReserveArgs a) {
     for (int i = 0; i < kPgPer; ++i) {
         const int b = tid * kPgPer + i;
         if (b < a.B) {
-            if (err[i] == SPEC_OK && s_pref[b + 1] > s_pref[b]) {
+            if (err[i] == SPEC_OK && grow[i] > 0) {  // the prefixes may have stopped at kMany, above any limit
                 if (s_pref[b + 1] <= limit) a.num[b] = s_num[b] + grow[i];
                 else err[i] = SPEC_ERR_POOL;
             }
