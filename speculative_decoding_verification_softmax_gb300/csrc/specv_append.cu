@@ -179,12 +179,21 @@ __device__ __forceinline__ void put_item(const AppendArgs& a, const CacheView& c
 // A block has RB adjacent rows of one request: a thread works its items' places
 // out once and takes them in every row, all rows' loads in flight together.  One
 // row a block (RB = 1) is for batches that would not fill the GPU otherwise; a
-// large batch with one row a block was bound by instructions.  4,600 rows of 40 + 8
-// heads of 128, 103 MB: one row 31 us, two rows 25 us (12 blocks of 128 threads an
-// SM; 26 us with 8), four rows 27 to 38 us (their registers leave fewer warps).  A
-// block's first loads are on their way before the angles and the pages are known.
+// large batch with one row a block was bound by instructions.  A block's first
+// loads are on their way before the angles and the pages are known.
+//
+// 4,600 rows of 40 + 8 heads of 128, bf16 (e4m3 cache, 103 MB), by rows a block and
+// blocks of 128 threads an SM: interleaved, 64 values turned, one row 38 us, two rows
+// 24 us (12 blocks), 25 (10), 26 (8), four rows 27 to 38 (their registers leave fewer
+// warps).  The half layout, whose items have two vectors a row, 128 values turned: one
+// row 38 us, two rows 32 (12 blocks, spilling at 40 registers), 28 (10), 27 (8); 1,700
+// rows 13, 18, 16 and 13 us.  fp32 rows (206 MB): one row 58, 38 (12), 38 (10), 40 (8).
+template <typename T, bool INTERLEAVED>
+constexpr int kAppendBlocks = sizeof(T) == 2 && !INTERLEAVED ? 8 : 12;
+
 template <typename T, typename C, bool INTERLEAVED, int E, int RB>
-__global__ void __launch_bounds__(RB == 1 ? kAppendMost : kAppendTwo, RB == 1 ? 1 : 12) k_append(AppendArgs a, CacheView c) {
+__global__ void __launch_bounds__(RB == 1 ? kAppendMost : kAppendTwo, RB == 1 ? 1 : kAppendBlocks<T, INTERLEAVED>)
+    k_append(AppendArgs a, CacheView c) {
     __shared__ __align__(16) float s_cos[RB][SPEC_MAX_HEAD_DIM / 2], s_sin[RB][SPEC_MAX_HEAD_DIM / 2];
     __shared__ long long s_entry[RB];
     pdl_trigger();
