@@ -242,7 +242,12 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t panel) {
 
 // Waits for phase `parity`.  A wait that runs out of time sets `fail`, and all
 // other waits of the block then end at once: every role runs its loops to their
-// ends, without results, and the block returns.  The waiting thread is suspended
+// ends, without results, and the block returns.  No slot that TMA fills is loaded
+// again then: one that looked free while its copy is under way would get an arrival
+// too many.  Wideners and loaders remember the first such wait of their own (a phase
+// that was skipped lets a later wait on its parity pass); the products go on giving
+// slots back (to end them cost 4% at 119 rows), so over a 16-bit cache the loaders,
+// who take those, look at `fail` behind each wait.  The waiting thread is suspended
 // for up to 20 us at a time and looks at the clock every 16th time only:
 // spinning on the clock slowed the softmax warps' exponentials several times over.
 __device__ __forceinline__ bool tc_try(uint64_t* bar, uint32_t parity) {
@@ -601,6 +606,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int of = lane / boxes, row = (lane & (boxes - 1)) << tc.shift;  // the lane's tile and first row
         const CUtensorMap* map = is_v ? &mv : &mk;
         uint32_t before = 0, issued = 0;  // items of the units before, items issued
+        bool ok = true;  // no wait for a slot has run out, see tc_wait
         Units w(s_units, unit_full, unit_empty, fail);
         while (w.next()) {
             const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
@@ -637,7 +643,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     have = false;
                 }
                 uint64_t* freed = F8 ? &raw_empty[slot] : &empty[slot];
-                const bool ok = __all_sync(0xffffffffu, item < NR || tc_wait(freed, ((item / NR) & 1) ^ 1, fail));
+                ok = ok && __all_sync(0xffffffffu, (item < NR || tc_wait(freed, ((item / NR) & 1) ^ 1, fail)) &&
+                                                       (F8 || !*fail));
                 // a 16-bit tile is ready when it has landed, unless it is to be repaired
                 uint64_t* bar = F8 || (is_v && !all_see<KT>(a, w.req, tile_key<KT>(w.req, w.t0 + t)))
                                     ? &raw_full[slot]
@@ -679,6 +686,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (WT > 32) asm volatile("bar.sync %0, 64;" ::"r"(3 + team) : "memory");
         };
         uint32_t item = 0, turns = 0;  // turns: phases of raw_full by slot (16-bit cache)
+        bool ok = true;                // no wait for a tile has run out
         int u = 0;
         Units w(s_units, unit_full, unit_empty, fail);
         while (all_agree(2, 128, w.next())) {
@@ -747,7 +755,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 bool dirty = false;
                 if (F8) {
                     const int rs = (int)(item % NR);
-                    tc_wait(&raw_full[rs], (item / NR) & 1, fail);
+                    ok = tc_wait(&raw_full[rs], (item / NR) & 1, fail) && ok;
                     const uint32_t from = raws + rs * Sh::kRawTile;
                     constexpr int STEP = WT / (D / 16), N = KT / STEP, IN = 8;  // rows of a step, steps, loads in flight
                     if (cut) {  // each thread's own chunks, as below
@@ -778,7 +786,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     fence_proxy_async_smem();
                     meet();
-                    if (lt == 0) mbar_arrive(&raw_empty[rs]);
+                    if (lt == 0 && ok) mbar_arrive(&raw_empty[rs]);
                 } else {
                     tc_wait(&raw_full[slot], (turns >> slot) & 1, fail);
                     turns ^= 1u << slot;

@@ -164,3 +164,20 @@ def test_missing_pages_are_told_before_the_tile_is_handed_on():
     loop = text[text.index("s_flags[w.u % kTcUnits], 1)"):]
     loop = loop[:loop.index("mbar_arrive_expect_tx(bar")]
     assert loop.count("__syncwarp();") == 1
+
+
+def test_after_a_wait_has_run_out_no_slot_is_loaded():
+    """A role whose wait has run out goes on without waiting, and gives slots back
+    whose copies may be under way.  A loader that took one would arrive on the
+    barrier of that copy once too often; so would one that skipped a slot and met
+    it again, two phases behind."""
+    text = source()
+    # loaders: one word for all later slots; over a 16-bit cache the products free them
+    assert "uint64_t* freed = F8 ? &raw_empty[slot] : &empty[slot];" in text
+    assert re.search(r"ok = ok && __all_sync\(0xffffffffu, \(item < NR \|\| tc_wait\(freed, .*, fail\)\) &&\s+"
+                     r"\(F8 \|\| !\*fail\)\);", text)
+    assert "if (lane == 0 && ok) mbar_arrive_expect_tx(" in text and "have = have && ok;" in text
+    # wideners give back what came by TMA, the repair hands on what did
+    assert "ok = tc_wait(&raw_full[rs], (item / NR) & 1, fail) && ok;" in text
+    assert re.findall(r"if \((.*)\) mbar_arrive\(&raw_empty\[rs\]\);", text) == ["lt == 0 && ok"]
+    assert re.findall(r"if \((.*)\) mbar_arrive\(&full\[slot\]\);", text) == ["lt == 0 && (F8 || !*fail)"]
