@@ -512,14 +512,18 @@ int spec_selftest_wait(long long limit_ns, int32_t* status, unsigned long long* 
                        spec_stream_t stream);
 
 /*
- * Test hook of the streaming kernel's timeout path (off by default).  While
+ * Test hook of the timeout paths (off by default).  The streaming kernel: while
  * `on` is nonzero, later spec_verify calls (made from any thread) treat the
  * first copy wait of every warp of the streaming kernel as expired, without
  * waiting for it.  The warps then let their copies in flight land (each wait
  * bounded as usual) and stop; the call marks every request invalid
  * (out_accept_len = -1) and its status word reads SPEC_ERR_TIMEOUT.  No copy
  * is lost and nothing hangs; it exercises the path that a bulk copy which
- * never completes would take.  Returns SPEC_OK.
+ * never completes would take.  The tensor-core attention kernel (spec_attend,
+ * more than 16 rows a KV head): the first wait for query rows counts as run out,
+ * with copies in flight.  All roles then run to their ends without waiting, the
+ * copies land, and the status word reads SPEC_ERR_TIMEOUT; the rows hold
+ * anything.  Returns SPEC_OK.
  */
 int spec_selftest_expire_first_wait(int on);
 

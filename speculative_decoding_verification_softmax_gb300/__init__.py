@@ -485,7 +485,8 @@ def selftest_wait(limit_ns: int = 1_000_000, stream=None):
 
 def selftest_expire_first_wait(on: bool) -> None:
     """Test hook: while on, the first copy wait of every streaming warp in later
-    verify calls counts as expired (the timeout path; see include/specv.h)."""
+    verify calls, and the first one of a tensor-core attention, counts as expired
+    (the timeout paths; see include/specv.h)."""
     _check(lib().spec_selftest_expire_first_wait(1 if on else 0), "spec_selftest_expire_first_wait")
 
 

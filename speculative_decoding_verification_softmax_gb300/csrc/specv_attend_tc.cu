@@ -93,6 +93,7 @@ int attend_tc(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype
     tc.box = box_tokens(c.page_size);
     tc.shift = 0;
     while ((1 << tc.shift) < tc.box) ++tc.shift;
+    tc.expire_first = expire_first_wait();
     CUtensorMap mk, mv;
     if (!make_map(mk, c.k, c, cache_dt, tc.box) || !make_map(mv, c.v, c, cache_dt, tc.box)) return SPEC_ERR_CUDA;
     if (cache_dt == SPEC_E4M3)

@@ -107,7 +107,8 @@ struct TcShape {
 };
 
 struct TcArgs {
-    int box, shift;  // tokens of a TMA box, 2^shift
+    int box, shift;    // tokens of a TMA box, 2^shift
+    int expire_first;  // test hook: the products' first wait counts as run out (0 in normal use)
 };
 
 // ------------------------------------------------------------------- PTX
@@ -846,6 +847,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t item = 0, first = 0;  // first: tiles of the units before
         Units w(s_units, unit_full, unit_empty, fail);
         while (w.next()) {
+            if (tc.expire_first) *fail = 1;
             tc_wait(&q_full, w.u & 1, fail);
             __syncwarp();
             tc_fence_after();

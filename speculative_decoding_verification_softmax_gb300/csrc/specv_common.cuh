@@ -19,6 +19,8 @@ constexpr int kStatsWarps = 20;
 constexpr int kStages = 2;
 // Bound on any device wait (nanoseconds of %globaltimer).
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+// Test hook of the kernels' timeout paths (0 in normal use).
+int expire_first_wait();
 // Largest grid of the streaming kernel (one word per CTA in the workspace,
 // read by the finish kernel's first warp as two 16-byte vectors per lane).
 constexpr int kMaxStatsGrid = 256;

@@ -978,13 +978,15 @@ __global__ void __launch_bounds__(kPackThreads) k_pack_rows(const int32_t* verif
 // ===================================================================== host
 using namespace specv;
 
+// test hook (spec_selftest_expire_first_wait)
+static std::atomic<int> g_expire_first{0};
+int specv::expire_first_wait() { return g_expire_first.load(std::memory_order_relaxed); }
+
 namespace {
 
 // profiling hook (spec_profile_events): atomics, so that setting it from one
 // thread while another launches is not a data race
 std::atomic<cudaEvent_t> g_ev_before{nullptr}, g_ev_after{nullptr};
-// test hook (spec_selftest_expire_first_wait)
-std::atomic<int> g_expire_first{0};
 
 struct DeviceInfo {
     int sms = 0;
@@ -1121,7 +1123,7 @@ int verify_impl(const void* target_logits, const void* draft_logits, const RowMa
     const char* t = (const char*)target_logits;
     const char* d = (const char*)draft_logits;
     char* ws = (char*)workspace;
-    StatsArgs sa{t, d, verify_len, B, gamma, V, c_hi, c_lo, ws, rm, g_expire_first.load(std::memory_order_relaxed)};
+    StatsArgs sa{t, d, verify_len, B, gamma, V, c_hi, c_lo, ws, rm, expire_first_wait()};
     FinishArgs fa{t,    d,    draft_tokens, verify_len, uniforms, out_tokens, out_accept_len, B, gamma, V,
                   c_hi, c_lo, ws,           rm,         0};
     cudaStream_t st = (cudaStream_t)stream;
