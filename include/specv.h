@@ -89,7 +89,7 @@ enum {
 #define SPEC_MAX_BATCH 4096
 #define SPEC_MAX_GAMMA 32
 #define SPEC_MAX_SCHED_CANDIDATES 16384 /* B * (gamma - min_len) for spec_schedule */
-#define SPEC_MAX_HEAD_DIM 256           /* of a cache; a multiple of 8 */
+#define SPEC_MAX_HEAD_DIM 256           /* of a cache; a multiple of 8, of 16 for SPEC_E4M3 */
 
 /* ------------------------------------------------------------- verification */
 
@@ -308,7 +308,7 @@ typedef struct {
     void* v;            /* device: values, same strides */
     spec_dtype dt;      /* SPEC_F32, SPEC_BF16, SPEC_F16 or SPEC_E4M3 */
     int layers;         /* fork and compact move a page's tokens in every layer; others use layer 0 */
-    int pages, page_size, kv_heads, head_dim; /* head_dim: a multiple of 8, at most 256 */
+    int pages, page_size, kv_heads, head_dim; /* head_dim: a multiple of 8 (SPEC_E4M3: 16), at most 256 */
     /* strides in elements (16-byte multiples; the head_dim values are adjacent) */
     long long layer_stride, page_stride, token_stride, head_stride;
     const float* k_scale; /* device [kv_heads], SPEC_E4M3 only: the entry stands for entry * scale; */
@@ -425,7 +425,10 @@ int spec_commit_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_coun
 
 /* Ends requests: gives back all pages of the n requests in `requests` [n]
  * (device), and sets their num_pages and cache_len to 0.  Naming one twice is
- * allowed; an id outside [0, B) is skipped (SPEC_ERR_REQUEST). */
+ * allowed; an id outside [0, B) is skipped (SPEC_ERR_REQUEST).  To the other
+ * calls the place is then a request of length 0, with its tested tokens: at
+ * verify_len 0 spec_reserve_pages takes one page for it in each round, and
+ * spec_commit_pages with an accept length of -1 gives that back. */
 int spec_free_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages, int32_t* cache_len,
                     const int32_t* requests, int n, int B, int max_pages, void* workspace, size_t workspace_bytes,
                     spec_stream_t stream);

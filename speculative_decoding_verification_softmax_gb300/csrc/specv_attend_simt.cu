@@ -6,9 +6,10 @@
 // softmax, to base 2: a tile's scores s give m' = max(m, max s), p = 2^(s - m'),
 // l' = l 2^(m - m') + sum p and o' = o 2^(m - m') + p V.
 //
-// Bound by the CUDA cores' products, of 16 rows whether a unit has them or not:
-// one token of 32 requests of 2000 to 4000 positions, 32/8 heads of 128, takes
-// 355 us for 820 MB, 2.3 TB/s.
+// Bound by the warps that work in the products: two of a block's eight have each
+// four of the 16 rows, and those whose rows a unit lacks wait at the barriers.  One
+// token of 32 requests of 2000 to 4000 positions, 32/8 heads of 128 (four rows, so
+// six warps wait), takes 354 us for 820 MB, 2.3 TB/s.
 #include "specv_attend.cuh"
 
 namespace specv {

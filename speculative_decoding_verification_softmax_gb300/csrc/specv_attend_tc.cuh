@@ -30,11 +30,11 @@
 // by itself to the rows that see it.
 //
 // Measured: 64 requests of 500 to 8192 positions, blocks of 16 drafts, 32/8 heads
-// of 128, bf16: 201 us for 1.22 GB, 6.1 TB/s (HBM; 10% go to the switches between
-// units).  19 requests of 16384 positions: 192 us, 6.7 TB/s; heads of 64 101 us,
-// 6.3 TB/s (127 with two places for scores).  e4m3 is bound by the softmax and the
-// widening instead: 105 us (heads of 64) and 142 us (128) there; ragged windows of
-// 4000, 28/4 heads of 64, pages of 16: 60 us for 116 MB.
+// of 128, bf16: 200 us for 1.22 GB, 6.1 TB/s (HBM; 10% go to the switches between
+// units).  19 requests of 16384 positions: 190 us, 6.7 TB/s; heads of 64 100 us,
+// 6.4 TB/s (127 with two places for scores).  e4m3 is bound by the softmax and the
+// widening instead: 105 us (heads of 64) and 145 to 159 us (128) there; ragged windows
+// of 4000, 28/4 heads of 64, pages of 16: 61 us for 116 MB (fp16 cache 55 us).
 #pragma once
 
 #include <cuda.h>
