@@ -31,3 +31,30 @@ def test_reserve_more_than_any_pool_holds(sv):
     assert num.cpu()[[0, B - 2]].tolist() == [4, 5] and int(num.sum()) == 9
     assert table[0, :5].tolist() == [0, 1, 2, 3, -1] and int((table != -1).sum()) == 4
     assert ref[:4].tolist() == [1] * 4 and int(ref.sum()) == 4
+
+
+def test_a_place_whose_request_has_ended(sv):
+    """At verify length 0 and accept length -1 it takes a page for each round and
+    gives it back, with no error, while its neighbours go on."""
+    B, slots, pages, page = 3, 4, 12, 4
+    table = torch.full((B, slots), -1, dtype=torch.int32, device="cuda")
+    num, ref, lens = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (B, pages, B))
+    ws = sv.alloc_cache_workspace(B)
+
+    def i32(*x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def step(ell, accept):
+        st, _ = sv.reserve_pages(table, num, ref, lens, i32(*ell), gamma=2, page_size=page, workspace=ws)
+        assert st.tolist() == [0] * B
+        held = num.tolist()
+        sv.commit_pages(table, num, ref, lens, i32(*accept), page_size=page, workspace=ws)
+        assert sv.read_status(ws) == 0
+        return held
+
+    step((2, 2, 2), (2, 2, 1))
+    sv.free_pages(table, num, ref, lens, i32(1), workspace=ws)
+    for k in range(1, 3):
+        assert step((2, 0, 2), (2, -1, 1))[1] == 1
+        assert lens.tolist() == [3 + 3 * k, 0, 2 + 2 * k] and num[1] == 0 and (table[1] == -1).all()
+        assert int(ref.sum()) == int(num.sum())
