@@ -103,11 +103,12 @@ __device__ __forceinline__ bool any_nonfinite<__half>(uint32_t w) {
 // those down to 2^-29 are rounded to 2^-11 of their own, and the sums of all smaller
 // ones are off by 2^-40 of the largest for each.  A long rest far below a few
 // dominant keys would be lost otherwise, in the product but not in the sum.  bf16
-// has fp32's exponents.  Times a power of two, all else stays exact.
+// has fp32's exponents.  What the weights refer to is the running maximum less 15,
+// rounded up: they stay at or below 2^15 where fp32 has steps of more than one.
 template <typename T>
-constexpr float kWeightsUp = std::is_same<T, __half>::value ? 15.0f : 0.0f;
-template <typename T>
-constexpr float kWeightsDown = std::is_same<T, __half>::value ? 1.0f / 32768.0f : 1.0f;
+__device__ __forceinline__ float reference_of(float top) {
+    return std::is_same<T, __half>::value ? __fsub_ru(top, 15.0f) : top;
+}
 
 // Four e4m3 values to fp16 (exact).
 __device__ __forceinline__ void widen4(uint32_t four, uint32_t& lo, uint32_t& hi) {
@@ -398,12 +399,12 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                     top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
                     up |= top[i] > m[i];
                     top[i] = fmaxf(top[i], m[i]);
-                    base[i] = top[i] == -INFINITY ? 0.0f : top[i];
+                    base[i] = top[i] == -INFINITY ? 0.0f : reference_of<T>(top[i]);
                 }
                 if (__any_sync(0xffffffffu, up)) {  // a new maximum: what there is shrinks
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float corr = ex2_approx(m[i] - base[i]);
+                        const float corr = ex2_approx(reference_of<T>(m[i]) - base[i]);
                         l[i] *= corr;
                         m[i] = top[i];
 #pragma unroll
@@ -413,11 +414,9 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                         }
                     }
                 }
-                // weights (see kWeightsUp); their sum is of the unrounded ones.  For
+                // weights (see reference_of); their sum is of the unrounded ones.  For
                 // the product they are rounded to T: 2^-8 (bf16) or 2^-11 of each at
                 // most, as much as the output's own rounding
-                base[0] -= kWeightsUp<T>;
-                base[1] -= kWeightsUp<T>;
 #pragma unroll
                 for (int n = 0; n < CK / 8; ++n)
 #pragma unroll
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             const int r = wr * 16 + g + 8 * i;
             if (t4 == 0) {
-                s_m[wk][r] = m[i];
+                s_m[wk][r] = reference_of<T>(m[i]);
                 s_l[wk][r] = l[i];
             }
             if (F8) {
@@ -518,9 +517,8 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 part[k] = WK == 1 ? 1.0f : ex2_approx(s_m[k][r] - base);
                 L += part[k] * s_l[k][r];
             }
-            L *= kWeightsDown<T>;
             const long long row = out_row(a, req.base, h, r0 + r);
-            const float inv = (whole ? vs / L : vs) * kWeightsDown<T>;
+            const float inv = whole ? vs / L : vs;
             for (int d = 2 * lane; d < dim; d += 64) {
                 float x = 0.0f, y = 0.0f;
 #pragma unroll

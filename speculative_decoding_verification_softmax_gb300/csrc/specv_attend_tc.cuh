@@ -33,8 +33,8 @@
 // of 128, bf16: 200 us for 1.22 GB, 6.1 TB/s (HBM; 10% go to the switches between
 // units).  19 requests of 16384 positions: 190 us, 6.7 TB/s; heads of 64 100 us,
 // 6.4 TB/s (127 with two places for scores).  e4m3 is bound by the softmax and the
-// widening instead: 105 us (heads of 64) and 145 to 159 us (128) there; ragged windows
-// of 4000, 28/4 heads of 64, pages of 16: 61 us for 116 MB (fp16 cache 55 us).
+// widening instead: 106 us (heads of 64) and 148 to 167 us (128) there; ragged windows
+// of 4000, 28/4 heads of 64, pages of 16: 62 us for 116 MB (fp16 cache 55 us).
 #pragma once
 
 #include <cuda.h>
@@ -50,19 +50,24 @@ constexpr int kTcRows = 128;
 constexpr int kTcThreads = 16 * 32;
 constexpr int kTcUnits = 8;  // ring of units under way
 
-// A running maximum stays the reference until it is passed by this much (to base 2):
-// weights reach 2^kTcSlack instead of 1, exactly as well in 16 bits, and the output
-// in TMEM is scaled again a few times a unit instead of every tile.  fp16 weights
-// (the least step is 2^-24) are taken times 2^kTcUp besides, to 2^15 in all: those
-// down to 2^-25 of the reference are rounded to 2^-11 of their own, smaller ones to
-// 2^-36 of the reference.  Without it a long rest far below a few dominant keys was
-// lost, in the product but not in the sum.
+// The weights' reference is the running maximum, and stays until it is passed by
+// kTcSlack (to base 2): weights reach 2^kTcSlack instead of 1, exactly as well in 16
+// bits, and the output in TMEM is scaled again a few times a unit instead of every
+// tile.  fp16 weights (the least step is 2^-24) have a reference kTcUp below it, and
+// reach 2^15: those down to 2^-25 of the maximum are rounded to 2^-11 of their own,
+// smaller ones to 2^-36 of it.  Without it a long rest far below a few dominant keys
+// was lost, in the product but not in the sum.  Maximum and reference are rounded up,
+// the limit down: no weight passes 2^15 where fp32 has steps of more than one.
 template <typename T>
 constexpr float kTcSlack = std::is_same<T, __half>::value ? 4.0f : 8.0f;
 template <typename T>
 constexpr float kTcUp = std::is_same<T, __half>::value ? 11.0f : 0.0f;
+// From this score on (fp32 has steps of 2^-4 there, for bf16 of 2) the products of the
+// matrix instructions are scaled and rounded before the reference is taken from them:
+// in one fused operation with it they would differ from their rounded maximum by more
+// than the weights' type holds (beyond 2^28, bf16 2^31).
 template <typename T>
-constexpr float kTcDown = std::is_same<T, __half>::value ? 1.0f / 2048.0f : 1.0f;
+constexpr float kTcFine = std::is_same<T, __half>::value ? 1048576.0f : 33554432.0f;
 
 // Shared memory: query rows, slots of 16-bit K or V tiles, and for an e4m3
 // cache the slots in which its tiles arrive.  The copies in flight cover HBM's
@@ -526,6 +531,24 @@ __device__ __noinline__ Eight sum_nonfinite(const AttendArgs& a, const CacheView
     return sum;
 }
 
+// Scales a row's scores where they are; the largest one.
+__device__ __noinline__ float scale_scores(uint32_t ts, float by) {
+    float x[32], top = -INFINITY;
+#pragma unroll 1
+    for (int q = 0; q < kTcKeys / 32; ++q) {
+        tc_ld32(x, ts + q * 32);
+        tc_wait32(x);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            x[e] *= by;
+            top = fmaxf(top, x[e]);
+        }
+        tc_st32(ts + q * 32, x);
+    }
+    tc_wait_st();
+    return top;
+}
+
 // T: type of the products, O: type of q and out, F8: e4m3 cache.
 template <typename T, typename O, bool F8, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -917,7 +940,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool active = (warp & 3) * 32 < w.R;  // the warp has rows
             const int pos = w.req.n + (row < w.R ? (int)a.by_group.div((uint32_t)(w.r0 + row)) : w.req.ell);
             float scale = fabsf(a.scale) * (F8 && c.k_scale ? fabsf(c.k_scale[w.h]) : 1.0f);
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f;  // the reference and the sum
+            bool coarse = false;            // a score of the warp has been beyond kTcFine
             for (int t = s; t < w.nt; t += 2) {
                 const uint32_t g = first + t, ts = tmem + lanes + (g % NB) * KT;
                 tc_wait(&s_full[g % NB], (g / NB) & 1, fail);
@@ -930,7 +954,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // The loops over 32 columns stay loops: the roles' code together has
                     // to fit the instruction cache (unrolled, they were 2.5 times slower)
                     float x[32], y[32], top = -INFINITY, top1 = -INFINITY;
-                    if (!all_see<KT>(a, w.req, key0)) {
+                    if (coarse || !all_see<KT>(a, w.req, key0)) {
                         // scores that the row does not see, in a pass of its own: a tile
                         // that a border cuts is rare, and this code cold.  The others are
                         // scaled here (at a scale of zero, infinity times it is no number)
@@ -960,10 +984,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     top = fmaxf(top, top1);
                     // nothing seen stays below everything, at a scale of zero too
-                    if (top != -INFINITY) top *= by;
-                    const bool up = top > m + kTcSlack<T>;
+                    if (top != -INFINITY) top = __fmul_ru(top, by);
+                    bool up = top > __fadd_rd(m, kTcUp<T> + kTcSlack<T>);
                     if (__any_sync(0xffffffffu, up)) {
-                        const float now = up ? top : m;
+                        if (!coarse && __any_sync(0xffffffffu, up && row < w.R && fabsf(top) >= kTcFine<T>)) {
+                            // the first such tile: its scores are scaled now, see kTcFine
+                            coarse = true;
+                            top = scale_scores(ts, by);
+                            by = 1.0f;
+                            up = top > __fadd_rd(m, kTcUp<T> + kTcSlack<T>);
+                        }
+                        const float now = up ? __fsub_ru(top, kTcUp<T>) : m;
                         const float corr = up ? ex2_approx(m - now) : 1.0f;
                         l *= corr;
                         m = now;
@@ -984,7 +1015,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // weights: their sum is of the unrounded ones; for the
                     // product they are rounded to T, 2^-8 (bf16) or 2^-11 of
                     // each at most, as much as the output's own rounding
-                    const float ref = (m == -INFINITY ? 0.0f : m) - kTcUp<T>;
+                    const float ref = m == -INFINITY ? 0.0f : m;
                     const Two by2 = two(by, by), ref2 = two(-ref, -ref);
                     Two sum0 = two(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll 1
@@ -1028,9 +1059,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float m1 = s_ml[0][row];
                 const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.0f : M;
                 const float w0 = ex2_approx(m - ref), w1 = ex2_approx(m1 - ref);
-                float L = (l * w0 + s_ml[1][row] * w1) * kTcDown<T>;
+                float L = l * w0 + s_ml[1][row] * w1;
                 if ((flags & 1) || *fail) L = __int_as_float(0x7fc00000);
-                const float inv = (complete ? kTcDown<T> / L : kTcDown<T>) * (F8 && c.v_scale ? c.v_scale[w.h] : 1.0f);
+                const float inv = (complete ? 1.0f / L : 1.0f) * (F8 && c.v_scale ? c.v_scale[w.h] : 1.0f);
                 s_ml[0][row] = w0 * inv;
                 s_ml[1][row] = w1 * inv;
                 if (row < w.R) {
