@@ -82,7 +82,8 @@ enum {
     SPEC_ERR_POOL = -15,       /* device: no free pages left for a request */
     SPEC_ERR_CACHE_LEN = -16,  /* device: a cache length outside the request's page table or pages */
     SPEC_ERR_PAGE = -17,       /* device: a needed page table entry outside [0, pages), or a page with no reference */
-    SPEC_ERR_REQUEST = -18     /* device: a request id outside [0, B), or one that a call may not name twice */
+    SPEC_ERR_REQUEST = -18,    /* device: a request id outside [0, B), or one that a call may not name twice */
+    SPEC_ERR_PLAN = -19        /* device: a plan that spec_share_plan did not make, or made for other sizes */
 };
 
 /* Limits of this build. */
@@ -364,6 +365,56 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
                 const int32_t* verify_len, const int32_t* q_row, int rows, int B, int gamma, float scale,
                 int window, int sinks, void* out, float* out_lse, void* workspace, size_t workspace_bytes,
                 spec_stream_t stream);
+
+/*
+ * Attention of a batch whose requests share prefixes (branches of spec_fork_pages,
+ * or any requests whose page tables begin with the same pages): the plan, made once
+ * for a round and used by all its layers.
+ *
+ * Requests whose first page is the same are a class, the lowest of them its head.
+ * depth_b is the number of leading entries that request b's row of the page table
+ * has like the head's, among pages that both have filled (cache_len / page_size).
+ * Of the depths d with d * page_size >= least, the one with the largest
+ * d * (members of depth >= d but the head), on ties the smallest, makes those members
+ * and the head a group that shares d pages.  The head leaves the class in any case, and
+ * the rest is taken again, up to 32 times.
+ *   page_table .. B, gamma   as for spec_attend; verify_len and q_row may be NULL.
+ *   least          shorter prefixes (in positions) are not shared; about 256.
+ *   out_leader     [B] int32: the group's head; b itself if alone.
+ *   out_shared     [B] int32: the pages that the group shares; 0 if alone.
+ *   plan           device, spec_share_plan_bytes(), 16-byte aligned; needs no
+ *                  initialisation.  Its first word is the status of the latest call
+ *                  (spec_read_status): SPEC_ERR_VERIFY_LEN, SPEC_ERR_ROW_INDEX or
+ *                  SPEC_ERR_CACHE_LEN of a request, which is then alone, with the rows
+ *                  that it has in spec_attend.
+ * The plan holds the lengths and rows of this call, and no page ids: it is to be
+ * made again when they change or when a shared entry does.  Rows of two requests may
+ * not overlap.  One launch.
+ */
+size_t spec_share_plan_bytes(int B, int gamma, int rows);
+int spec_share_plan(const int32_t* page_table, int max_pages, int page_size, const int32_t* cache_len,
+                    const int32_t* verify_len, const int32_t* q_row, int rows, int B, int gamma, int least,
+                    int32_t* out_leader, int32_t* out_shared, void* plan, size_t plan_bytes, spec_stream_t stream);
+
+/* Bytes of device workspace of spec_attend_shared; 0 if out of range.  `rows` is
+ * that of the plan: B * (gamma+1), or the packed rows. */
+size_t spec_attend_shared_workspace_bytes(int B, int gamma, int rows, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * spec_attend (without a window) by a plan: the positions that a group shares are
+ * read once for the rows of all its members.  rows, B, gamma, max_pages and the
+ * cache's page_size are those that the plan was made with (else SPEC_ERR_PLAN, and
+ * nothing is written); lengths and rows are the plan's.  Other arguments, errors of
+ * requests and numbers as for spec_attend; rows of shared prefixes are sums of two
+ * parts, joined in fp32.  A page of a shared prefix is taken from the row of the
+ * page table of the group's head.  The workspace holds nothing between calls but
+ * its status word; two calls that share one must be ordered on one stream.  Two
+ * launches.
+ */
+int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_stride, spec_dtype dt, int q_heads,
+                       const spec_cache* cache, const int32_t* page_table, int max_pages, const void* plan,
+                       size_t plan_bytes, int rows, int B, int gamma, float scale, void* out, float* out_lse,
+                       void* workspace, size_t workspace_bytes, spec_stream_t stream);
 
 /*
  * Rotary positions and the append of the tested tokens' keys and values.  Row

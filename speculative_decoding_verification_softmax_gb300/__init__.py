@@ -20,9 +20,9 @@ _CSRC = os.path.join(_HERE, "csrc")
 LIB_PATH = os.path.join(_HERE, "libspecv.so")
 SOURCES = ["specv_verify.cu", "specv_sched.cu", "specv_api.cu", "specv_static.cu", "specv_pages.cu",
            "specv_append.cu", "specv_attend.cu", "specv_attend_simt.cu", "specv_attend_mma16.cu",
-           "specv_attend_mma8.cu", "specv_attend_tc.cu"]
+           "specv_attend_mma8.cu", "specv_attend_tc.cu", "specv_share.cu", "specv_share_mma.cu", "specv_share_tc.cu"]
 HEADERS = ["specv_common.cuh", "specv_rowstats.cuh", "specv_cache.cuh", "specv_attend.cuh", "specv_attend_mma.cuh", "specv_attend_tc.cuh",
-           "specv_trace.h"]
+           "specv_attend_tc_launch.cuh", "specv_trace.h"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 
@@ -31,6 +31,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_TEMPERATURE = 0, -1, -2, -3, -4
 ERR_VERIFY_LEN, ERR_TOKEN, ERR_WORKSPACE, ERR_COST_TABLE = -5, -6, -7, -8
 ERR_NONFINITE, ERR_TIMEOUT, ERR_CUDA, ERR_UNIFORM, ERR_CONFIDENCE = -9, -10, -11, -12, -13
 ERR_ROW_INDEX, ERR_POOL, ERR_CACHE_LEN, ERR_PAGE, ERR_REQUEST = -14, -15, -16, -17, -18
+ERR_PLAN = -19
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 SCHED_EXACT, SCHED_ALGORITHM1, SCHED_DCUT = 0, 1, 2
 MAX_BATCH, MAX_GAMMA, MAX_SCHED_CANDIDATES = 4096, 32, 16384
@@ -42,7 +43,8 @@ EXPORTED = ["spec_verify_workspace_bytes", "spec_verify", "spec_verify_stats",
             "spec_pack_rows", "spec_selftest_wait", "spec_selftest_expire_first_wait",
             "spec_cache_workspace_bytes", "spec_attend_workspace_bytes", "spec_attend", "spec_append_kv",
             "spec_reserve_pages", "spec_commit_pages", "spec_free_pages", "spec_fork_pages",
-            "spec_compact_pages"]
+            "spec_compact_pages", "spec_share_plan_bytes", "spec_share_plan",
+            "spec_attend_shared_workspace_bytes", "spec_attend_shared"]
 STATIC_WORKSPACE_BYTES = 8 << 20
 
 
@@ -151,7 +153,14 @@ def lib():
                 L.spec_free_pages.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, vp, sz, vp]
                 L.spec_fork_pages.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, cp, vp, vp, sz, vp]
                 L.spec_compact_pages.argtypes = [vp, vp, vp, i32, i32, cp, vp, vp, vp, vp, sz, vp]
-                for f in (L.spec_attend, L.spec_append_kv, L.spec_reserve_pages, L.spec_commit_pages,
+                L.spec_share_plan_bytes.argtypes = [i32, i32, i32]
+                L.spec_share_plan_bytes.restype = sz
+                L.spec_share_plan.argtypes = [vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+                L.spec_attend_shared_workspace_bytes.argtypes = [i32] * 6
+                L.spec_attend_shared_workspace_bytes.restype = sz
+                L.spec_attend_shared.argtypes = [vp, ll, ll, i32, i32, cp, vp, i32, vp, sz, i32, i32, i32, f32, vp, vp,
+                                                 vp, sz, vp]
+                for f in (L.spec_share_plan, L.spec_attend_shared, L.spec_attend, L.spec_append_kv, L.spec_reserve_pages, L.spec_commit_pages,
                           L.spec_free_pages, L.spec_fork_pages, L.spec_compact_pages):
                     f.restype = i32
                 _lib = L
@@ -713,6 +722,100 @@ def attend(q, k_cache, v_cache, page_table, cache_len, verify_len=None, row=None
                            workspace.data_ptr(), _workspace_bytes(workspace, dev), _raw_stream(stream, dev))
     if rc != OK:
         raise SpecError(rc, "spec_attend")
+    return out, workspace
+
+
+def alloc_share_plan(B: int, gamma: int, rows: int | None = None, device=None):
+    """A plan of share_plan; rows: the packed rows, B * (gamma + 1) by default."""
+    torch = _torch()
+    n = int(lib().spec_share_plan_bytes(B, gamma, B * (gamma + 1) if rows is None else rows))
+    if n == 0:
+        raise SpecError(ERR_SHAPE, "spec_share_plan_bytes")
+    w = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    w[:256].zero_()
+    return w
+
+
+def alloc_attend_shared_workspace(B: int, gamma: int, q_heads: int, kv_heads: int, head_dim: int,
+                                  rows: int | None = None, device=None):
+    """A workspace of attend_shared (its status word zeroed, sticky until read_status)."""
+    torch = _torch()
+    n = int(lib().spec_attend_shared_workspace_bytes(B, gamma, B * (gamma + 1) if rows is None else rows, q_heads,
+                                                     kv_heads, head_dim))
+    if n == 0:
+        raise SpecError(ERR_SHAPE, "spec_attend_shared_workspace_bytes")
+    w = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    w[:256].zero_()
+    return w
+
+
+def share_plan(page_table, cache_len, verify_len=None, row=None, *, gamma: int, page_size: int,
+               rows: int | None = None, least: int = 256, out_leader=None, out_shared=None, plan=None, stream=None):
+    """Run spec_share_plan: groups of requests whose page tables begin with the
+    same pages, for attend_shared.  page_table, cache_len, verify_len and row as for
+    attend; rows: those of q where they are packed (with `row`).  The plan serves all
+    layers of a round, and is made again when lengths, rows or shared entries change.
+    Returns (plan, out_leader [B], out_shared [B])."""
+    torch = _torch()
+    dev = _current_device(page_table)
+    B, slots = page_table.shape
+    _tables(page_table, cache_len, verify_len, row, dev)
+    if rows is None:
+        if row is not None:
+            raise ValueError("packed rows need rows")
+        rows = B * (gamma + 1)
+    elif row is None and rows != B * (gamma + 1):
+        raise ValueError(f"padded rows are {B * (gamma + 1)}, got {rows}")
+    for name, t in (("out_leader", out_leader), ("out_shared", out_shared)):
+        if t is not None:
+            _want(name, t, torch.int32, (B,), dev)
+    if out_leader is None:
+        out_leader = _made_on(stream, torch.empty, (B,), dtype=torch.int32, device=page_table.device)
+    if out_shared is None:
+        out_shared = _made_on(stream, torch.empty, (B,), dtype=torch.int32, device=page_table.device)
+    if plan is None:
+        plan = _made_on(stream, alloc_share_plan, B, gamma, rows, page_table.device)
+    _want("plan", plan, torch.uint8, (plan.numel(),), dev)
+    rc = lib().spec_share_plan(page_table.data_ptr(), slots, page_size, cache_len.data_ptr(), _address(verify_len),
+                               _address(row), rows, B, gamma, least, out_leader.data_ptr(), out_shared.data_ptr(),
+                               plan.data_ptr(), plan.numel(), _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_share_plan")
+    return plan, out_leader, out_shared
+
+
+def attend_shared(q, k_cache, v_cache, page_table, plan, *, gamma=None, scale=None, k_scale=None, v_scale=None,
+                  out=None, out_lse=None, workspace=None, stream=None):
+    """Run spec_attend_shared: attend without a window, for a batch that shares
+    prefixes by the plan of share_plan, which holds the lengths and rows.  q [B,
+    gamma+1, heads, head_dim], or packed [rows, heads, head_dim] with gamma; other
+    arguments as for attend.  Returns (out, workspace)."""
+    torch = _torch()
+    dt = _row_dtype("q", q)
+    packed = q.dim() == 3
+    gamma = _gamma_of(q, True if packed else None, gamma)
+    dev = _current_device(q)
+    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale, dev)
+    B, slots = page_table.shape
+    heads, dim = q.shape[-2], k_cache.shape[-1]
+    rows, rs, hs = _row_strides("q", q, q.dtype, heads, dim, B, gamma, packed, dev)
+    _want("page_table", page_table, torch.int32, (B, slots), dev)
+    _want("plan", plan, torch.uint8, (plan.numel(),), dev)
+    if out is None:
+        out = _made_on(stream, torch.empty, q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _want("out", out, q.dtype, q.shape, dev)
+    if out_lse is not None:
+        _want("out_lse", out_lse, torch.float32, q.shape[:-1], dev)
+    if workspace is None:
+        workspace = _made_on(stream, alloc_attend_shared_workspace, B, gamma, heads, k_cache.shape[-2], dim, rows,
+                             q.device)
+    rc = lib().spec_attend_shared(q.data_ptr(), rs, hs, dt, heads, cache, page_table.data_ptr(), slots,
+                                  plan.data_ptr(), plan.numel(), rows, B, gamma, dim ** -0.5 if scale is None else scale,
+                                  out.data_ptr(), _address(out_lse), workspace.data_ptr(),
+                                  _workspace_bytes(workspace, dev), _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_attend_shared")
     return out, workspace
 
 

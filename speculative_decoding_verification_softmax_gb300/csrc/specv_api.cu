@@ -114,6 +114,7 @@ const char* spec_status_string(int status) {
         case SPEC_ERR_CACHE_LEN: return "a cache length lies outside the request's page table or pages";
         case SPEC_ERR_PAGE: return "a needed page table entry is not a page, or a page has no reference";
         case SPEC_ERR_REQUEST: return "a request id is out of range or named twice";
+        case SPEC_ERR_PLAN: return "the plan was not made by spec_share_plan, or for other sizes";
         default: return "unknown status";
     }
 }

@@ -8,6 +8,18 @@
 
 namespace specv {
 
+// A batch that shares prefixes (SH below) is split into items by a plan made once
+// for all layers (specv_share.cu): of each group the shared positions, for the
+// rows of all its members, and of each request the positions behind them.  An item
+// is to the kernels what a request is otherwise.
+enum { kAlone = 0, kRest = 1, kPrefix = 2 };  // an item: a whole request, one's rest, a group's prefix
+struct alignas(16) ShareItem {
+    int n, ell;      // as a request's, without the positions of `skip` (a prefix: its last position, and 0)
+    int base, rows;  // first row; of a prefix, its place in the plan's list of rows
+    int b, skip;     // row of the page table, and its entries left out
+    int kind, code;
+};
+
 struct AttendArgs {
     const char* q;
     long long q_row, q_head;  // strides in bytes
@@ -31,6 +43,15 @@ struct AttendArgs {
     float part_cost;  // of a part when joined, in tiles
     float scale;      // of the scores, to base 2
     FastDiv by_group;
+    // SH: the plan, and the parts of rows that two items have (each side: [rows][q_heads])
+    const int* plan;  // its header
+    const ShareItem* items;
+    const int32_t* list;
+    const uint8_t* kinds;
+    float* side;      // [2][rows][q_heads][D], sums scaled by 2^-M
+    float2* side_ml;  // [2][rows][q_heads]: M and the sum of weights
+    int2* where;      // [2][rows][q_heads]: parts of a unit that was cut, and block << 7 | row of the unit
+                      // of the first; 0 in `side`, -1 nothing to join
 };
 
 // ---------------------------------------------------------------- the work
@@ -47,11 +68,43 @@ struct Request {
     int n, ell;    // cache length, drafts
     int base;      // first row
     int sink_tiles, first_tile, tiles, row_tiles, units;
+    int rows, b, skip, kind;  // SH, see ShareItem
 };
 
-template <int KT>
+// Items of a plan, or requests.  A plan made for other sizes has none.
+constexpr int kPlanMagic = 0x73706c6e;
+enum { kPlanStatus, kPlanIs, kPlanB, kPlanGamma, kPlanRows, kPlanSlots, kPlanPage, kPlanItems, kPlanWords };
+template <bool SH>
+__device__ __forceinline__ int requests_of(const AttendArgs& a, const CacheView& c) {
+    if constexpr (SH) {
+        const bool fits = a.plan[kPlanIs] == kPlanMagic && a.plan[kPlanB] == a.B && a.plan[kPlanGamma] == a.gamma &&
+                          a.plan[kPlanRows] == a.rows && a.plan[kPlanSlots] == a.max_pages &&
+                          a.plan[kPlanPage] == c.page_size;
+        return fits ? a.plan[kPlanItems] : 0;
+    }
+    return a.B;
+}
+
+template <int KT, bool SH>
 __device__ __forceinline__ Request request_of(const AttendArgs& a, const CacheView& c, int b) {
     Request r;
+    if constexpr (SH) {
+        const int4* p = (const int4*)(a.items + b);
+        const int4 x = p[0], y = p[1];
+        r.n = x.x;
+        r.ell = x.y;
+        r.base = x.z;
+        r.rows = x.w;
+        r.b = y.x;
+        r.skip = y.y;
+        r.kind = y.z;
+        r.code = y.w;
+        r.sink_tiles = r.first_tile = 0;
+        r.tiles = r.code == SPEC_OK ? (int)((uint32_t)(r.n + r.ell) / KT) + 1 : 0;
+        r.row_tiles = r.code == SPEC_OK ? (r.rows * a.group + a.tile_rows - 1) >> a.tile_shift : 0;
+        r.units = r.row_tiles * c.kv_heads;
+        return r;
+    }
     r.n = a.len[b];
     r.ell = a.ell ? a.ell[b] : a.gamma;
     r.base = a.row ? a.row[b] : b * (a.gamma + 1);
@@ -72,6 +125,25 @@ __device__ __forceinline__ Request request_of(const AttendArgs& a, const CacheVi
     r.row_tiles = ((r.ell + 1) * a.group + a.tile_rows - 1) >> a.tile_shift;
     r.units = r.row_tiles * c.kv_heads;
     return r;
+}
+
+// Rows (of a head) of a request, and of them row j: its row in q and out, its
+// position.
+template <bool SH>
+__device__ __forceinline__ int rows_of(const Request& r) { return SH ? r.rows : r.ell + 1; }
+template <bool SH>
+__device__ __forceinline__ int row_of(const AttendArgs& a, const Request& r, int j) {
+    if constexpr (SH)
+        if (r.kind == kPrefix) return a.list[r.base + j];
+    return r.base + j;
+}
+template <bool SH>
+__device__ __forceinline__ int position_of(const Request& r, int j) { return r.n + (SH ? min(j, r.ell) : j); }
+
+// The pages of a request (or item) b.
+template <bool SH>
+__device__ __forceinline__ const int32_t* pages_of(const AttendArgs& a, const Request& r, int b) {
+    return SH ? a.table + (size_t)r.b * a.max_pages + r.skip : a.table + (size_t)b * a.max_pages;
 }
 
 // First key of tile t of a request.
@@ -116,17 +188,18 @@ __device__ __forceinline__ long long quotient(long long n, uint32_t d) {
 }
 
 // The block's run, in s.run.  All threads call it.
-template <int KT, int THREADS>
+template <int KT, bool SH, int THREADS>
 __device__ __forceinline__ void run_of(const AttendArgs& a, const CacheView& c, RunShared<THREADS>& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.B + THREADS - 1) / THREADS;
-    const int b0 = tid * per, b1 = min(a.B, b0 + per);
+    const int count = requests_of<SH>(a, c);
+    const int per = (count + THREADS - 1) / THREADS;
+    const int b0 = tid * per, b1 = min(count, b0 + per);
     long long mine = 0;
     int longest = 0;
     Request r = {};
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-        r = request_of<KT>(a, c, b);
+        r = request_of<KT, SH>(a, c, b);
         mine += (long long)r.units * (r.tiles + a.lead);
         longest = max(longest, r.tiles);
     }
@@ -161,7 +234,7 @@ __device__ __forceinline__ void run_of(const AttendArgs& a, const CacheView& c, 
         if (per > 1) {
 #pragma unroll 1
             for (;; ++b) {
-                r = request_of<KT>(a, c, b);
+                r = request_of<KT, SH>(a, c, b);
                 const long long w = (long long)r.units * (r.tiles + a.lead);
                 if (at < w) break;
                 at -= w;
@@ -182,7 +255,7 @@ __device__ __forceinline__ int4 open_of(int parts, int base, int r0, int R, int 
 
 // The segments of a run: tiles t0 .. t0 + nt - 1 of a unit, for the rows r0 ..
 // r0 + R - 1 of KV head h.
-template <int KT>
+template <int KT, bool SH>
 struct Walk {
     Request req;
     int b, unit, t0, nt, h, r0, R;
@@ -208,7 +281,7 @@ struct Walk {
                 if (++unit == req.units) {
                     unit = 0;
 #pragma unroll 1
-                    do req = request_of<KT>(a, c, ++b);
+                    do req = request_of<KT, SH>(a, c, ++b);
                     while (req.units == 0);
                 }
             }
@@ -221,7 +294,7 @@ struct Walk {
         }
         h = unit / req.row_tiles;
         r0 = (unit - h * req.row_tiles) * a.tile_rows;
-        R = min((req.ell + 1) * a.group - r0, a.tile_rows);
+        R = min(rows_of<SH>(req) * a.group - r0, a.tile_rows);
         return true;
     }
     // True if the segment is the whole unit; else its parts are joined, and the
@@ -238,6 +311,34 @@ struct Walk {
 // slot 0 if it began in an earlier one.
 __device__ __forceinline__ float* part_at(const AttendArgs& a, int block, int slot) {
     return a.parts + ((long long)block * 2 + slot) * a.part_floats;
+}
+
+// SH: a row's part of a unit, where it goes.  `i` is the index of the row (its own
+// of out, or behind all of these for a prefix).
+struct PartRow {
+    float* o;
+    float* m;
+    float* l;
+};
+__device__ __forceinline__ PartRow part_row(const AttendArgs& a, float* part, int dim, int r) {
+    return {part + r * dim, part + a.tile_rows * dim + r, part + a.tile_rows * (dim + 1) + r};
+}
+__device__ __forceinline__ PartRow side_row(const AttendArgs& a, int dim, long long i) {
+    float* ml = (float*)(a.side_ml + i);
+    return {a.side + i * dim, ml, ml + 1};
+}
+// Row r of KV head h of a request in out, and its index in `where`.
+__device__ __forceinline__ long long shared_out_row(const AttendArgs& a, const Request& q, int h, int r) {
+    const int j = (int)a.by_group.div((uint32_t)r);
+    return (long long)row_of<true>(a, q, j) * a.q_heads + h * a.group + (r - j * a.group);
+}
+__device__ __forceinline__ long long where_of(const AttendArgs& a, int kind, long long row) {
+    return kind == kPrefix ? row + (long long)a.rows * a.q_heads : row;
+}
+// What the joining kernel is told of row r of a unit, by the block with its tile 0:
+// `parts` of a unit that was cut.
+__device__ __forceinline__ void tell(const AttendArgs& a, long long i, bool whole, bool direct, int parts, int r) {
+    a.where[i] = whole ? make_int2(direct ? -1 : 0, 0) : make_int2(parts, (int)(blockIdx.x << 7) | r);
 }
 
 // The row of out (and the index of lse) of row r of KV head h of a request whose
@@ -259,11 +360,13 @@ __device__ __forceinline__ long long key_at(const AttendArgs& a, const CacheView
 // After its run, a block reports requests without work, and fills the rows of
 // those whose positions do not fit (blocks share the requests).  Called by the
 // first `threads` threads of the block.
-template <typename T, int KT>
+template <typename T, int KT, bool SH>
 __device__ __forceinline__ void report_requests(const AttendArgs& a, const CacheView& c, int threads) {
+    const int count = requests_of<SH>(a, c);
+    if (SH && count == 0 && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, SPEC_ERR_PLAN);
 #pragma unroll 1
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const Request r = request_of<KT>(a, c, b);
+    for (int b = blockIdx.x; b < count; b += gridDim.x) {
+        const Request r = request_of<KT, SH>(a, c, b);
         if (r.code == SPEC_OK) continue;
         if (threadIdx.x == 0) set_status(a.status, r.code);
         if (r.code != SPEC_ERR_CACHE_LEN) continue;
@@ -297,16 +400,22 @@ struct AttendPlan {
 // fp32 rows: products on the CUDA cores.
 AttendPlan attend_simt_plan(int rows, int head_dim, int sms);
 int attend_simt(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st);
+int attend_simt_shared(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st);
 
 // 16-bit rows: warp-level matrix instructions, over 16-bit and e4m3 caches.
 AttendPlan attend_mma_plan(int rows, int head_dim, bool f8, int sms);
 int attend_mma16(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 int attend_mma8(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
+AttendPlan attend_mma_shared_plan(int head_dim, bool f8, int sms);
+int attend_mma_shared(const AttendArgs& a, const CacheView& c, spec_dtype dt, bool f8, int blocks, cudaStream_t st);
 
 // 16-bit rows, many of them a KV head: the tensor cores, over 16-bit and e4m3 caches.
+constexpr int kTcLeast = 16;  // rows that the warp-level kernels take as well
 bool attend_tc_takes(const CacheView& c, int rows);
 AttendPlan attend_tc_plan(int sms);
 int attend_tc(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype cache_dt, int blocks,
               cudaStream_t st);
+int attend_tc_shared(const AttendArgs& a, const CacheView& c, spec_dtype dt, spec_dtype cache_dt, int blocks,
+                     cudaStream_t st);
 
 }  // namespace specv

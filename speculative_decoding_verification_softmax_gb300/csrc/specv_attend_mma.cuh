@@ -150,7 +150,7 @@ struct MmaShape {
 };
 
 // T: type of the products, O: type of q and out, F8: e4m3 cache.
-template <typename T, typename O, bool F8, int D, int WR, int WK>
+template <typename T, typename O, bool F8, int D, int WR, int WK, bool SH>
 __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm) k_attend_mma(AttendArgs a,
                                                                                             CacheView c) {
     using Sh = MmaShape<F8, D, WR, WK>;
@@ -169,16 +169,16 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
 
     pdl_trigger();
     pdl_wait();
-    run_of<KT>(a, c, s_run);
+    run_of<KT, SH>(a, c, s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
     const bool has_chunk = lch * 16 < dim * (F8 ? 1 : 2);
     const bool by_group = c.page_size % RP == 0;  // a thread's rows share a page
-    Walk<KT> w(a, c, s_run.run);
+    Walk<KT, SH> w(a, c, s_run.run);
     while (w.next(a, c)) {
         const Request& req = w.req;
         const int t0 = w.t0, nt = w.nt, h = w.h, r0 = w.r0, R = w.R;
-        const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
+        const int32_t* pages = pages_of<SH>(a, req, w.b);
         bool bad = false;
 
         // ---- loads of tile t into stage s; `page`: the group's page, fetched a tile ahead
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 have[i] = wr * 16 + g + 8 * i < R;
                 const int j = have[i] ? (int)a.by_group.div((uint32_t)r) : 0;
                 const int head = h * a.group + (have[i] ? r - j * a.group : 0);
-                qp[i] = a.q + (long long)(req.base + j) * a.q_row + head * a.q_head;
-                pos[i] = have[i] ? req.n + j : req.n + req.ell;
+                qp[i] = a.q + (long long)row_of<SH>(a, req, j) * a.q_row + head * a.q_head;
+                pos[i] = have[i] ? position_of<SH>(req, j) : req.n + req.ell;
             }
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
@@ -517,8 +517,11 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                 part[k] = WK == 1 ? 1.0f : ex2_approx(s_m[k][r] - base);
                 L += part[k] * s_l[k][r];
             }
-            const long long row = out_row(a, req.base, h, r0 + r);
-            const float inv = whole ? vs / L : vs;
+            const long long row = SH ? shared_out_row(a, req, h, r0 + r) : out_row(a, req.base, h, r0 + r);
+            const long long at = SH ? where_of(a, req.kind, row) : 0;
+            const bool direct = whole && (!SH || req.kind == kAlone);
+            const PartRow part_to = SH && whole ? side_row(a, dim, at) : part_row(a, out, dim, r);
+            const float inv = direct ? vs / L : vs;
             for (int d = 2 * lane; d < dim; d += 64) {
                 float x = 0.0f, y = 0.0f;
 #pragma unroll
@@ -527,30 +530,31 @@ __global__ void __launch_bounds__(32 * WR * WK, MmaShape<F8, D, WR, WK>::kPerSm)
                     x += part[k] * o.x;
                     y += part[k] * o.y;
                 }
-                if (whole) *(uint32_t*)((char*)a.out + (row * dim + d) * 2) = pack2<O>(x * inv, y * inv);
-                else *(float2*)(out + r * dim + d) = make_float2(x * inv, y * inv);
+                if (direct) *(uint32_t*)((char*)a.out + (row * dim + d) * 2) = pack2<O>(x * inv, y * inv);
+                else *(float2*)(part_to.o + d) = make_float2(x * inv, y * inv);
             }
             if (lane == 0) {
-                if (!whole) {
-                    out[a.tile_rows * dim + r] = M;
-                    out[a.tile_rows * (dim + 1) + r] = L;
+                if (!direct) {
+                    *part_to.m = M;
+                    *part_to.l = L;
                 } else if (a.lse) {
                     a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
                 }
+                if (SH && t0 == 0) tell(a, at, whole, direct, w.open().x, r);
             }
         }
         __syncthreads();  // the stages are free for the next unit
         if (t0 == 0 && !whole) open = w.open();
     }
-    if (tid == 0) a.open[blockIdx.x] = open;
-    report_requests<O, KT>(a, c, THREADS);
+    if (!SH && tid == 0) a.open[blockIdx.x] = open;
+    report_requests<O, KT, SH>(a, c, THREADS);
 }
 
 // ------------------------------------------------------------------- launch
-template <typename T, typename O, bool F8, int D, int WR, int WK>
+template <typename T, typename O, bool F8, int D, int WR, int WK, bool SH = false>
 int mma_launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
     using Sh = MmaShape<F8, D, WR, WK>;
-    auto* f = k_attend_mma<T, O, F8, D, WR, WK>;
+    auto* f = k_attend_mma<T, O, F8, D, WR, WK, SH>;
     static std::atomic<unsigned long long> done{0};
     if (const int rc = allow_smem((const void*)f, Sh::kSmem, done)) return rc;
     return launch_dependent(f, dim3(blocks), Sh::kThreads, Sh::kSmem, st, 0, a, c);

@@ -436,7 +436,7 @@ __device__ __forceinline__ void tc_widen(uint32_t four, uint32_t& lo, uint32_t& 
 struct Unit {
     int n, ell, base, b;
     int sink_tiles, first_tile, t0, nt;
-    int h, r0, unused;
+    int h, r0, skip;  // SH: skip, and b | kind << 16
     int rows_parts;  // rows R, and the parts if the unit is left open here << 8, -1 if it is whole
 
     __device__ __forceinline__ int rows() const { return rows_parts & 255; }
@@ -447,6 +447,9 @@ struct Unit {
         r.n = n;
         r.ell = ell;
         r.base = base;
+        r.b = b & 0xffff;
+        r.kind = b >> 16;
+        r.skip = skip;
         r.sink_tiles = sink_tiles;
         r.first_tile = first_tile;
         return r;
@@ -508,11 +511,11 @@ struct Eight {
 // The sums of the values that are not finite, of columns col .. col + 7, of the
 // keys that the row at position p sees in the tiles of a segment that a border
 // cuts.
-template <typename T, bool F8, int KT>
+template <typename T, bool F8, int KT, bool SH>
 __device__ __noinline__ Eight sum_nonfinite(const AttendArgs& a, const CacheView& c, Unit w, int p, int col) {
     const Request req = w.request();
     Eight sum = {};
-    const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
+    const int32_t* pages = pages_of<SH>(a, req, w.b);
     for (int t = 0; t < w.nt; ++t) {
         const int key0 = tile_key<KT>(req, w.t0 + t);
         if (all_see<KT>(a, req, key0)) continue;
@@ -532,7 +535,7 @@ __device__ __noinline__ Eight sum_nonfinite(const AttendArgs& a, const CacheView
 }
 
 // Scales a row's scores where they are; the largest one.
-__device__ __noinline__ float scale_scores(uint32_t ts, float by) {
+static __device__ __noinline__ float scale_scores(uint32_t ts, float by) {
     float x[32], top = -INFINITY;
 #pragma unroll 1
     for (int q = 0; q < kTcKeys / 32; ++q) {
@@ -550,7 +553,7 @@ __device__ __noinline__ float scale_scores(uint32_t ts, float by) {
 }
 
 // T: type of the products, O: type of q and out, F8: e4m3 cache.
-template <typename T, typename O, bool F8, int D>
+template <typename T, typename O, bool F8, int D, bool SH>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_attend_tc(const __grid_constant__ AttendArgs a, const __grid_constant__ CacheView c, TcArgs tc,
                 const __grid_constant__ CUtensorMap mk,
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_wait();
     if (warp == 15) tc_alloc(&s_tmem, Sh::kCols);
     tc_fence_before();
-    run_of<KT>(a, c, s_of.run);  // also the barrier behind the set-up
+    run_of<KT, SH>(a, c, s_of.run);  // also the barrier behind the set-up
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = s_tmem;
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;  // no wait for a slot has run out, see tc_wait
         Units w(s_units, unit_full, unit_empty, fail);
         while (w.next()) {
-            const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
+            const int32_t* pages = pages_of<SH>(a, w.req, w.b);
             const int end = w.req.n + w.req.ell, first = min(NB, w.nt);
             int page = 0, token = 0, page1 = 0, token1 = 0;
             bool need = false, need1 = false;  // some row sees some of the box
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int r = qt / CW; r < w.R; r += QSTEP) {
                 const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
                 const int hq = w.h * a.group + (w.r0 + r - j * a.group);
-                const char* from = a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + qch * 16;
+                const char* from = a.q + (long long)row_of<SH>(a, w.req, j) * a.q_row + hq * a.q_head + qch * 16;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(r, qch)),
                              "l"(inside ? from : a.q), "r"(inside ? 16 : 0)
                              : "memory");
@@ -829,7 +832,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp == 13) {
         // -------------------------------------------------------------- units
-        Walk<KT> w(a, c, s_of.run.run);
+        Walk<KT, SH> w(a, c, s_of.run.run);
         for (int u = 0;; ++u) {
             const bool more = w.next(a, c);
             const int at = u % kTcUnits;
@@ -844,7 +847,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     s.n = w.req.n;
                     s.ell = w.req.ell;
                     s.base = w.req.base;
-                    s.b = w.b;
+                    s.b = SH ? w.req.b | w.req.kind << 16 : w.b;
+                    if (SH) s.skip = w.req.skip;
                     s.sink_tiles = w.req.sink_tiles;
                     s.first_tile = w.req.first_tile;
                     s.t0 = w.t0;
@@ -938,7 +942,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         Units w(s_units, unit_full, unit_empty, fail);
         while (all_agree(1, 256, w.next())) {
             const bool active = (warp & 3) * 32 < w.R;  // the warp has rows
-            const int pos = w.req.n + (row < w.R ? (int)a.by_group.div((uint32_t)(w.r0 + row)) : w.req.ell);
+            const int pos = row < w.R ? position_of<SH>(w.req, (int)a.by_group.div((uint32_t)(w.r0 + row)))
+                                      : w.req.n + w.req.ell;
             float scale = fabsf(a.scale) * (F8 && c.k_scale ? fabsf(c.k_scale[w.h]) : 1.0f);
             float m = -INFINITY, l = 0.0f;  // the reference and the sum
             bool coarse = false;            // a score of the warp has been beyond kTcFine
@@ -1051,10 +1056,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // the two streams' weights, for both of them; the parts' maximum and
             // sum, or the reciprocal of the sum in the weights
             const int flags = s_flags[u % kTcUnits];
-            const bool complete = w.now().parts() < 0;
+            const bool whole = w.now().parts() < 0;
+            const bool complete = whole && (!SH || w.req.kind == kAlone);
             float* part = part_at(a, blockIdx.x, w.t0 == 0 ? 1 : 0);
-            long long orow = 0;
-            if (row < w.R) orow = out_row(a, w.req.base, w.h, w.r0 + row);
+            long long orow = 0, at = 0;
+            if (row < w.R) orow = SH ? shared_out_row(a, w.req, w.h, w.r0 + row) : out_row(a, w.req.base, w.h, w.r0 + row);
+            if (SH) at = where_of(a, w.req.kind, orow);
+            const PartRow to_part = SH && whole ? side_row(a, c.head_dim, at) : part_row(a, part, c.head_dim, row);
             if (s == 0) {
                 const float m1 = s_ml[0][row];
                 const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.0f : M;
@@ -1066,11 +1074,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 s_ml[1][row] = w1 * inv;
                 if (row < w.R) {
                     if (!complete) {
-                        part[a.tile_rows * c.head_dim + row] = M;
-                        part[a.tile_rows * (c.head_dim + 1) + row] = L;
+                        *to_part.m = M;
+                        *to_part.l = L;
                     } else if (a.lse) {
                         a.lse[orow] = (M + log2f(L)) * 0.6931471805599453f;
                     }
+                    if (SH && w.t0 == 0) tell(a, at, whole, complete, w.now().parts(), row);
                 }
             }
             __syncwarp();
@@ -1091,7 +1100,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (w.nt > 1) x[e] = fmaf(w1, y[e], x[e]);
                     }
                     if (flags & 2) {
-                        const Eight more = sum_nonfinite<T, F8, KT>(a, c, w.now(), pos, col);
+                        const Eight more = sum_nonfinite<T, F8, KT, SH>(a, c, w.now(), pos, col);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] += more.x[e];
                     }
@@ -1101,7 +1110,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 make_uint4(tc_pack<O>(x[0], x[1]), tc_pack<O>(x[2], x[3]), tc_pack<O>(x[4], x[5]),
                                            tc_pack<O>(x[6], x[7]));
                         } else {
-                            float4* p = (float4*)(part + row * c.head_dim + col);
+                            float4* p = (float4*)(to_part.o + col);
                             p[0] = make_float4(x[0], x[1], x[2], x[3]);
                             p[1] = make_float4(x[4], x[5], x[6], x[7]);
                         }
@@ -1109,18 +1118,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (tid == 0 && (flags & 1)) set_status(a.status, SPEC_ERR_PAGE);
-            if (w.now().parts() > 0) open = open_of(w.now().parts(), w.req.base, w.r0, w.R, w.h);
+            if (!SH && w.now().parts() > 0) open = open_of(w.now().parts(), w.req.base, w.r0, w.R, w.h);
             __syncwarp();
             tc_fence_before();  // the barrier on the way to the next unit: both halves are written
             ++u;
             w.done();
         }
-        if (tid == 0) a.open[blockIdx.x] = open;
+        if (!SH && tid == 0) a.open[blockIdx.x] = open;
         __syncwarp();
         tc_fence_before();
         __syncthreads();
         if (tid == 0 && s_fail) set_status(a.status, SPEC_ERR_TIMEOUT);
-        report_requests<O, KT>(a, c, 256);
+        report_requests<O, KT, SH>(a, c, 256);
     }
 }
 
