@@ -316,7 +316,7 @@ typedef struct {
     const float* v_scale; /* NULL: 1 */
 } spec_cache;
 
-/* Bytes of device workspace of spec_append_kv, spec_reserve_pages,
+/* Bytes of device workspace of spec_append_kv, spec_append_rows, spec_map_rows, spec_reserve_pages,
  * spec_commit_pages, spec_free_pages, spec_fork_pages (pages may be 0 for
  * these) and spec_compact_pages; 0 if out of range. */
 size_t spec_cache_workspace_bytes(int B, int pages);
@@ -444,6 +444,52 @@ int spec_append_kv(const void* q, long long q_row_stride, long long q_head_strid
                    const int32_t* row, int rows, int B, int gamma, const uint64_t* turns, int rotary_dim,
                    int interleaved, float mscale, void* out_q, void* workspace, size_t workspace_bytes,
                    spec_stream_t stream);
+
+/*
+ * Rotary positions and the append of rows by their slots: any number of rows, of
+ * any requests (a step's prompts and single tokens as spec_map_rows lists them; a
+ * drafter's context, which has no queries).  Row r, at position[r], is turned as by
+ * spec_append_kv, and its k and v go to token slot[r] % page_size of page slot[r] /
+ * page_size.
+ *   position     [rows] int32; below 0: no row (its out_q is left as it was).
+ *   slot         [rows] int64; below 0: the row is turned but not stored, and so is
+ *                one behind the cache's last slot (SPEC_ERR_PAGE).  Two rows of one
+ *                call may not name the same slot.
+ *   q_heads      0 where there are no queries (q and out_q are not used then).
+ * Other arguments as for spec_append_kv.  One launch.
+ */
+int spec_append_rows(const void* q, long long q_row_stride, long long q_head_stride, const void* k, const void* v,
+                     long long k_row_stride, long long k_head_stride, long long v_row_stride,
+                     long long v_head_stride, spec_dtype dt, int q_heads, const spec_cache* cache,
+                     const int32_t* position, const int64_t* slot, int rows, const uint64_t* turns, int rotary_dim,
+                     int interleaved, float mscale, void* out_q, void* workspace, size_t workspace_bytes,
+                     spec_stream_t stream);
+
+/*
+ * Page tables and a slot map from the requests' lengths: new_len[b] positions, of any
+ * number, behind cache_len[b] (a prompt's, a part of one, a single token, none).
+ * Request b's slots are grown to hold them, with the lowest free pages in request
+ * order as by spec_reserve_pages, and their rows are listed one request behind the
+ * other: rows out_first[b] .. out_first[b] + new_len[b] - 1.
+ *   out_first     [B+1] int32: sums of new_len; out_first[B] is the number of rows.
+ *   out_request   [rows] int32: b.
+ *   out_position  [rows] int32: cache_len[b] + row - out_first[b].
+ *   out_slot      [rows] int64: page * page_size + position % page_size, for
+ *                 spec_append_rows.
+ *   rows          what the arrays hold; rows behind the last one get -1 in all three.
+ *   out_status    [B] int32: SPEC_OK, SPEC_ERR_POOL, SPEC_ERR_CACHE_LEN (a negative
+ *                 length, more than max_pages slots) or SPEC_ERR_ROW_INDEX (rows that
+ *                 end behind the arrays).  Such a request is left as it was, and its
+ *                 rows have slot -1 (with a negative new_len it has none, with a
+ *                 negative cache_len they have position -1).
+ * A position whose entry is not a page gets slot -1 (SPEC_ERR_PAGE).  Once the rows
+ * are appended, cache_len + new_len is the new length; spec_commit_pages with accept_len
+ * = new_len - 1 sets it, and with -1 gives the new pages back.  Two launches.
+ */
+int spec_map_rows(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages, const int32_t* cache_len,
+                  const int32_t* new_len, int B, int max_pages, int page_size, int rows, int32_t* out_first,
+                  int32_t* out_request, int32_t* out_position, int64_t* out_slot, int32_t* out_status, void* workspace,
+                  size_t workspace_bytes, spec_stream_t stream);
 
 /*
  * Pages for the tested tokens: request b's slots are grown to hold cache_len[b]

@@ -19,9 +19,9 @@ _ROOT = os.path.dirname(_HERE)
 _CSRC = os.path.join(_HERE, "csrc")
 LIB_PATH = os.path.join(_HERE, "libspecv.so")
 SOURCES = ["specv_verify.cu", "specv_sched.cu", "specv_api.cu", "specv_static.cu", "specv_pages.cu",
-           "specv_append.cu", "specv_attend.cu", "specv_attend_simt.cu", "specv_attend_mma16.cu",
+           "specv_append.cu", "specv_append_rows.cu", "specv_attend.cu", "specv_attend_simt.cu", "specv_attend_mma16.cu",
            "specv_attend_mma8.cu", "specv_attend_tc.cu", "specv_share.cu", "specv_share_mma.cu", "specv_share_tc.cu"]
-HEADERS = ["specv_common.cuh", "specv_rowstats.cuh", "specv_cache.cuh", "specv_attend.cuh", "specv_attend_mma.cuh", "specv_attend_tc.cuh",
+HEADERS = ["specv_common.cuh", "specv_rowstats.cuh", "specv_cache.cuh", "specv_append.cuh", "specv_attend.cuh", "specv_attend_mma.cuh", "specv_attend_tc.cuh",
            "specv_attend_tc_launch.cuh", "specv_trace.h"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
@@ -44,7 +44,7 @@ EXPORTED = ["spec_verify_workspace_bytes", "spec_verify", "spec_verify_stats",
             "spec_cache_workspace_bytes", "spec_attend_workspace_bytes", "spec_attend", "spec_append_kv",
             "spec_reserve_pages", "spec_commit_pages", "spec_free_pages", "spec_fork_pages",
             "spec_compact_pages", "spec_share_plan_bytes", "spec_share_plan",
-            "spec_attend_shared_workspace_bytes", "spec_attend_shared"]
+            "spec_attend_shared_workspace_bytes", "spec_attend_shared", "spec_append_rows", "spec_map_rows"]
 STATIC_WORKSPACE_BYTES = 8 << 20
 
 
@@ -160,7 +160,10 @@ def lib():
                 L.spec_attend_shared_workspace_bytes.restype = sz
                 L.spec_attend_shared.argtypes = [vp, ll, ll, i32, i32, cp, vp, i32, vp, sz, i32, i32, i32, f32, vp, vp,
                                                  vp, sz, vp]
-                for f in (L.spec_share_plan, L.spec_attend_shared, L.spec_attend, L.spec_append_kv, L.spec_reserve_pages, L.spec_commit_pages,
+                L.spec_append_rows.argtypes = [vp, ll, ll, vp, vp, ll, ll, ll, ll, i32, i32, cp, vp, vp, i32, vp, i32, i32,
+                                               f32, vp, vp, sz, vp]
+                L.spec_map_rows.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+                for f in (L.spec_append_rows, L.spec_map_rows, L.spec_share_plan, L.spec_attend_shared, L.spec_attend, L.spec_append_kv, L.spec_reserve_pages, L.spec_commit_pages,
                           L.spec_free_pages, L.spec_fork_pages, L.spec_compact_pages):
                     f.restype = i32
                 _lib = L
@@ -909,6 +912,53 @@ def append_kv(q, k, v, k_cache, v_cache, page_table, cache_len, verify_len=None,
     return out_q, workspace
 
 
+def append_rows(q, k, v, k_cache, v_cache, position, slot, *, turns=None, interleaved: bool = False,
+                mscale: float = 1.0, k_scale=None, v_scale=None, out_q=None, workspace=None, stream=None):
+    """Run spec_append_rows: rotary positions, and keys and values of any rows into
+    their slots.
+
+    q [rows, heads, head_dim] (None: no queries), k and v [rows, kv_heads, head_dim];
+    any 16-byte strides.  position [rows] int32 and slot [rows] int64 as map_rows
+    writes them (a position below 0: no row; a slot below 0: not stored).  Other
+    arguments as for append_kv.  Returns (out_q, workspace)."""
+    torch = _torch()
+    dt = _row_dtype("k", k)
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("q, k and v must be [rows, heads, head_dim]")
+    dev = _current_device(k)
+    cache = _cache_arg(k_cache, v_cache, k_scale, v_scale, dev)
+    H, dim = k_cache.shape[-2], k_cache.shape[-1]
+    rows, krs, khs = _row_strides("k", k, k.dtype, H, dim, 0, 0, True, dev)
+    vrows, vrs, vhs = _row_strides("v", v, k.dtype, H, dim, 0, 0, True, dev)
+    heads, rs, hs = 0, 0, 0
+    if q is not None:
+        heads = q.shape[1]
+        qrows, rs, hs = _row_strides("q", q, k.dtype, heads, dim, 0, 0, True, dev)
+        if qrows != rows:
+            raise ValueError(f"q and k must have the same rows, got {qrows} and {rows}")
+        if out_q is None:
+            out_q = _made_on(stream, torch.empty, q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _want("out_q", out_q, q.dtype, q.shape, dev)
+    if vrows != rows:
+        raise ValueError(f"k and v must have the same rows, got {rows} and {vrows}")
+    _want("position", position, torch.int32, (rows,), dev)
+    _want("slot", slot, torch.int64, (rows,), dev)
+    n = 0
+    if turns is not None:
+        n = turns.numel()
+        _want("turns", turns, torch.int64, (n,), dev)
+    if workspace is None:
+        workspace = _made_on(stream, alloc_cache_workspace, 1, 0, k.device)
+    rc = lib().spec_append_rows(_address(q), rs, hs, k.data_ptr(), v.data_ptr(), krs, khs, vrs, vhs, dt, heads, cache,
+                                position.data_ptr(), slot.data_ptr(), rows, _address(turns), 2 * n,
+                                1 if interleaved else 0, mscale, _address(out_q), workspace.data_ptr(),
+                                _workspace_bytes(workspace, dev), _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_append_rows")
+    return out_q, workspace
+
+
 def _page_state(page_table, num_pages, ref_count, cache_len=None):
     """(device, B, max_pages, pages) of tensors that belong together."""
     i32 = _torch().int32
@@ -945,6 +995,37 @@ def reserve_pages(page_table, num_pages, ref_count, cache_len, verify_len=None, 
     if rc != OK:
         raise SpecError(rc, "spec_reserve_pages")
     return out_status, workspace
+
+
+def map_rows(page_table, num_pages, ref_count, cache_len, new_len, *, rows: int, page_size: int, out_first=None,
+             out_request=None, out_position=None, out_slot=None, out_status=None, workspace=None, stream=None):
+    """Run spec_map_rows: pages for new_len[b] ([B] int32, any number) positions
+    behind cache_len[b], and the request, position and slot of each of their rows,
+    one request behind the other, in arrays of `rows`.  page_table, num_pages and
+    ref_count are updated.  Returns (out_first [B+1], out_request [rows],
+    out_position [rows], out_slot [rows] int64, out_status [B], workspace)."""
+    torch = _torch()
+    i32 = torch.int32
+    dev, B, slots, pages = _page_state(page_table, num_pages, ref_count, cache_len)
+    _want("new_len", new_len, i32, (B,), dev)
+    outs = []
+    for name, t, dtype, n in (("out_first", out_first, i32, B + 1), ("out_request", out_request, i32, rows),
+                              ("out_position", out_position, i32, rows), ("out_slot", out_slot, torch.int64, rows),
+                              ("out_status", out_status, i32, B)):
+        if t is None:
+            t = _made_on(stream, torch.empty, (n,), dtype=dtype, device=page_table.device)
+        else:
+            _want(name, t, dtype, (n,), dev)
+        outs.append(t)
+    if workspace is None:
+        workspace = _made_on(stream, alloc_cache_workspace, B, 0, page_table.device)
+    rc = lib().spec_map_rows(page_table.data_ptr(), num_pages.data_ptr(), ref_count.data_ptr(), pages,
+                             cache_len.data_ptr(), new_len.data_ptr(), B, slots, page_size, rows,
+                             *[t.data_ptr() for t in outs], workspace.data_ptr(), _workspace_bytes(workspace, dev),
+                             _raw_stream(stream, dev))
+    if rc != OK:
+        raise SpecError(rc, "spec_map_rows")
+    return (*outs, workspace)
 
 
 def commit_pages(page_table, num_pages, ref_count, cache_len, accept_len, *, page_size: int, window: int = 0,

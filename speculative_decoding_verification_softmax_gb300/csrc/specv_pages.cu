@@ -13,6 +13,7 @@
 // 0.6 GB of pages, 1.19 GB read and written, in 197 us, 6.0 TB/s.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "specv_cache.cuh"
@@ -189,51 +190,13 @@ __device__ __forceinline__ void release(int32_t* ref_count, int pages, int page,
     }
 }
 
-struct ReserveArgs {
-    int32_t* table;
-    int32_t* num;
-    int32_t* ref;
-    const int32_t* len;
-    const int32_t* ell;
-    int32_t* out_status;
-    int* status;
-    int pages, B, gamma, max_pages, page_size;
-};
-
-// Reserve: every block sums the requests' needs (4096 at most, four a thread),
-// the cluster scans the pool, and the warp that sees the r-th free page gives
-// it to the request whose range of needs holds r (a binary search in shared
-// memory).  Latency bound: 1024 requests over a pool of 250,000 pages read 1 MB.
-__global__ void __launch_bounds__(kPgThreads) k_reserve_pages(ReserveArgs a) {
-    pdl_trigger();
-    pdl_wait();
-    __shared__ int s_pref[SPEC_MAX_BATCH + 1];
-    __shared__ int s_num[SPEC_MAX_BATCH];
-    __shared__ int s_warp[kPgWarps + 1], s_cta[2 * kPgCluster];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int tid = threadIdx.x, lane = tid & 31;
-
-    int grow[kPgPer], err[kPgPer];
-#pragma unroll
-    for (int i = 0; i < kPgPer; ++i) {
-        const int b = tid * kPgPer + i;
-        grow[i] = 0;
-        err[i] = SPEC_OK;
-        if (b < a.B) {
-            const int ell = a.ell ? a.ell[b] : a.gamma, n = a.len[b], held = a.num[b];
-            s_num[b] = held;
-            if (ell < 0 || ell > a.gamma) err[i] = SPEC_ERR_VERIFY_LEN;
-            else if (n < 0 || held < 0 || held > a.max_pages) err[i] = SPEC_ERR_CACHE_LEN;
-            else {
-                const long long need = ((long long)n + ell + a.page_size) / a.page_size;
-                if (need > a.max_pages) err[i] = SPEC_ERR_CACHE_LEN;
-                else if (need > held) grow[i] = min((int)need - held, kMany);
-            }
-        }
-    }
-    block_prefix(grow, a.B, s_pref, s_warp);
-    const int need = s_pref[a.B];
+// Gives the s_pref[B] wanted pages, the lowest free ones, to the requests whose
+// ranges of the prefix hold them, in entries from s_num[b] on; returns how many
+// (whole requests, as the pool allows).
+template <typename A>
+__device__ __forceinline__ int take_pages(const A& a, const int* s_pref, const int* s_num, int* s_warp, int* s_cta,
+                                          int rank, int ranks) {
+    const int lane = threadIdx.x & 31, need = s_pref[a.B];
     int limit = 0;
     if (need > 0) {
         PoolScan scan(s_warp, s_cta, ranks, rank, a.pages);
@@ -259,6 +222,54 @@ __global__ void __launch_bounds__(kPgThreads) k_reserve_pages(ReserveArgs a) {
             }
         }
     }
+    return limit;
+}
+
+struct ReserveArgs {
+    int32_t* table;
+    int32_t* num;
+    int32_t* ref;
+    const int32_t* len;
+    const int32_t* ell;
+    int32_t* out_status;
+    int* status;
+    int pages, B, gamma, max_pages, page_size;
+};
+
+// Reserve: every block sums the requests' needs (4096 at most, four a thread),
+// the cluster scans the pool, and the warp that sees the r-th free page gives
+// it to the request whose range of needs holds r (a binary search in shared
+// memory).  Latency bound: 1024 requests over a pool of 250,000 pages read 1 MB.
+__global__ void __launch_bounds__(kPgThreads) k_reserve_pages(ReserveArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int s_pref[SPEC_MAX_BATCH + 1];
+    __shared__ int s_num[SPEC_MAX_BATCH];
+    __shared__ int s_warp[kPgWarps + 1], s_cta[2 * kPgCluster];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int tid = threadIdx.x;
+
+    int grow[kPgPer], err[kPgPer];
+#pragma unroll
+    for (int i = 0; i < kPgPer; ++i) {
+        const int b = tid * kPgPer + i;
+        grow[i] = 0;
+        err[i] = SPEC_OK;
+        if (b < a.B) {
+            const int ell = a.ell ? a.ell[b] : a.gamma, n = a.len[b], held = a.num[b];
+            s_num[b] = held;
+            if (ell < 0 || ell > a.gamma) err[i] = SPEC_ERR_VERIFY_LEN;
+            else if (n < 0 || held < 0 || held > a.max_pages) err[i] = SPEC_ERR_CACHE_LEN;
+            else {
+                const long long need = ((long long)n + ell + a.page_size) / a.page_size;
+                if (need > a.max_pages) err[i] = SPEC_ERR_CACHE_LEN;
+                else if (need > held) grow[i] = min((int)need - held, kMany);
+            }
+        }
+    }
+    block_prefix(grow, a.B, s_pref, s_warp);
+    const int limit = take_pages(a, s_pref, s_num, s_warp, s_cta, rank, ranks);
     if (rank != 0) return;
 #pragma unroll
     for (int i = 0; i < kPgPer; ++i) {
@@ -270,6 +281,116 @@ __global__ void __launch_bounds__(kPgThreads) k_reserve_pages(ReserveArgs a) {
             }
             a.out_status[b] = err[i];
             if (err[i] != SPEC_OK) set_status(a.status, err[i]);
+        }
+    }
+}
+
+struct MapArgs {
+    int32_t* table;
+    int32_t* num;
+    int32_t* ref;
+    const int32_t* len;
+    const int32_t* more;
+    int32_t* first;
+    int32_t* request;
+    int32_t* position;
+    long long* slot;
+    int32_t* out_status;
+    int* status;
+    int pages, B, max_pages, page_size, rows;
+};
+
+// Map, the pages: as reserve, for any number of new positions; and the first row of
+// each request.
+__global__ void __launch_bounds__(kPgThreads) k_map_pages(MapArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int s_pref[SPEC_MAX_BATCH + 1];
+    __shared__ int s_num[SPEC_MAX_BATCH];
+    __shared__ int s_warp[kPgWarps + 1], s_cta[2 * kPgCluster];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int tid = threadIdx.x;
+
+    int grow[kPgPer], more[kPgPer], err[kPgPer];
+#pragma unroll
+    for (int i = 0; i < kPgPer; ++i) {
+        const int b = tid * kPgPer + i;
+        more[i] = b < a.B ? min(max(a.more[b], 0), kMany) : 0;
+    }
+    block_prefix(more, a.B, s_pref, s_warp);
+#pragma unroll
+    for (int i = 0; i < kPgPer; ++i) {
+        const int b = tid * kPgPer + i;
+        grow[i] = 0;
+        err[i] = SPEC_OK;
+        if (b < a.B) {
+            const int n = a.len[b], held = a.num[b];
+            s_num[b] = held;
+            if (rank == 0) a.first[b] = s_pref[b];
+            if (rank == 0 && b == a.B - 1) a.first[a.B] = s_pref[a.B];
+            if (a.more[b] < 0 || n < 0 || held < 0 || held > a.max_pages) err[i] = SPEC_ERR_CACHE_LEN;
+            else if (more[i] > 0 && s_pref[b + 1] > a.rows) err[i] = SPEC_ERR_ROW_INDEX;
+            else {
+                const long long end = (long long)n + more[i];
+                const long long need = (end + a.page_size - 1) / a.page_size;
+                if (need > a.max_pages || end > 0x7fffffffll) err[i] = SPEC_ERR_CACHE_LEN;
+                else if (need > held) grow[i] = min((int)need - held, kMany);
+            }
+        }
+    }
+    __syncthreads();
+    block_prefix(grow, a.B, s_pref, s_warp);
+    const int limit = take_pages(a, s_pref, s_num, s_warp, s_cta, rank, ranks);
+    if (rank != 0) return;
+#pragma unroll
+    for (int i = 0; i < kPgPer; ++i) {
+        const int b = tid * kPgPer + i;
+        if (b < a.B) {
+            if (err[i] == SPEC_OK && grow[i] > 0) {
+                if (s_pref[b + 1] <= limit) a.num[b] = s_num[b] + grow[i];
+                else err[i] = SPEC_ERR_POOL;
+            }
+            a.out_status[b] = err[i];
+            if (err[i] != SPEC_OK) set_status(a.status, err[i]);
+        }
+    }
+}
+
+constexpr int kMapThreads = 256;
+constexpr int kMapRows = kMapThreads * 4;
+
+// Map, the rows: four adjacent rows a thread, their request by a binary search.
+// Bound by the writes, 16 bytes a row.
+__global__ void __launch_bounds__(kMapThreads) k_map_rows(MapArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int s_first[SPEC_MAX_BATCH + 1];
+    for (int b = threadIdx.x; b <= a.B; b += kMapThreads) s_first[b] = a.first[b];
+    __syncthreads();
+    const int all = s_first[a.B];
+    for (long long r0 = (long long)blockIdx.x * kMapRows; r0 < a.rows; r0 += (long long)gridDim.x * kMapRows) {
+        for (int i = 0; i < 4; ++i) {
+            const long long r = r0 + i * kMapThreads + threadIdx.x;
+            if (r >= a.rows) break;
+            int request = -1, position = -1;
+            long long slot = -1;
+            if (r < all) {
+                const int b = owner_of(s_first, a.B, (int)r);
+                const int n = a.len[b];
+                const long long pos = (long long)n + r - s_first[b];
+                request = b;
+                if (n >= 0 && pos <= 0x7fffffffll) position = (int)pos;
+                if (a.out_status[b] == SPEC_OK) {
+                    const int s = position / a.page_size;
+                    const int page = a.table[(size_t)b * a.max_pages + s];
+                    if (page >= 0 && page < a.pages) slot = (long long)page * a.page_size + (position - s * a.page_size);
+                    else set_status(a.status, SPEC_ERR_PAGE);
+                }
+            }
+            a.request[r] = request;
+            a.position[r] = position;
+            a.slot[r] = slot;
         }
     }
 }
@@ -684,7 +805,8 @@ int pages_info(PagesInfo& out) {
     PagesInfo& d = g_pg[dev];
     if (!d.cluster) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SPEC_ERR_CUDA;
-        const void* fns[3] = {(const void*)k_reserve_pages, (const void*)k_fork_tables, (const void*)k_compact_plan};
+        const void* fns[4] = {(const void*)k_reserve_pages, (const void*)k_fork_tables, (const void*)k_compact_plan,
+                              (const void*)k_map_pages};
         int cl = kPgCluster;
         for (const void* f : fns) {
             int n = 0;
@@ -781,6 +903,29 @@ int spec_reserve_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_cou
     const ReserveArgs a{page_table, num_pages, ref_count, cache_len, verify_len, out_status,
                         (int*)workspace, pages, B, gamma, max_pages, page_size};
     return launch_cluster(k_reserve_pages, a, 1, d.cluster, (cudaStream_t)stream);
+}
+
+int spec_map_rows(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages, const int32_t* cache_len,
+                  const int32_t* new_len, int B, int max_pages, int page_size, int rows, int32_t* out_first,
+                  int32_t* out_request, int32_t* out_position, int64_t* out_slot, int32_t* out_status, void* workspace,
+                  size_t workspace_bytes, spec_stream_t stream) {
+    TraceRange tr("spec_map_rows");
+    if (!tables_shape_ok(pages, B, max_pages) || page_size < 1 || rows < 0 || rows > kMany) return SPEC_ERR_SHAPE;
+    if (B == 0) return SPEC_OK;
+    if (!cache_len || !new_len || !out_first || !out_status || (rows > 0 && (!out_request || !out_position || !out_slot)))
+        return SPEC_ERR_NULL;
+    int rc = check_tables(page_table, num_pages, ref_count, pages, B, max_pages, workspace, workspace_bytes, 256);
+    if (rc != SPEC_OK) return rc;
+    if (((uintptr_t)cache_len | (uintptr_t)new_len | (uintptr_t)out_first | (uintptr_t)out_request |
+         (uintptr_t)out_position | (uintptr_t)out_status) & 3 || ((uintptr_t)out_slot & 7))
+        return SPEC_ERR_ALIGN;
+    PagesInfo d;
+    if ((rc = pages_info(d)) != SPEC_OK) return rc;
+    const MapArgs a{page_table, num_pages, ref_count, cache_len, new_len, out_first, out_request, out_position,
+                    (long long*)out_slot, out_status, (int*)workspace, pages, B, max_pages, page_size, rows};
+    if ((rc = launch_cluster(k_map_pages, a, 1, d.cluster, (cudaStream_t)stream)) != SPEC_OK || rows == 0) return rc;
+    const int blocks = (int)std::min(((long long)rows + kMapRows - 1) / kMapRows, 8ll * d.sms);
+    return launch_dependent(k_map_rows, dim3(blocks), kMapThreads, 0, (cudaStream_t)stream, 0, a);
 }
 
 int spec_commit_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages,
