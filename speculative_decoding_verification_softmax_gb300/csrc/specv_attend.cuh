@@ -52,6 +52,7 @@ struct AttendArgs {
     float2* side_ml;  // [2][rows][q_heads]: M and the sum of weights
     int2* where;      // [2][rows][q_heads]: parts of a unit that was cut, and block << 7 | row of the unit
                       // of the first; 0 in `side`, -1 nothing to join
+    FastDiv by_heads;
 };
 
 // ---------------------------------------------------------------- the work

@@ -24,9 +24,7 @@ namespace specv {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanCluster = 8;
-constexpr int kPlanPer = SPEC_MAX_BATCH / kPlanThreads;  // requests of a thread
 constexpr int kPlanPasses = 32;
-constexpr int kPlanInts = 8;  // shared memory of a request
 
 struct PlanArgs {
     const int32_t* table;
@@ -41,12 +39,13 @@ struct PlanArgs {
     uint8_t* kinds;
     int rows, B, gamma, max_pages, page_size, least;
     int limit;
+    int hash;  // places of the classes' table, a power of two
 };
 
 // Leading entries that two rows of the page table have alike, `most` at most; by a
-// warp, eight words of 32 entries at a time.
+// warp, sixteen words of 32 entries at a time.
 __device__ __forceinline__ int common_pages(const int32_t* x, const int32_t* y, int most) {
-    constexpr int W = 8;
+    constexpr int W = 16;
     const int lane = threadIdx.x & 31;
     for (int i0 = 0; i0 < most; i0 += 32 * W) {
         int32_t p[W], q[W];
@@ -65,6 +64,13 @@ __device__ __forceinline__ int common_pages(const int32_t* x, const int32_t* y, 
     return most;
 }
 
+__device__ __forceinline__ void put_item(ShareItem* to, int n, int ell, int base, int rows, int b, int skip, int kind,
+                                         int code) {
+    int4* p = (int4*)to;
+    p[0] = make_int4(n, ell, base, rows);
+    p[1] = make_int4(b, skip, kind, code);
+}
+
 // The plan.  Requests that begin with the same page are a class, the lowest of
 // them its head.  Each counts the leading full pages that it has like the head;
 // the depth d that saves most reads, (members of depth >= d but the head) * d, makes
@@ -72,127 +78,158 @@ __device__ __forceinline__ int common_pages(const int32_t* x, const int32_t* y, 
 // others go into the next pass: a tree of prompts takes a pass for each of its
 // groups.  Then the groups' rows are listed and the items written.
 //
-// The requests' few numbers are in every block's shared memory, and each block
-// takes the same decisions from them; only the page tables' rows are divided over
-// the cluster's warps.  Bound by latency: barriers, and a chain of a few round trips
-// to the tables a pass.
+// The requests' few numbers are in every block's shared memory.  What takes a step
+// for each pair of requests, or reads the tables, is divided over the cluster's warps
+// (a request each), whose results go to all blocks.  Bound by latency: barriers,
+// and a few round trips to the tables a pass.
+template <int PER>  // requests of a thread
 __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
     pdl_trigger();
     pdl_wait();
-    extern __shared__ int s_mem[];
-    int* s_first = s_mem;            // class: the first page, -1 placed
-    int* s_full = s_first + a.B;     // full pages
-    int* s_head = s_full + a.B;      // of this pass; then the leader
-    int* s_shared = s_head + a.B;    // pages shared; 0 alone
-    int* s_rows = s_shared + a.B;    // rows, 0 of a request with an error
-    int* s_leader = s_rows + a.B;
-    int* s_depth = s_leader + a.B;   // [2][B] by pass; then the groups' rows, and their places
-    // key of the best depth by head; B is not always even
-    __shared__ unsigned long long s_best[SPEC_MAX_BATCH];
-    __shared__ unsigned long long s_scan[kPlanWarps + 1];
+    extern __shared__ unsigned long long s_mem[];
+    unsigned long long* s_best = s_mem;               // the best depth's key, by head
+    int* s_class = (int*)(s_best + a.B);              // place in the classes' table; -1 placed
+    int* s_full = s_class + a.B;                      // full pages
+    int* s_head = s_full + a.B;                       // of its last pass
+    int* s_shared = s_head + a.B;                     // pages shared; 0 alone
+    int* s_rows = s_shared + a.B;                     // rows, 0 of a request with an error
+    int* s_depth = s_rows + a.B;                      // [2][B] by pass; then the groups' rows and their places
+    int* s_others = s_depth + 2 * a.B;                // members of its depth or more, but the head
+    int* s_page = s_others + a.B;                     // [hash] the classes' first pages
+    int* s_low = s_page + a.hash;                     // [hash] the lowest request of a class
+    __shared__ unsigned long long s_scan[kPlanWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int warp0 = warp * ranks + rank, warps = kPlanWarps * ranks;  // among the cluster's
+    auto meet = [&] {
+        if (ranks > 1) cluster.sync();
+        else __syncthreads();
+    };
 
-    int code[kPlanPer], n[kPlanPer], ell[kPlanPer], base[kPlanPer];
-    bool any = false;
+    int code[PER], n[PER], ell[PER], base[PER], first[PER];
+    for (int i = tid; i < a.hash; i += kPlanThreads) s_page[i] = -1;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const int b = i * kPlanThreads + tid;
         code[i] = SPEC_OK;
-        if (b >= a.B) continue;
-        n[i] = a.len[b];
-        ell[i] = a.ell ? a.ell[b] : a.gamma;
-        base[i] = a.row ? a.row[b] : b * (a.gamma + 1);
-        if (ell[i] < 0 || ell[i] > a.gamma) code[i] = SPEC_ERR_VERIFY_LEN;
-        else if (base[i] < 0 || base[i] > a.rows - ell[i] - 1) code[i] = SPEC_ERR_ROW_INDEX;
-        else if (n[i] < 0 || n[i] >= a.limit - ell[i]) code[i] = SPEC_ERR_CACHE_LEN;
-        const bool good = code[i] == SPEC_OK;
-        const int full = good ? n[i] / a.page_size : 0;
-        const int first = full > 0 ? a.table[(size_t)b * a.max_pages] : -1;
-        s_first[b] = first < 0 ? -1 : first;
-        s_full[b] = full;
-        s_shared[b] = 0;
-        s_leader[b] = b;
-        s_rows[b] = good ? ell[i] + 1 : 0;
-        any |= first >= 0;
+        n[i] = ell[i] = base[i] = 0;
+        first[i] = -1;
+        if (b < a.B) {
+            n[i] = a.len[b];
+            ell[i] = a.ell ? a.ell[b] : a.gamma;
+            base[i] = a.row ? a.row[b] : b * (a.gamma + 1);
+            first[i] = a.table[(size_t)b * a.max_pages];
+        }
     }
     if (rank == 0 && tid == 0) a.plan[kPlanStatus] = SPEC_OK;
     for (int r = rank * kPlanThreads + tid; r < a.rows; r += ranks * kPlanThreads) a.kinds[r] = 0;
-    cluster.sync();
+    __syncthreads();
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = i * kPlanThreads + tid;
+        if (b >= a.B) continue;
+        if (ell[i] < 0 || ell[i] > a.gamma) code[i] = SPEC_ERR_VERIFY_LEN;
+        else if (base[i] < 0 || base[i] > a.rows - ell[i] - 1) code[i] = SPEC_ERR_ROW_INDEX;
+        else if (n[i] < 0 || n[i] >= a.limit - ell[i]) code[i] = SPEC_ERR_CACHE_LEN;
+        const int full = code[i] == SPEC_OK ? n[i] / a.page_size : 0;
+        int at = -1;
+        if (full > 0 && first[i] >= 0) {
+            at = (int)((uint32_t)first[i] * 2654435761u >> 12 & (uint32_t)(a.hash - 1));
+            for (;; at = (at + 1) & (a.hash - 1)) {  // at least half of the table is free
+                const int old = atomicCAS(&s_page[at], -1, first[i]);
+                if (old == -1 || old == first[i]) break;
+            }
+            any = true;
+        }
+        s_class[b] = at;
+        s_full[b] = full;
+        s_head[b] = b;
+        s_shared[b] = 0;
+        s_rows[b] = code[i] == SPEC_OK ? ell[i] + 1 : 0;
+        s_best[b] = 0;
+    }
+    if (ranks > 1) cluster.sync();  // every block runs, and its kinds are zero
 
     for (int pass = 0; pass < kPlanPasses && __syncthreads_or(any); ++pass) {
         int* s_d = s_depth + (pass & 1) * a.B;
+        for (int i = tid; i < a.hash; i += kPlanThreads) s_low[i] = 0x7fffffff;
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPlanPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const int b = i * kPlanThreads + tid;
-            if (b >= a.B || s_first[b] < 0) continue;
-            int h = 0;
-            while (s_first[h] != s_first[b]) ++h;
-            s_head[b] = h;
-            s_best[b] = 0;
+            if (b < a.B && s_class[b] >= 0) atomicMin(&s_low[s_class[b]], b);
         }
         __syncthreads();
-        for (int b = warp * ranks + rank; b < a.B; b += kPlanWarps * ranks) {
-            const int h = s_first[b] < 0 ? b : s_head[b];
+        for (int b = warp0; b < a.B; b += warps) {
+            const int c = s_class[b], h = c < 0 ? b : s_low[c];
             if (h == b) continue;
             const int d = common_pages(a.table + (size_t)b * a.max_pages, a.table + (size_t)h * a.max_pages,
                                        min(s_full[b], s_full[h]));
             if (lane < ranks) *cluster.map_shared_rank(s_d + b, lane) = d;
         }
-        cluster.sync();
-#pragma unroll
-        for (int i = 0; i < kPlanPer; ++i) {
-            const int b = i * kPlanThreads + tid;
-            if (b >= a.B || s_first[b] < 0) continue;
-            const int h = s_head[b];
+        meet();
+        for (int b = warp0; b < a.B; b += warps) {
+            const int c = s_class[b], h = c < 0 ? b : s_low[c];
             if (h == b || (long long)s_d[b] * a.page_size < a.least) continue;
-            unsigned long long others = 0;
-            for (int x = h + 1; x < a.B; ++x) others += s_first[x] == s_first[b] && s_d[x] >= s_d[b];
-            atomicMax(&s_best[h], others * s_d[b] << 13 | others);
+            const int d = s_d[b];
+            int others = 0;
+            for (int x = h + 1 + lane; x < a.B; x += 32) others += s_class[x] == c && s_d[x] >= d;
+            others = __reduce_add_sync(0xffffffffu, others);
+            if (lane < ranks) *cluster.map_shared_rank(s_others + b, lane) = others;
+        }
+        meet();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int b = i * kPlanThreads + tid;
+            if (b >= a.B || s_class[b] < 0) continue;
+            const int h = s_low[s_class[b]], d = s_d[b];
+            const unsigned long long others = (unsigned)s_others[b];
+            if (h != b && (long long)d * a.page_size >= a.least) atomicMax(&s_best[h], others * d << 13 | others);
         }
         __syncthreads();
         any = false;
-        int now[kPlanPer];
+        int now[PER];
 #pragma unroll
-        for (int i = 0; i < kPlanPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const int b = i * kPlanThreads + tid;
             now[i] = -1;
-            if (b >= a.B || s_first[b] < 0) continue;
-            const int h = s_head[b];
+            if (b >= a.B || s_class[b] < 0) continue;
+            const int h = s_low[s_class[b]];
             const unsigned long long best = s_best[h];
             const int d = best ? (int)((best >> 13) / (best & 8191)) : 0;
             if (d > 0 && (b == h || s_d[b] >= d)) {
-                s_leader[b] = h;
+                s_head[b] = h;
                 s_shared[b] = d;
             } else if (b != h) {
-                now[i] = s_first[b];
+                now[i] = s_class[b];
                 any = true;
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPlanPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const int b = i * kPlanThreads + tid;
-            if (b < a.B) s_first[b] = now[i];
+            if (b < a.B) s_class[b] = now[i];
         }
     }
 
     // the groups' rows: their number, and the place of the first in the list
     int* s_sum = s_depth;
     int* s_start = s_depth + a.B;
-    cluster.sync();  // nobody writes another's depths any more
+    __syncthreads();
     for (int b = tid; b < a.B; b += kPlanThreads) s_sum[b] = 0;
     __syncthreads();
     for (int b = tid; b < a.B; b += kPlanThreads)
-        if (s_shared[b] > 0) atomicAdd(&s_sum[s_leader[b]], s_rows[b]);
+        if (s_shared[b] > 0) atomicAdd(&s_sum[s_head[b]], s_rows[b]);
     __syncthreads();
-    // groups << 32 | rows, before each of four adjacent requests
+    // groups << 32 | rows, before each of PER adjacent requests
     unsigned long long mine = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-        const int b = tid * kPlanPer + i;
-        if (b < a.B && s_shared[b] > 0 && s_leader[b] == b) mine += 1ull << 32 | (unsigned long long)s_sum[b];
+    for (int i = 0; i < PER; ++i) {
+        const int b = tid * PER + i;
+        if (b < a.B && s_shared[b] > 0 && s_head[b] == b) mine += 1ull << 32 | (unsigned long long)s_sum[b];
     }
     unsigned long long x = mine;
 #pragma unroll
@@ -203,61 +240,48 @@ __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
     if (lane == 31) s_scan[warp] = x;
     __syncthreads();
     unsigned long long before = x - mine, total = 0;
+#pragma unroll
     for (int w = 0; w < kPlanWarps; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
     const int groups = (int)(total >> 32);
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-        const int b = tid * kPlanPer + i;
-        if (b < a.B && s_shared[b] > 0 && s_leader[b] == b) {
+    for (int i = 0; i < PER; ++i) {
+        const int b = tid * PER + i;
+        if (b < a.B && s_shared[b] > 0 && s_head[b] == b) {
             s_start[b] = (int)before;
-            if (rank == 0) {
-                ShareItem it;
-                it.n = s_shared[b] * a.page_size - 1;
-                it.ell = 0;
-                it.base = (int)before;
-                it.rows = s_sum[b];
-                it.b = b;
-                it.skip = 0;
-                it.kind = kPrefix;
-                it.code = SPEC_OK;
-                a.items[before >> 32] = it;
-            }
+            if (rank == 0)
+                put_item(a.items + (before >> 32), s_shared[b] * a.page_size - 1, 0, (int)before, s_sum[b], b, 0, kPrefix,
+                         SPEC_OK);
             before += 1ull << 32 | (unsigned long long)s_sum[b];
         }
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const int b = i * kPlanThreads + tid;
-        if (b >= a.B || (warp % ranks) != rank) continue;
-        ShareItem it;
-        const int shared = s_shared[b], leader = s_leader[b];
-        it.code = code[i];
-        it.n = n[i] - shared * a.page_size;
-        it.ell = ell[i];
-        it.base = base[i];
-        it.rows = s_rows[b];
-        it.b = b;
-        it.skip = shared;
-        it.kind = shared > 0 ? kRest : kAlone;
-        a.items[groups + b] = it;
-        a.leader[b] = leader;
+        if (b >= a.B || warp % ranks != rank) continue;
+        const int shared = s_shared[b];
+        put_item(a.items + groups + b, n[i] - shared * a.page_size, ell[i], base[i], s_rows[b], b, shared,
+                 shared > 0 ? kRest : kAlone, code[i]);
+        a.leader[b] = s_head[b];
         a.shared[b] = shared;
-        if (code[i] != SPEC_OK) {
-            set_status(a.plan + kPlanStatus, code[i]);
+        if (code[i] != SPEC_OK) set_status(a.plan + kPlanStatus, code[i]);
+    }
+    __syncthreads();
+    // the rows: of a group's members, behind those of the members before
+    for (int b = warp0; b < a.B; b += warps) {
+        const int rows = s_rows[b], h = s_head[b], row = a.row ? a.row[b] : b * (a.gamma + 1);
+        if (s_shared[b] == 0) {
+            for (int j = lane; j < rows; j += 32) a.kinds[row + j] = 1;
             continue;
         }
         int at = 0;
-        if (shared > 0) {
-            at = s_start[leader];
-            for (int y = leader; y < b; ++y) at += s_leader[y] == leader ? s_rows[y] : 0;
-        }
-        for (int j = 0; j <= ell[i]; ++j) {
-            a.kinds[base[i] + j] = shared > 0 ? 2 : 1;
-            if (shared > 0) a.list[at + j] = base[i] + j;
+        for (int y = h + lane; y < b; y += 32) at += s_shared[y] > 0 && s_head[y] == h ? s_rows[y] : 0;
+        at = s_start[h] + __reduce_add_sync(0xffffffffu, at);
+        for (int j = lane; j < rows; j += 32) {
+            a.kinds[row + j] = 2;
+            a.list[at + j] = row + j;
         }
     }
     if (rank == 0 && tid == 0) {
@@ -273,88 +297,104 @@ __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
 
 constexpr int kShareJoinThreads = 256;
 constexpr int kShareJoinRows = kShareJoinThreads / 32;
-constexpr int kSharePairs = SPEC_MAX_HEAD_DIM / 64;  // column pairs of a lane
+
+// The running maximum and sums of parts.
+template <int V>
+struct Joined {
+    float M, L;
+    float4 o[V];
+};
+
+template <int V>
+__device__ __forceinline__ void take_part(Joined<V>& s, float m, float l, const float4 (&o)[V]) {
+    const float top = fmaxf(m, s.M), ref = top == -INFINITY ? 0.0f : top;
+    const float x = exp2f(s.M - ref), y = exp2f(m - ref);
+    s.M = top;
+    s.L = s.L * x + y * l;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        s.o[v] = make_float4(s.o[v].x * x + y * o[v].x, s.o[v].y * x + y * o[v].y, s.o[v].z * x + y * o[v].z,
+                             s.o[v].w * x + y * o[v].w);
+}
+
+template <int V>
+__device__ __forceinline__ void load_part(const PartRow& p, int dim, float& m, float& l, float4 (&o)[V]) {
+    const int lane = threadIdx.x & 31;
+    m = *p.m;
+    l = *p.l;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (4 * lane + 128 * v < dim) o[v] = *(const float4*)(p.o + 4 * lane + 128 * v);
+    }
+}
 
 // Joins the parts of rows that two items have, or that one has in several blocks'
-// runs: one warp a row and head, up to four parts' loads under way.  The order of
-// the parts is fixed.
-template <typename T>
+// runs: one warp a row and head, four adjacent columns a lane (V times).  Most parts
+// are in `side`, and are read along with the word that says so: a round trip less.
+// The order of the parts is fixed.
+template <typename T, int V>
 __global__ void __launch_bounds__(kShareJoinThreads) k_share_join(AttendArgs a, CacheView c, int blocks) {
-    constexpr int BATCH = 4;
     pdl_trigger();
     pdl_wait();
     const int row = blockIdx.x * kShareJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int all = a.rows * a.q_heads;
-    if (row >= all || requests_of<true>(a, c) == 0) return;
-    const int kind = a.kinds[row / a.q_heads];
-    if (kind == 0) return;
-    const int2 x0 = a.where[row], x1 = kind == 2 ? a.where[(long long)all + row] : make_int2(0, 0);
-    if (x0.x < 0) return;
-    const int dim = c.head_dim;
-    const int n0 = max(x0.x, 1), n = n0 + (kind == 2 ? max(x1.x, 1) : 0);
+    const int all = a.rows * a.q_heads, dim = c.head_dim;
+    if (row >= all) return;
+    // what a row of another kind has here is anything, and not used
+    const int kind = a.kinds[a.by_heads.div((uint32_t)row)];
+    const int2 x0 = a.where[row], x1 = a.where[(long long)all + row];
+    float m0, l0, m1, l1;
+    float4 o0[V], o1[V];
+    load_part<V>(side_row(a, dim, row), dim, m0, l0, o0);
+    load_part<V>(side_row(a, dim, (long long)all + row), dim, m1, l1, o1);
+    if (requests_of<true>(a, c) == 0 || kind == 0 || x0.x < 0) return;
     // a call whose waits ran out may have told nothing of a row
     auto fits = [&](int2 x) {
         return x.x == 0 || (x.x > 0 && x.x <= blocks && x.y >= 0 && (x.y >> 7) + x.x <= blocks && (x.y & 127) < a.tile_rows);
     };
-    const bool good = fits(x0) && fits(x1);
-    float M = -INFINITY, L = 0.0f;
-    float2 sum[kSharePairs];
+    Joined<V> s;
+    s.M = -INFINITY;
+    s.L = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kSharePairs; ++e) sum[e] = make_float2(0.0f, 0.0f);
+    for (int v = 0; v < V; ++v) s.o[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto parts_of = [&](int2 x, float m, float l, const float4 (&o)[V]) {
+        if (!fits(x)) {
+            s.L = __int_as_float(0x7fc00000);
+            return;
+        }
+        if (x.x == 0) {
+            take_part<V>(s, m, l, o);
+            return;
+        }
+        constexpr int BATCH = 4 / V;  // parts under way
 #pragma unroll 1
-    for (int i0 = 0; good && i0 < n; i0 += BATCH) {
-        float m[BATCH], l[BATCH];
-        float2 o[BATCH][kSharePairs];
+        for (int i0 = 0; i0 < x.x; i0 += BATCH) {
+            float mm[BATCH], ll[BATCH];
+            float4 oo[BATCH][V];
 #pragma unroll
-        for (int f = 0; f < BATCH; ++f) {
-            const int i = i0 + f;
-            m[f] = -INFINITY;
-            l[f] = 0.0f;
-            if (i < n) {
-                const bool rest = i < n0;
-                const int2 x = rest ? x0 : x1;
-                const int q = rest ? i : i - n0;
-                const PartRow p = x.x == 0 ? side_row(a, dim, rest ? row : (long long)all + row)
-                                           : part_row(a, part_at(a, (x.y >> 7) + q, q == 0 ? 1 : 0), dim, x.y & 127);
-                m[f] = *p.m;
-                l[f] = *p.l;
+            for (int f = 0; f < BATCH; ++f)
+                if (i0 + f < x.x)
+                    load_part<V>(part_row(a, part_at(a, (x.y >> 7) + i0 + f, i0 + f == 0 ? 1 : 0), dim, x.y & 127), dim,
+                                 mm[f], ll[f], oo[f]);
 #pragma unroll
-                for (int e = 0; e < kSharePairs; ++e)
-                    if (2 * lane + 64 * e < dim) o[f][e] = *(const float2*)(p.o + 2 * lane + 64 * e);
-            }
+            for (int f = 0; f < BATCH; ++f)
+                if (i0 + f < x.x) take_part<V>(s, mm[f], ll[f], oo[f]);
         }
-        const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
-        const float ref = top == -INFINITY ? 0.0f : top, old = exp2f(M - ref);
-        M = top;
-        L *= old;
+    };
+    parts_of(x0, m0, l0, o0);
+    if (kind == 2) parts_of(x1, m1, l1, o1);
+    const float inv = 1.0f / s.L;
 #pragma unroll
-        for (int e = 0; e < kSharePairs; ++e) {
-            sum[e].x *= old;
-            sum[e].y *= old;
+    for (int v = 0; v < V; ++v)
+        if (4 * lane + 128 * v < dim) {
+            Vec<T, 4> four;
+            four.x[0] = from_f32<T>(s.o[v].x * inv);
+            four.x[1] = from_f32<T>(s.o[v].y * inv);
+            four.x[2] = from_f32<T>(s.o[v].z * inv);
+            four.x[3] = from_f32<T>(s.o[v].w * inv);
+            *(Vec<T, 4>*)((T*)a.out + (long long)row * dim + 4 * lane + 128 * v) = four;
         }
-#pragma unroll
-        for (int f = 0; f < BATCH; ++f)
-            if (i0 + f < n) {
-                const float w = exp2f(m[f] - ref);
-                L = fmaf(w, l[f], L);
-#pragma unroll
-                for (int e = 0; e < kSharePairs; ++e)
-                    if (2 * lane + 64 * e < dim) {
-                        sum[e].x = fmaf(w, o[f][e].x, sum[e].x);
-                        sum[e].y = fmaf(w, o[f][e].y, sum[e].y);
-                    }
-            }
-    }
-    const float inv = 1.0f / L;
-#pragma unroll
-    for (int e = 0; e < kSharePairs; ++e)
-        if (2 * lane + 64 * e < dim) {
-            Vec<T, 2> two;
-            two.x[0] = from_f32<T>(good ? sum[e].x * inv : __int_as_float(0x7fc00000));
-            two.x[1] = from_f32<T>(good ? sum[e].y * inv : __int_as_float(0x7fc00000));
-            *(Vec<T, 2>*)((T*)a.out + (long long)row * dim + 2 * lane + 64 * e) = two;
-        }
-    if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * 0.6931471805599453f;
+    if (a.lse && lane == 0) a.lse[row] = (s.M + log2f(s.L)) * 0.6931471805599453f;
 }
 
 }  // namespace specv
@@ -377,6 +417,18 @@ struct PlanLayout {
         total = kinds + up((size_t)rows);
     }
 };
+
+// Shared memory of the plan: 10 words a request, two a place of the table (224 KB for
+// the largest batch).
+template <int PER>
+int launch_plan(const PlanArgs& a, int blocks, cudaStream_t st) {
+    auto smem = [](size_t B, size_t hash) { return 4 * (10 * B + 2 * hash); };
+    static std::atomic<unsigned long long> done{0};
+    if (const int rc = allow_smem((const void*)k_share_plan<PER>,
+                                  (int)smem(PER * kPlanThreads, 2 * PER * kPlanThreads), done))
+        return rc;
+    return launch_dependent(k_share_plan<PER>, dim3(blocks), kPlanThreads, smem(a.B, a.hash), st, blocks, a);
+}
 
 bool plan_shape_ok(int B, int gamma, int rows) {
     return B >= 0 && B <= SPEC_MAX_BATCH && gamma >= 0 && gamma <= SPEC_MAX_GAMMA && rows >= 0;
@@ -413,7 +465,8 @@ bool share_shape_ok(int B, int gamma, int rows, int q_heads, int kv_heads) {
 template <typename T>
 int launch_join(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
     const int n = (a.rows * a.q_heads + kShareJoinRows - 1) / kShareJoinRows;
-    return launch_dependent(k_share_join<T>, dim3(n), kShareJoinThreads, 0, st, 0, a, c, blocks);
+    return c.head_dim <= 128 ? launch_dependent(k_share_join<T, 1>, dim3(n), kShareJoinThreads, 0, st, 0, a, c, blocks)
+                             : launch_dependent(k_share_join<T, 2>, dim3(n), kShareJoinThreads, 0, st, 0, a, c, blocks);
 }
 
 }  // namespace
@@ -456,13 +509,13 @@ int spec_share_plan(const int32_t* page_table, int max_pages, int page_size, con
     a.page_size = page_size;
     a.least = least;
     a.limit = (int)std::min((long long)max_pages * page_size, 0x7fffffc0ll);
-    static std::atomic<unsigned long long> done{0};
-    if (const int rc = allow_smem((const void*)k_share_plan, SPEC_MAX_BATCH * kPlanInts * 4, done)) return rc;
+    a.hash = 32;
+    while (a.hash < 2 * B) a.hash *= 2;
     // a warp a request, in a cluster of a power of two
     int blocks = 1;
     while (blocks < kPlanCluster && blocks * kPlanWarps < B) blocks *= 2;
-    return launch_dependent(k_share_plan, dim3(blocks), kPlanThreads, sizeof(int) * kPlanInts * (size_t)B,
-                            (cudaStream_t)stream, blocks, a);
+    cudaStream_t st = (cudaStream_t)stream;
+    return B <= kPlanThreads ? launch_plan<1>(a, blocks, st) : launch_plan<SPEC_MAX_BATCH / kPlanThreads>(a, blocks, st);
 }
 
 size_t spec_attend_shared_workspace_bytes(int B, int gamma, int rows, int q_heads, int kv_heads, int head_dim) {
@@ -515,6 +568,7 @@ int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_s
     a.max_pages = max_pages;
     a.scale = scale * 1.4426950408889634f;  // log2(e)
     a.by_group = FastDiv((uint32_t)a.group);
+    a.by_heads = FastDiv((uint32_t)q_heads);
     a.plan = (const int*)plan;
     a.items = (const ShareItem*)((const char*)plan + in.items);
     a.list = (const int32_t*)((const char*)plan + in.list);
