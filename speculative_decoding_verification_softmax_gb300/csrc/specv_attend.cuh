@@ -401,7 +401,10 @@ struct AttendPlan {
 // fp32 rows: products on the CUDA cores.
 AttendPlan attend_simt_plan(int rows, int head_dim, int sms);
 int attend_simt(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st);
-int attend_simt_shared(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st);
+
+// The same over the items of a plan, for units of many rows.
+AttendPlan attend_f32_shared_plan(int head_dim, int sms);
+int attend_f32_shared(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st);
 
 // 16-bit rows: warp-level matrix instructions, over 16-bit and e4m3 caches.
 AttendPlan attend_mma_plan(int rows, int head_dim, bool f8, int sms);

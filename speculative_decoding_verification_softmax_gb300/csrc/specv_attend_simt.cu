@@ -27,7 +27,7 @@ constexpr size_t simt_smem() {
     return sizeof(float) * (kSimtRows * D + kSimtKeys * (D + 4) + kSimtKeys * D + kSimtKeys * kSimtPad);
 }
 
-template <int D, bool SH>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(AttendArgs a, CacheView c) {
     using T = float;
     constexpr int KT = kSimtKeys, CN = D / 64;
@@ -44,14 +44,14 @@ __global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(At
 
     pdl_trigger();
     pdl_wait();
-    run_of<KT, SH>(a, c, s_run);
+    run_of<KT, false>(a, c, s_run);
     int4 open = make_int4(0, 0, 0, 0);
     const int dim = c.head_dim;
-    Walk<KT, SH> w(a, c, s_run.run);
+    Walk<KT, false> w(a, c, s_run.run);
     while (w.next(a, c)) {
         const Request& req = w.req;
         const int t0 = w.t0, nt = w.nt, h = w.h, r0 = w.r0, R = w.R;
-        const int32_t* pages = pages_of<SH>(a, req, w.b);
+        const int32_t* pages = a.table + (size_t)w.b * a.max_pages;
 
         __syncthreads();
         for (int i = tid; i < kSimtRows * D; i += kSimtThreads) {
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(At
             if (r < R && d < dim) {
                 const int j = (int)a.by_group.div((uint32_t)(r0 + r));
                 const int head = h * a.group + (r0 + r - j * a.group);
-                x = ((const T*)(a.q + (long long)row_of<SH>(a, req, j) * a.q_row + head * a.q_head))[d];
+                x = ((const T*)(a.q + (long long)(req.base + j) * a.q_row + head * a.q_head))[d];
             }
             s_q[i] = x;
         }
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(At
         float m = -INFINITY, l = 0.0f;
         bool bad = false;
         const int myrow = r0 + srow;
-        const int mypos = position_of<SH>(req, (int)a.by_group.div((uint32_t)myrow));
+        const int mypos = req.n + (int)a.by_group.div((uint32_t)myrow);
 
         for (int t = t0; t < t0 + nt; ++t) {
             const int key0 = tile_key<KT>(req, t);
@@ -170,24 +170,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(At
         for (int i = 0; i < 4; ++i) {
             const int r = rg * 4 + i;
             if (r >= R) break;
-            if constexpr (SH) {
-                const long long row = shared_out_row(a, req, h, r0 + r), at = where_of(a, req.kind, row);
-                const bool direct = whole && req.kind == kAlone;
-                const PartRow to = whole ? side_row(a, dim, at) : part_row(a, part, dim, r);
-                const float inv = direct ? 1.0f / s_l[r] : 1.0f;
-#pragma unroll
-                for (int n = 0; n < CN; ++n)
-                    if (col + 64 * n < dim) (direct ? (T*)a.out + row * dim : to.o)[col + 64 * n] = acc[i][n] * inv;
-                if (col == 0) {
-                    if (!direct) {
-                        *to.m = s_m[r];
-                        *to.l = s_l[r];
-                    } else if (a.lse) {
-                        a.lse[row] = (s_m[r] + log2f(s_l[r])) * 0.6931471805599453f;
-                    }
-                    if (t0 == 0) tell(a, at, whole, direct, w.open().x, r);
-                }
-            } else if (whole) {
+            if (whole) {
                 const long long row = out_row(a, req.base, h, r0 + r);
                 const float inv = 1.0f / s_l[r];
 #pragma unroll
@@ -206,8 +189,8 @@ __global__ void __launch_bounds__(kSimtThreads, simt_per_sm(D)) k_attend_simt(At
         }
         if (t0 == 0 && !whole) open = w.open();
     }
-    if (!SH && tid == 0) a.open[blockIdx.x] = open;
-    report_requests<T, KT, SH>(a, c, kSimtThreads);
+    if (tid == 0) a.open[blockIdx.x] = open;
+    report_requests<T, KT, false>(a, c, kSimtThreads);
 }
 
 AttendPlan attend_simt_plan(int rows, int head_dim, int sms) {
@@ -220,9 +203,9 @@ AttendPlan attend_simt_plan(int rows, int head_dim, int sms) {
 
 namespace {
 
-template <int D, bool SH>
+template <int D>
 int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
-    auto* f = k_attend_simt<D, SH>;
+    auto* f = k_attend_simt<D>;
     static std::atomic<unsigned long long> done{0};
     if (const int rc = allow_smem((const void*)f, (int)simt_smem<D>(), done)) return rc;
     return launch_dependent(f, dim3(blocks), kSimtThreads, simt_smem<D>(), st, 0, a, c);
@@ -231,15 +214,9 @@ int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st)
 }  // namespace
 
 int attend_simt(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
-    if (c.head_dim <= 64) return launch<64, false>(a, c, blocks, st);
-    if (c.head_dim <= 128) return launch<128, false>(a, c, blocks, st);
-    return launch<256, false>(a, c, blocks, st);
-}
-
-int attend_simt_shared(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
-    if (c.head_dim <= 64) return launch<64, true>(a, c, blocks, st);
-    if (c.head_dim <= 128) return launch<128, true>(a, c, blocks, st);
-    return launch<256, true>(a, c, blocks, st);
+    if (c.head_dim <= 64) return launch<64>(a, c, blocks, st);
+    if (c.head_dim <= 128) return launch<128>(a, c, blocks, st);
+    return launch<256>(a, c, blocks, st);
 }
 
 }  // namespace specv

@@ -438,7 +438,7 @@ bool plan_shape_ok(int B, int gamma, int rows) {
 struct ShareLayout {
     size_t parts, side, side_ml, where, total;
     ShareLayout(int rows, int q_heads, int head_dim) {
-        const AttendPlan plans[4] = {attend_simt_plan(1, head_dim, kMostSms),
+        const AttendPlan plans[4] = {attend_f32_shared_plan(head_dim, kMostSms),
                                      attend_mma_shared_plan(head_dim, false, kMostSms),
                                      attend_mma_shared_plan(head_dim, true, kMostSms), attend_tc_plan(kMostSms)};
         size_t most = 0;
@@ -580,7 +580,7 @@ int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_s
 
     const bool f8 = cache->dt == SPEC_E4M3;
     const bool tc = dt != SPEC_F32 && attend_tc_takes(c, kTcLeast + 1);
-    const AttendPlan p = dt == SPEC_F32 ? attend_simt_plan(1, c.head_dim, sms)
+    const AttendPlan p = dt == SPEC_F32 ? attend_f32_shared_plan(c.head_dim, sms)
                          : tc           ? attend_tc_plan(sms)
                                         : attend_mma_shared_plan(c.head_dim, f8, sms);
     a.tile_rows = p.tile_rows;
@@ -588,7 +588,7 @@ int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_s
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
     a.lead = tc ? 3 : 2;
     a.part_cost = tc ? 0.2f / 1.1f : 0.2f / 0.45f;  // as in spec_attend
-    if (dt == SPEC_F32) rc = attend_simt_shared(a, c, p.blocks, st);
+    if (dt == SPEC_F32) rc = attend_f32_shared(a, c, p.blocks, st);
     else if (tc) rc = attend_tc_shared(a, c, dt, cache->dt, p.blocks, st);
     else rc = attend_mma_shared(a, c, dt, f8, p.blocks, st);
     if (rc != SPEC_OK) return rc;

@@ -6,7 +6,7 @@ namespace specv {
 
 namespace {
 
-constexpr int kWr = 4;
+constexpr int kWr = 8;
 
 template <typename T, typename O, bool F8>
 int launch(const AttendArgs& a, const CacheView& c, int blocks, cudaStream_t st) {
