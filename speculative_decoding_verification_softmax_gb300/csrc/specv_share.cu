@@ -438,9 +438,10 @@ bool plan_shape_ok(int B, int gamma, int rows) {
 struct ShareLayout {
     size_t parts, side, side_ml, where, total;
     ShareLayout(int rows, int q_heads, int head_dim) {
-        const AttendPlan plans[4] = {attend_f32_shared_plan(head_dim, kMostSms),
-                                     attend_mma_shared_plan(head_dim, false, kMostSms),
-                                     attend_mma_shared_plan(head_dim, true, kMostSms), attend_tc_plan(kMostSms)};
+        const AttendPlan plans[6] = {
+            attend_f32_shared_plan(head_dim, kMostSms),           attend_mma_shared_plan(1, head_dim, false, kMostSms),
+            attend_mma_shared_plan(1, head_dim, true, kMostSms),  attend_mma_shared_plan(17, head_dim, false, kMostSms),
+            attend_mma_shared_plan(17, head_dim, true, kMostSms), attend_tc_plan(kMostSms)};
         size_t most = 0;
         for (const AttendPlan& p : plans)
             most = std::max(most, sizeof(float) * 2 * (size_t)p.blocks * p.tile_rows * (head_dim + 2));
@@ -579,10 +580,14 @@ int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_s
     cudaStream_t st = (cudaStream_t)stream;
 
     const bool f8 = cache->dt == SPEC_E4M3;
+    const int most = (int)std::min((long long)B * (gamma + 1) * a.group, 1ll << 30);  // of an item
+    // the tensor-core kernel whenever it takes the cache, for few rows too: 4 requests of one
+    // token behind 30,000 positions, 32/8 heads, bf16 45 us against 52 of the warp-level one
+    // (e4m3 41 against 47, heads of 64 35 against 41), 16 requests without grouped heads 35 and 37
     const bool tc = dt != SPEC_F32 && attend_tc_takes(c, kTcLeast + 1);
     const AttendPlan p = dt == SPEC_F32 ? attend_f32_shared_plan(c.head_dim, sms)
                          : tc           ? attend_tc_plan(sms)
-                                        : attend_mma_shared_plan(c.head_dim, f8, sms);
+                                        : attend_mma_shared_plan(most, c.head_dim, f8, sms);
     a.tile_rows = p.tile_rows;
     while ((1 << a.tile_shift) < p.tile_rows) ++a.tile_shift;
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
