@@ -410,7 +410,7 @@ int attend_f32_shared(const AttendArgs& a, const CacheView& c, int blocks, cudaS
 AttendPlan attend_mma_plan(int rows, int head_dim, bool f8, int sms);
 int attend_mma16(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
 int attend_mma8(const AttendArgs& a, const CacheView& c, spec_dtype dt, int blocks, cudaStream_t st);
-AttendPlan attend_mma_shared_plan(int head_dim, bool f8, int sms);
+AttendPlan attend_mma_shared_plan(int rows, int head_dim, bool f8, int sms);
 int attend_mma_shared(const AttendArgs& a, const CacheView& c, spec_dtype dt, bool f8, int blocks, cudaStream_t st);
 
 // 16-bit rows, many of them a KV head: the tensor cores, over 16-bit and e4m3 caches.
