@@ -206,6 +206,7 @@ __device__ __forceinline__ int take_pages(const A& a, const int* s_pref, const i
         while (passes < scan.passes && scan.total < need);
         limit = covered(s_pref, a.B, min(need, scan.total));
         if (passes > 1) scan.total = 0;
+        int b = 0;
         for (int p = 0; p < passes && (passes == 1 || scan.total < limit); ++p) {
             if (passes > 1) scan.read<false>(a.ref, p, unused);  // a pool of several passes is read again
             int upto = scan.before;
@@ -214,7 +215,7 @@ __device__ __forceinline__ int take_pages(const A& a, const int* s_pref, const i
                 uint32_t w;
                 const int r = scan.rank_of(j, w, upto);
                 if (((w >> lane) & 1u) && r < limit) {
-                    const int b = owner_of(s_pref, a.B, r);
+                    if (r < s_pref[b] || r >= s_pref[b + 1]) b = owner_of(s_pref, a.B, r);  // mostly the one before
                     const int page = scan.first + 32 * j + lane;
                     a.table[(size_t)b * a.max_pages + s_num[b] + (r - s_pref[b])] = page;
                     a.ref[page] = 1;
@@ -298,7 +299,42 @@ struct MapArgs {
     int32_t* out_status;
     int* status;
     int pages, B, max_pages, page_size, rows;
+    FastDiv by_page;
 };
+
+// The 32 N rows from r0 on, by a warp, and further ones `step` apart: it looks their first
+// one's request up by a binary search, and most have the same.
+template <int N>
+__device__ __forceinline__ void map_rows(const MapArgs& a, const int* first, const int* status, long long r0,
+                                         long long step) {
+    const int lane = threadIdx.x & 31, all = first[a.B];
+    for (; r0 < a.rows; r0 += step) {
+        int b = r0 < all ? owner_of(first, a.B, (int)r0) : 0;
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {
+            const long long r = r0 + i * 32 + lane;
+            if (r >= a.rows) break;
+            int request = -1, position = -1;
+            long long slot = -1;
+            if (r < all) {
+                if (r >= first[b + 1]) b = owner_of(first, a.B, (int)r);
+                const int n = a.len[b];
+                const long long pos = (long long)n + r - first[b];
+                request = b;
+                if (n >= 0 && pos <= 0x7fffffffll) position = (int)pos;
+                if (status[b] == SPEC_OK) {
+                    const int s = (int)a.by_page.div((uint32_t)position);
+                    const int page = a.table[(size_t)b * a.max_pages + s];
+                    if (page >= 0 && page < a.pages) slot = (long long)page * a.page_size + (position - s * a.page_size);
+                    else set_status(a.status, SPEC_ERR_PAGE);
+                }
+            }
+            a.request[r] = request;
+            a.position[r] = position;
+            a.slot[r] = slot;
+        }
+    }
+}
 
 // Map, the pages: as reserve, for any number of new positions; and the first row of
 // each request.
@@ -358,41 +394,19 @@ __global__ void __launch_bounds__(kPgThreads) k_map_pages(MapArgs a) {
 }
 
 constexpr int kMapThreads = 256;
-constexpr int kMapRows = kMapThreads * 4;
 
-// Map, the rows: four adjacent rows a thread, their request by a binary search.
-// Bound by the writes, 16 bytes a row.
+// Map, the rows: 32 N adjacent ones a warp.  Large steps are bound by the writes, 16 bytes
+// a row, and their instructions: 1,080,000 rows, four words a warp, 9 us, 1.9 TB/s; small
+// ones by a chain of loads, one word a warp.
+template <int N>
 __global__ void __launch_bounds__(kMapThreads) k_map_rows(MapArgs a) {
     pdl_trigger();
     pdl_wait();
     __shared__ int s_first[SPEC_MAX_BATCH + 1];
     for (int b = threadIdx.x; b <= a.B; b += kMapThreads) s_first[b] = a.first[b];
     __syncthreads();
-    const int all = s_first[a.B];
-    for (long long r0 = (long long)blockIdx.x * kMapRows; r0 < a.rows; r0 += (long long)gridDim.x * kMapRows) {
-        for (int i = 0; i < 4; ++i) {
-            const long long r = r0 + i * kMapThreads + threadIdx.x;
-            if (r >= a.rows) break;
-            int request = -1, position = -1;
-            long long slot = -1;
-            if (r < all) {
-                const int b = owner_of(s_first, a.B, (int)r);
-                const int n = a.len[b];
-                const long long pos = (long long)n + r - s_first[b];
-                request = b;
-                if (n >= 0 && pos <= 0x7fffffffll) position = (int)pos;
-                if (a.out_status[b] == SPEC_OK) {
-                    const int s = position / a.page_size;
-                    const int page = a.table[(size_t)b * a.max_pages + s];
-                    if (page >= 0 && page < a.pages) slot = (long long)page * a.page_size + (position - s * a.page_size);
-                    else set_status(a.status, SPEC_ERR_PAGE);
-                }
-            }
-            a.request[r] = request;
-            a.position[r] = position;
-            a.slot[r] = slot;
-        }
-    }
+    map_rows<N>(a, s_first, a.out_status, ((long long)blockIdx.x * (kMapThreads / 32) + (threadIdx.x >> 5)) * 32 * N,
+                (long long)gridDim.x * kMapThreads * N);
 }
 
 struct CommitArgs {
@@ -405,6 +419,8 @@ struct CommitArgs {
     int* status;
     int pages, B, max_pages, page_size, window, sinks;
 };
+
+constexpr int kDrop = 8;
 
 // Commit: one warp a request, a lane per slot given back.
 __global__ void __launch_bounds__(256) k_commit_pages(CommitArgs a) {
@@ -424,9 +440,32 @@ __global__ void __launch_bounds__(256) k_commit_pages(CommitArgs a) {
         return;
     }
     const int keep = (int)((now + a.page_size - 1) / a.page_size);
-    for (int s = keep + lane; s < held; s += 32) {
-        release(a.ref, a.pages, row[s], a.status);
-        row[s] = -1;
+    if (held - keep <= 32) {
+        const int s = keep + lane;
+        if (s < held) {
+            release(a.ref, a.pages, row[s], a.status);
+            row[s] = -1;
+        }
+    } else {
+        // eight entries of a lane at a time: their reads, then their references, under way together
+        for (int s0 = keep + lane; s0 < held; s0 += 32 * kDrop) {
+            int page[kDrop], old[kDrop];
+#pragma unroll
+            for (int i = 0; i < kDrop; ++i) page[i] = s0 + 32 * i < held ? row[s0 + 32 * i] : -1;
+#pragma unroll
+            for (int i = 0; i < kDrop; ++i) {
+                old[i] = 1;
+                if (page[i] >= a.pages) set_status(a.status, SPEC_ERR_PAGE);
+                else if (page[i] >= 0) old[i] = atomicSub(a.ref + page[i], 1);
+                if (s0 + 32 * i < held) row[s0 + 32 * i] = -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kDrop; ++i)
+                if (old[i] <= 0) {
+                    atomicAdd(a.ref + page[i], 1);
+                    set_status(a.status, SPEC_ERR_PAGE);
+                }
+        }
     }
     if (a.window > 0) {
         // pages that start at or behind the sinks and end before the first
@@ -921,11 +960,16 @@ int spec_map_rows(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, i
         return SPEC_ERR_ALIGN;
     PagesInfo d;
     if ((rc = pages_info(d)) != SPEC_OK) return rc;
+    // blocks for the pool's scan, and one for each 4096 pages that the rows may take
+    const int least = (int)std::min((long long)rows / page_size / 4096, (long long)kPgCluster);
     const MapArgs a{page_table, num_pages, ref_count, cache_len, new_len, out_first, out_request, out_position,
-                    (long long*)out_slot, out_status, (int*)workspace, pages, B, max_pages, page_size, rows};
-    if ((rc = launch_cluster(k_map_pages, a, 1, d.cluster, (cudaStream_t)stream)) != SPEC_OK || rows == 0) return rc;
-    const int blocks = (int)std::min(((long long)rows + kMapRows - 1) / kMapRows, 8ll * d.sms);
-    return launch_dependent(k_map_rows, dim3(blocks), kMapThreads, 0, (cudaStream_t)stream, 0, a);
+                    (long long*)out_slot, out_status, (int*)workspace, pages, B, max_pages, page_size, rows, FastDiv((uint32_t)page_size)};
+    if ((rc = launch_cluster(k_map_pages, a, least, d.cluster, (cudaStream_t)stream)) != SPEC_OK || rows == 0) return rc;
+    const long long words = ((long long)rows + kMapThreads - 1) / kMapThreads;
+    if (words <= 4ll * d.sms)
+        return launch_dependent(k_map_rows<1>, dim3((int)words), kMapThreads, 0, (cudaStream_t)stream, 0, a);
+    return launch_dependent(k_map_rows<4>, dim3((int)std::min((words + 3) / 4, 8ll * d.sms)), kMapThreads, 0,
+                            (cudaStream_t)stream, 0, a);
 }
 
 int spec_commit_pages(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages,
