@@ -725,14 +725,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             constexpr int QSTEP = 128 / CW;  // rows of a step
             const int qt = tid & 127, qch = qt % CW;
             const bool inside = qch * 8 < c.head_dim;
+            if constexpr (SH) {
+                // a group's rows are in a list: the reads of eight entries under way together
+                // (one by one they took 10,000 cycles a unit of 128 rows)
+                constexpr int QIN = 8;
+#pragma unroll 1
+                for (int rb = qt / CW; rb < w.R; rb += QSTEP * QIN) {
+                    const char* from[QIN];
+#pragma unroll
+                    for (int i = 0; i < QIN; ++i) {
+                        const int r = rb + i * QSTEP;
+                        from[i] = a.q;
+                        if (r < w.R && inside) {
+                            const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
+                            const int hq = w.h * a.group + (w.r0 + r - j * a.group);
+                            from[i] += (long long)row_of<true>(a, w.req, j) * a.q_row + hq * a.q_head + qch * 16;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < QIN; ++i)
+                        if (rb + i * QSTEP < w.R)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(rb + i * QSTEP, qch)),
+                                         "l"(from[i]), "r"(inside ? 16 : 0)
+                                         : "memory");
+                }
+            } else {
 #pragma unroll 1
             for (int r = qt / CW; r < w.R; r += QSTEP) {
                 const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
                 const int hq = w.h * a.group + (w.r0 + r - j * a.group);
-                const char* from = a.q + (long long)row_of<SH>(a, w.req, j) * a.q_row + hq * a.q_head + qch * 16;
+                const char* from = a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + qch * 16;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(r, qch)),
                              "l"(inside ? from : a.q), "r"(inside ? 16 : 0)
                              : "memory");
+            }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             if (!std::is_same<T, O>::value || flip) {
