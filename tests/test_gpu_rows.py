@@ -93,10 +93,17 @@ def test_random_maps(sv, B, pages, page, most):
         pool.end(r.sample(range(B), B // 3))
 
 
-def test_map_is_undone_by_commit(sv):
-    pool = Pool(3, 8, 30, 4)
-    state, _, ws = map_call(sv, pool, [9, 0, 5], 14)
+@pytest.mark.parametrize("new", [[9, 0, 5], [4 * 33, 1, 4 * 700 + 1]])
+def test_map_is_undone_by_commit(sv, new):
+    """What a step took goes back, a few pages or many of a request; a page that has lost its reference is told."""
+    pool = Pool(3, 800, 900, 4)
+    state, _, ws = map_call(sv, pool, new, sum(new))
+    table, num, ref, length = state
+    if max(new) > 1000:
+        lost = int(table[2, 500])
+        ref[lost] = 0
     sv.commit_pages(*state, i32([-1] * 3), page_size=4, workspace=ws)
+    assert sv.read_status(ws) == (sv.ERR_PAGE if max(new) > 1000 else 0)
     pool.same(*state)
 
 

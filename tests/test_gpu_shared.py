@@ -321,3 +321,32 @@ def test_a_wait_that_runs_out(sv):
     finally:
         sv.selftest_expire_first_wait(False)
     _run(sv, case)
+
+
+def test_empty_batches(sv):
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    table = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    plan, leader, shared = sv.share_plan(table, none, gamma=2, page_size=16)
+    assert leader.numel() == shared.numel() == 0
+    q = torch.zeros(0, 3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(5, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, ws = sv.attend_shared(q, k, k, table, plan)
+    assert out.shape == q.shape and sv.read_status(ws) == 0
+
+
+def test_rows_behind_the_last_and_a_plan_used_again(sv):
+    """Packed rows with room behind them; the same plan for a cache of another type and other heads."""
+    base = dict(share=[([0, 1, 2], 3)], lens=[60, 48, 71], ell=[2, 0, 1], gamma=3, dim=64, packed=True, seed=3)
+    cases = [SharedCase(heads=8, kv_heads=2, **base), SharedCase(heads=6, kv_heads=6, dtype="fp32", cache="fp32", **base),
+             SharedCase(heads=8, kv_heads=1, dtype="fp16", cache="e4m3", **base)]
+    for c in cases:
+        c.q = torch.cat([c.q, torch.randn(4, *c.q.shape[1:]).to(c.q.dtype)])
+    plan, leader, _ = cases[0].make_plan(sv)
+    assert leader.tolist() == [0, 0, 0]
+    for c in cases:
+        out = torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device="cuda")
+        c.table = cases[0].table          # the pages of the plan
+        _, ws = c.call(sv, plan=plan, out=out)
+        assert sv.read_status(ws) == 0
+        c.check(out)
+        assert (out[-4:] == 7.0).all()
