@@ -23,7 +23,7 @@ namespace specv {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanCluster = 8;
+constexpr int kPlanCluster = 16;
 constexpr int kPlanPasses = 32;
 
 struct PlanArgs {
@@ -80,8 +80,10 @@ __device__ __forceinline__ void put_item(ShareItem* to, int n, int ell, int base
 //
 // The requests' few numbers are in every block's shared memory.  What takes a step
 // for each pair of requests, or reads the tables, is divided over the cluster's warps
-// (a request each), whose results go to all blocks.  Bound by latency: barriers,
-// and a few round trips to the tables a pass.
+// (a request each), whose results go to all blocks.  Bound by latency: barriers, and a
+// few round trips to the tables a pass.  16 requests 8.4 us, 64 of one prompt 7.8, 64 in a
+// tree of 8 prompts 14; 1024 in a tree of 120 prompts 35 us (48 with 8 blocks; with 64
+// requests a block 256 take 21 us, with 32 of them 16).
 template <int PER>  // requests of a thread
 __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
     pdl_trigger();
@@ -418,15 +420,50 @@ struct PlanLayout {
     }
 };
 
+// Blocks of the largest cluster: 16 where the GPU can place them, else the portable 8.
+int plan_cluster(const void* kernel, size_t smem, std::atomic<int> (&known)[64], int& blocks) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+    blocks = known[dev].load(std::memory_order_relaxed);
+    if (blocks) return SPEC_OK;
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPlanCluster);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPlanCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    blocks = kPlanCluster;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        blocks = 8;
+    }
+    known[dev].store(blocks, std::memory_order_relaxed);
+    return SPEC_OK;
+}
+
 // Shared memory of the plan: 10 words a request, two a place of the table (224 KB for
 // the largest batch).
 template <int PER>
-int launch_plan(const PlanArgs& a, int blocks, cudaStream_t st) {
+int launch_plan(const PlanArgs& a, cudaStream_t st) {
     auto smem = [](size_t B, size_t hash) { return 4 * (10 * B + 2 * hash); };
     static std::atomic<unsigned long long> done{0};
     if (const int rc = allow_smem((const void*)k_share_plan<PER>,
                                   (int)smem(PER * kPlanThreads, 2 * PER * kPlanThreads), done))
         return rc;
+    static std::atomic<int> known[64];
+    int most = 0;
+    const size_t largest = smem(PER * kPlanThreads, 2 * PER * kPlanThreads);
+    if (const int rc = plan_cluster((const void*)k_share_plan<PER>, largest, known, most)) return rc;
+    // a warp a request, in a cluster of a power of two
+    int blocks = 1;
+    while (blocks < most && blocks * kPlanWarps < a.B) blocks *= 2;
     return launch_dependent(k_share_plan<PER>, dim3(blocks), kPlanThreads, smem(a.B, a.hash), st, blocks, a);
 }
 
@@ -512,11 +549,8 @@ int spec_share_plan(const int32_t* page_table, int max_pages, int page_size, con
     a.limit = (int)std::min((long long)max_pages * page_size, 0x7fffffc0ll);
     a.hash = 32;
     while (a.hash < 2 * B) a.hash *= 2;
-    // a warp a request, in a cluster of a power of two
-    int blocks = 1;
-    while (blocks < kPlanCluster && blocks * kPlanWarps < B) blocks *= 2;
     cudaStream_t st = (cudaStream_t)stream;
-    return B <= kPlanThreads ? launch_plan<1>(a, blocks, st) : launch_plan<SPEC_MAX_BATCH / kPlanThreads>(a, blocks, st);
+    return B <= kPlanThreads ? launch_plan<1>(a, st) : launch_plan<SPEC_MAX_BATCH / kPlanThreads>(a, st);
 }
 
 size_t spec_attend_shared_workspace_bytes(int B, int gamma, int rows, int q_heads, int kv_heads, int head_dim) {
