@@ -1,4 +1,4 @@
-// Rotary positions and the append of the tested tokens to a paged cache.
+// Rotary positions and the append of rows to a paged cache: the kernels.
 //
 // Angles.  The angle of position p and pair i is p f_i.  With f_i / (2 pi) held
 // as a fraction F of 2^64, p F mod 2^64 is the angle's fraction of a turn, an
@@ -12,7 +12,10 @@
 // once), by launch and one round trip of the page table for small ones.
 //
 // BY_SLOT: rows of any number whose positions and places are given, one by one
-// (spec_append_rows); else a batch's tested tokens (spec_append_kv).
+// (spec_append_rows); else a batch's tested tokens (spec_append_kv).  100 rows of 32 + 8
+// heads of 128 take 3.4 us; 26,364, interleaved, 64 values turned, e4m3, 121 us for 594 MB,
+// 4.9 TB/s, bound by the loads' latency at 12 blocks of an SM (eight rows a block with
+// four rows' loads under way 131 us, loads an item ahead 123 to 129).
 #pragma once
 
 #include <type_traits>

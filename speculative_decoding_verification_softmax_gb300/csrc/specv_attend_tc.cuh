@@ -35,6 +35,13 @@
 // 6.4 TB/s (127 with two places for scores).  e4m3 is bound by the softmax and the
 // widening instead: 106 us (heads of 64) and 148 to 167 us (128) there; ragged windows
 // of 4000, 28/4 heads of 64, pages of 16: 62 us for 116 MB (fp16 cache 55 us).
+//
+// SH: the units are those of a plan's items (specv_share.cu), whose query rows may be any
+// requests'.  64 x 17 rows behind 8192 shared positions, 32/8 heads of 128, bf16: 173 us,
+// 950 TFLOP/s; 240 x 4 rows over three prefixes of 32768: 128 us, 945.  Bound by the two
+// streams' chains: of the 1,700 to 1,800 cycles of a tile the products are 1,024, and a
+// stream has scores 1,400 cycles after it has handed its weights over and weights
+// 2,000 cycles after that.
 #pragma once
 
 #include <cuda.h>

