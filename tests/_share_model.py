@@ -66,3 +66,24 @@ class SharedCase(Case):
         return sv.attend_shared(self.to(self.q) if q is None else q, caches[0], caches[1],
                                 self.to(self.table if table is None else table), plan, gamma=self.gamma,
                                 k_scale=self.to(self.k_scale), v_scale=self.to(self.v_scale), **kw)
+
+
+class Banded:
+    """Buffers of a size between bands of a known byte."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, shape, dtype, fill=None):
+        n = int(torch.tensor(shape).prod()) * torch.empty((), dtype=dtype).element_size()
+        raw = torch.full((n + 2 * 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        x = raw[4096:4096 + n].view(dtype).view(shape)
+        if fill is not None:
+            x.fill_(fill)
+        self.all.append((raw, n))
+        return x
+
+    def check(self):
+        torch.cuda.synchronize()
+        for raw, n in self.all:
+            assert (raw[:4096] == 0xA5).all() and (raw[4096 + n:] == 0xA5).all()

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from tests._cache_model import TYPES, Pool, need_pages, rotated
+from tests._share_model import Banded
 
 pytestmark = pytest.mark.gpu
 
@@ -381,3 +382,23 @@ def test_prompts_branches_and_rounds(sv, captured):
             for i in range(layers):
                 del history[b][i][0][n[b]:], history[b][i][1][n[b]:]
         assert length.tolist() == n
+
+
+def test_nothing_is_written_beside_the_buffers(sv):
+    band = Banded()
+    B, slots, pages, page, rows, H, D = 5, 9, 31, 5, 77, 2, 64
+    table, num, ref = band((B, slots), torch.int32, -1), band((B,), torch.int32, 0), band((pages,), torch.int32, 0)
+    first, request, position = band((B + 1,), torch.int32), band((rows,), torch.int32), band((rows,), torch.int32)
+    slot, status, ws = band((rows,), torch.int64), band((B,), torch.int32), band((256,), torch.uint8, 0)
+    sv.map_rows(table, num, ref, i32([0] * B), i32([45, 3, 0, 99, 20]), rows=rows, page_size=page, out_first=first,
+                out_request=request, out_position=position, out_slot=slot, out_status=status, workspace=ws)
+    assert status.tolist() == [0, 0, 0, -14, -14]
+    k = torch.randn(rows, H, D, device="cuda")
+    q = torch.randn(rows, 3, D, device="cuda")
+    K, V, out = band((pages, page, H, D), torch.float32, 0), band((pages, page, H, D), torch.float32, 0), band(q.shape, q.dtype)
+    slot[-1] = pages * page                                    # one behind the cache
+    position[-1] = 4
+    turns = sv.rope_table(sv.rope_frequencies(D))
+    sv.append_rows(q, k, k, K, V, position, slot, turns=turns, out_q=out, workspace=ws)
+    assert sv.read_status(ws) in (sv.ERR_ROW_INDEX, sv.ERR_PAGE)
+    band.check()

@@ -5,7 +5,7 @@ import random
 import pytest
 import torch
 
-from tests._share_model import SharedCase, groups
+from tests._share_model import Banded, SharedCase, groups
 
 pytestmark = pytest.mark.gpu
 
@@ -350,3 +350,60 @@ def test_rows_behind_the_last_and_a_plan_used_again(sv):
         assert sv.read_status(ws) == 0
         c.check(out)
         assert (out[-4:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,cache,dim", [("bf16", "bf16", 64), ("fp16", "e4m3", 128), ("bf16", "bf16", 192), ("fp32", "fp32", 64)])
+def test_many_requests_as_attend(sv, dtype, cache, dim):
+    """More items than a block has threads: 1500 requests in 30 groups, and some alone."""
+    B, page, H, heads, gamma = 1500, 16, 1, 2, 1
+    g = torch.Generator().manual_seed(5)
+    r = random.Random(5)
+    deep = [r.randint(1, 6) for _ in range(30)]
+    pool, table, lens, ell = sum(deep), [], [], []
+    start = [sum(deep[:i]) for i in range(30)]
+    for b in range(B):
+        x = r.randrange(33)
+        common = list(range(start[x], start[x] + deep[x])) if x < 30 else []
+        n = len(common) * page + r.randint(0, 40)
+        own = -(-(n + gamma + 1) // page) - len(common)
+        table.append(common + list(range(pool, pool + own)))
+        pool += own
+        lens.append(n)
+        ell.append(r.randint(0, gamma))
+    slots = max(map(len, table))
+    t = torch.tensor([x + [-1] * (slots - len(x)) for x in table], dtype=torch.int32, device="cuda")
+    n, e = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lens, ell))
+    types = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32, "e4m3": torch.float8_e4m3fn}
+    k, v = (torch.randn(pool, page, H, dim, generator=g).to(types[cache]).cuda() for _ in "kv")
+    q = torch.randn(B, gamma + 1, heads, dim, generator=g).to(types[dtype]).cuda()
+    plan, leader, shared = sv.share_plan(t, n, e, gamma=gamma, page_size=page, least=1)
+    assert (leader.tolist(), shared.tolist()) == groups(t.tolist(), lens, page, 1)
+    outs, lses = [torch.full_like(q, 7.0) for _ in "ab"], [torch.full(q.shape[:-1], 7.0, device="cuda") for _ in "ab"]
+    _, ws = sv.attend_shared(q, k, v, t, plan, out=outs[0], out_lse=lses[0])
+    _, wa = sv.attend(q, k, v, t, n, e, out=outs[1], out_lse=lses[1])
+    assert sv.read_status(ws) == 0 and sv.read_status(wa) == 0
+    # both are within the rounding of the output and of the weights of the same sums
+    eps = torch.finfo(types[dtype]).eps
+    d = (outs[0].double() - outs[1].double()).abs()
+    assert (d <= 4 * eps * (1.0 + outs[1].double().abs()) + 2.0 ** -17).all(), float(d.max())
+    assert ((lses[0] - lses[1]).abs() <= 2.0 ** -16 * (1.0 + lses[1].abs())).all()
+
+
+@pytest.mark.parametrize("dtype,cache,dim,page", [("bf16", "bf16", 128, 16), ("fp16", "e4m3", 64, 8), ("fp32", "fp32", 80, 5),
+                                                  ("fp16", "fp16", 256, 16)])
+def test_nothing_is_written_beside_the_buffers(sv, dtype, cache, dim, page):
+    n0 = 48 // page * page
+    c = SharedCase(share=[([0, 2, 3], n0 // page)], lens=[n0, 9, n0 + 70, n0 + 1], ell=[4, 0, 3, 4], gamma=4, heads=6,
+                   kv_heads=2, dim=dim, dtype=dtype, cache=cache, page=page, packed=True, seed=2)
+    c.ell[3] = 9                                              # an error among them
+    band = Banded()
+    rows = c.q.shape[0]
+    L = sv.lib()
+    plan = band((L.spec_share_plan_bytes(4, 4, rows),), torch.uint8, 0)
+    ws = band((L.spec_attend_shared_workspace_bytes(4, 4, rows, 6, 2, dim),), torch.uint8, 0)
+    leader, shared = band((4,), torch.int32), band((4,), torch.int32)
+    out, lse = band(c.q.shape, c.q.dtype), band(c.q.shape[:-1], torch.float32)
+    c.make_plan(sv, plan=plan, out_leader=leader, out_shared=shared)
+    c.call(sv, plan=plan, out=out, out_lse=lse, workspace=ws)
+    assert sv.read_status(ws) == sv.ERR_VERIFY_LEN
+    band.check()
