@@ -53,6 +53,7 @@ struct AttendArgs {
     int2* where;      // [2][rows][q_heads]: parts of a unit that was cut, and block << 7 | row of the unit
                       // of the first; 0 in `side`, -1 nothing to join
     FastDiv by_heads;
+    int few, cost[2];  // what a tile costs, in the measure of `lead`: of items of at most `few` rows a KV head, of others
 };
 
 // ---------------------------------------------------------------- the work
@@ -147,6 +148,16 @@ __device__ __forceinline__ const int32_t* pages_of(const AttendArgs& a, const Re
     return SH ? a.table + (size_t)r.b * a.max_pages + r.skip : a.table + (size_t)b * a.max_pages;
 }
 
+// What a tile, and a unit with its set-up, cost in the measure of the runs.
+template <bool SH>
+__device__ __forceinline__ int cost_of(const AttendArgs& a, const Request& r) {
+    return SH ? a.cost[r.rows * a.group > a.few] : 1;
+}
+template <bool SH>
+__device__ __forceinline__ int length_of(const AttendArgs& a, const Request& r) {
+    return r.tiles * cost_of<SH>(a, r) + a.lead;
+}
+
 // First key of tile t of a request.
 template <int KT>
 __device__ __forceinline__ int tile_key(const Request& r, int t) {
@@ -201,8 +212,8 @@ __device__ __forceinline__ void run_of(const AttendArgs& a, const CacheView& c, 
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         r = request_of<KT, SH>(a, c, b);
-        mine += (long long)r.units * (r.tiles + a.lead);
-        longest = max(longest, r.tiles);
+        mine += (long long)r.units * length_of<SH>(a, r);
+        longest = max(longest, r.tiles * cost_of<SH>(a, r));
     }
     longest = (int)__reduce_max_sync(0xffffffffu, (unsigned)longest);
     long long x = mine;
@@ -226,7 +237,7 @@ __device__ __forceinline__ void run_of(const AttendArgs& a, const CacheView& c, 
         longest = max(longest, s.longest[w]);
     }
     // few long units are not cut into more parts than joining them is worth
-    const int least = max(2, (int)sqrtf(a.part_cost * (float)longest));
+    const int least = max(SH ? max(2, max(a.cost[0], a.cost[1])) : 2, (int)sqrtf(a.part_cost * (float)longest));
     const long long step = max(quotient(total + gridDim.x - 1, gridDim.x), (long long)least);
     const long long start = (long long)blockIdx.x * step;
     if (start >= before && start < before + mine) {
@@ -236,7 +247,7 @@ __device__ __forceinline__ void run_of(const AttendArgs& a, const CacheView& c, 
 #pragma unroll 1
             for (;; ++b) {
                 r = request_of<KT, SH>(a, c, b);
-                const long long w = (long long)r.units * (r.tiles + a.lead);
+                const long long w = (long long)r.units * length_of<SH>(a, r);
                 if (at < w) break;
                 at -= w;
             }
@@ -261,6 +272,7 @@ struct Walk {
     Request req;
     int b, unit, t0, nt, h, r0, R;
     int place;  // in the unit, leads included
+    int rest;   // of the unit behind the segment
     long long left, step;
 
     __device__ __forceinline__ Walk(const AttendArgs& a, const CacheView& c, const Run& run) {
@@ -270,14 +282,14 @@ struct Walk {
         unit = place = 0;
         if (left > 0) {
             req = run.req;
-            unit = (int)quotient(run.at, (uint32_t)(req.tiles + a.lead));
-            place = (int)(run.at - (long long)unit * (req.tiles + a.lead));
+            unit = (int)quotient(run.at, (uint32_t)length_of<SH>(a, req));
+            place = (int)(run.at - (long long)unit * length_of<SH>(a, req));
         }
     }
     __device__ __forceinline__ bool next(const AttendArgs& a, const CacheView& c) {
         for (;;) {
             if (left <= 0) return false;
-            if (place == req.tiles + a.lead) {
+            if (place == length_of<SH>(a, req)) {
                 place = 0;
                 if (++unit == req.units) {
                     unit = 0;
@@ -286,9 +298,18 @@ struct Walk {
                     while (req.units == 0);
                 }
             }
-            const int take = (int)min((long long)(req.tiles + a.lead - place), left);
+            const int length = length_of<SH>(a, req);
+            const int take = (int)min((long long)(length - place), left);
+            // a tile belongs to the run that its cost ends in: a unit's last run has at least
+            // one, and so have those between (step is no less than a tile's cost)
             t0 = max(place - a.lead, 0);
-            nt = max(place + take - a.lead, 0) - t0;
+            nt = max(place + take - a.lead, 0);
+            if constexpr (SH) {
+                t0 /= cost_of<SH>(a, req);
+                nt /= cost_of<SH>(a, req);
+            }
+            nt -= t0;
+            rest = length - place - take;
             place += take;
             left -= take;
             if (nt > 0) break;
@@ -302,7 +323,6 @@ struct Walk {
     // block with tile 0 says how many there are.
     __device__ __forceinline__ bool whole() const { return nt == req.tiles; }
     __device__ __forceinline__ int4 open() const {
-        const int rest = req.tiles - nt;
         const int parts = rest <= step ? rest > 0 : (int)((uint32_t)(rest - 1) / (uint32_t)step) + 1;
         return open_of(1 + parts, req.base, r0, R, h);
     }
