@@ -37,8 +37,8 @@
 // of 4000, 28/4 heads of 64, pages of 16: 62 us for 116 MB (fp16 cache 55 us).
 //
 // SH: the units are those of a plan's items (specv_share.cu), whose query rows may be any
-// requests'.  64 x 17 rows behind 8192 shared positions, 32/8 heads of 128, bf16: 173 us,
-// 950 TFLOP/s; 240 x 4 rows over three prefixes of 32768: 128 us, 945.  Bound by the two
+// requests'.  64 x 17 rows behind 8192 shared positions, 32/8 heads of 128, bf16: 163 us,
+// 1,006 TFLOP/s; 240 x 4 rows over three prefixes of 32768: 128 us, 945.  Bound by the two
 // streams' chains: of the 1,700 to 1,800 cycles of a tile the products are 1,024, and a
 // stream has scores 1,400 cycles after it has handed its weights over and weights
 // 2,000 cycles after that.

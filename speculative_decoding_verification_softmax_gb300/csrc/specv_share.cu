@@ -630,11 +630,14 @@ int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_s
     // is sooner done; a unit's set-up and end cost as much as four tiles of many rows.  The
     // bench batches in us, 64 chats / three documents / 64 blocks / a tree, by the cost of a
     // tile of few rows, of many, and of a set-up: 1, 1, 3 162 / 147 / 196 / 78; 1, 1, 4 162 /
-    // 146 / 188 / 77; 3, 4, 12 148 / 165 / - / -; 4, 5, 20 152 / 145 / 188 / 76
+    // 146 / 188 / 77; 3, 4, 12 148 / 165 / - / -; 4, 5, 20 152 / 145 / 188 / 76.  The others,
+    // whose tiles are smaller: fp32, 40 x 9 rows of 16 heads of 256 behind 444 positions by
+    // leads of 1, 2, 3 tiles 197, 215, 224 us, 64 single tokens 242, 250, 260; 16 bits, heads
+    // of 192 over e4m3 334, 252, 223, of 256 191, 191, 195
     a.few = tc ? 32 : 0;
     a.cost[0] = tc ? 4 : 1;
     a.cost[1] = tc ? 5 : 1;
-    a.lead = tc ? 20 : 2;
+    a.lead = tc ? 20 : dt == SPEC_F32 ? 1 : 3;
     a.part_cost = (tc ? 0.2f / 1.1f : 0.2f / 0.45f) * a.cost[1];  // as in spec_attend
     if (dt == SPEC_F32) rc = attend_f32_shared(a, c, p.blocks, st);
     else if (tc) rc = attend_tc_shared(a, c, dt, cache->dt, p.blocks, st);
