@@ -758,14 +758,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             } else {
 #pragma unroll 1
-            for (int r = qt / CW; r < w.R; r += QSTEP) {
-                const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
-                const int hq = w.h * a.group + (w.r0 + r - j * a.group);
-                const char* from = a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + qch * 16;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(r, qch)),
-                             "l"(inside ? from : a.q), "r"(inside ? 16 : 0)
-                             : "memory");
-            }
+                for (int r = qt / CW; r < w.R; r += QSTEP) {
+                    const int j = (int)a.by_group.div((uint32_t)(w.r0 + r));
+                    const int hq = w.h * a.group + (w.r0 + r - j * a.group);
+                    const char* from = a.q + (long long)(w.req.base + j) * a.q_row + hq * a.q_head + qch * 16;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + panel_at(r, qch)),
+                                 "l"(inside ? from : a.q), "r"(inside ? 16 : 0)
+                                 : "memory");
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             if (!std::is_same<T, O>::value || flip) {

@@ -85,10 +85,8 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         sv.share_plan(table, lens, gamma=1, page_size=16)      # host tensors
     with pytest.raises(ValueError):
-        sv.alloc_share_plan and sv.attend_shared(torch.zeros(3, 2, 8, 64, dtype=torch.bfloat16),
-                                                 torch.zeros(9, 16, 2, 64, dtype=torch.bfloat16),
-                                                 torch.zeros(9, 16, 2, 64, dtype=torch.bfloat16), table,
-                                                 torch.zeros(1024, dtype=torch.uint8))
+        k = torch.zeros(9, 16, 2, 64, dtype=torch.bfloat16)
+        sv.attend_shared(torch.zeros(3, 2, 8, 64, dtype=torch.bfloat16), k, k, table, torch.zeros(1024, dtype=torch.uint8))
     with pytest.raises(ValueError):                            # packed rows need gamma
         sv.attend_shared(torch.zeros(6, 8, 64, dtype=torch.bfloat16), None, None, table, None)
 
