@@ -408,8 +408,8 @@ size_t spec_attend_shared_workspace_bytes(int B, int gamma, int rows, int q_head
  * requests and numbers as for spec_attend; rows of shared prefixes are sums of two
  * parts, joined in fp32.  A page of a shared prefix is taken from the row of the
  * page table of the group's head.  The workspace holds nothing between calls but
- * its status word; two calls that share one must be ordered on one stream.  Two
- * launches.
+ * its status word; two calls that share one must be ordered on one stream.  After a
+ * wait that ran out (SPEC_ERR_TIMEOUT) all rows of requests are NaN.  Two launches.
  */
 int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_stride, spec_dtype dt, int q_heads,
                        const spec_cache* cache, const int32_t* page_table, int max_pages, const void* plan,
@@ -623,7 +623,8 @@ int spec_selftest_wait(long long limit_ns, int32_t* status, unsigned long long* 
  * more than 16 rows a KV head): the first wait for query rows counts as run out,
  * with copies in flight.  All roles then run to their ends without waiting, the
  * copies land, and the status word reads SPEC_ERR_TIMEOUT; the rows hold
- * anything.  Returns SPEC_OK.
+ * anything (those of spec_attend_shared, whose tensor-core kernel is the same: NaN).
+ * Returns SPEC_OK.
  */
 int spec_selftest_expire_first_wait(int on);
 

@@ -53,6 +53,7 @@ struct AttendArgs {
     int2* where;      // [2][rows][q_heads]: parts of a unit that was cut, and block << 7 | row of the unit
                       // of the first; 0 in `side`, -1 nothing to join
     FastDiv by_heads;
+    int* failed;  // [blocks], by every call: 1 if a wait of the block ran out; NULL: the kernel has no waits
     int few, cost[2];  // what a tile costs, in the measure of `lead`: of items of at most `few` rows a KV head, of others
 };
 

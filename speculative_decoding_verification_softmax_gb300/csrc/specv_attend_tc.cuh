@@ -1162,6 +1162,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_before();
         __syncthreads();
         if (tid == 0 && s_fail) set_status(a.status, SPEC_ERR_TIMEOUT);
+        if (SH && tid == 0) a.failed[blockIdx.x] = s_fail;
         report_requests<O, KT, SH>(a, c, 256);
     }
 }

@@ -299,6 +299,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
 
 constexpr int kShareJoinThreads = 256;
 constexpr int kShareJoinRows = kShareJoinThreads / 32;
+constexpr int kMostSms = 160;
+static_assert(kMostSms <= kShareJoinThreads, "a thread of the joining kernel for each block that may have failed");
 
 // The running maximum and sums of parts.
 template <int V>
@@ -334,15 +336,17 @@ __device__ __forceinline__ void load_part(const PartRow& p, int dim, float& m, f
 // Joins the parts of rows that two items have, or that one has in several blocks'
 // runs: one warp a row and head, four adjacent columns a lane (V times).  Most parts
 // are in `side`, and are read along with the word that says so: a round trip less.
-// The order of the parts is fixed.  34,816 rows and heads 17 us (28 with a round trip
+// The order of the parts is fixed.  Once a wait of any block has run out, `where` may
+// still be an earlier call's, and rows written directly an earlier call's too: all rows
+// become NaN.  34,816 rows and heads 17 us (28 with a round trip
 // each for the kind, the place and the parts), 2,048 5.5 us.
 template <typename T, int V>
 __global__ void __launch_bounds__(kShareJoinThreads) k_share_join(AttendArgs a, CacheView c, int blocks) {
     pdl_trigger();
     pdl_wait();
-    const int row = blockIdx.x * kShareJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int all = a.rows * a.q_heads, dim = c.head_dim;
-    if (row >= all) return;
+    const int all = a.rows * a.q_heads, dim = c.head_dim, lane = threadIdx.x & 31;
+    const int mine = blockIdx.x * kShareJoinRows + (threadIdx.x >> 5), row = min(mine, all - 1);
+    const bool fail = a.failed && (int)threadIdx.x < blocks && a.failed[threadIdx.x];
     // what a row of another kind has here is anything, and not used
     const int kind = a.kinds[a.by_heads.div((uint32_t)row)];
     const int2 x0 = a.where[row], x1 = a.where[(long long)all + row];
@@ -350,8 +354,9 @@ __global__ void __launch_bounds__(kShareJoinThreads) k_share_join(AttendArgs a, 
     float4 o0[V], o1[V];
     load_part<V>(side_row(a, dim, row), dim, m0, l0, o0);
     load_part<V>(side_row(a, dim, (long long)all + row), dim, m1, l1, o1);
-    if (requests_of<true>(a, c) == 0 || kind == 0 || x0.x < 0) return;
-    // a call whose waits ran out may have told nothing of a row
+    const bool lost = a.failed && __syncthreads_or(fail);
+    if (mine >= all || requests_of<true>(a, c) == 0 || kind == 0 || (x0.x < 0 && !lost)) return;
+    // whatever `where` holds, reads stay in range
     auto fits = [&](int2 x) {
         return x.x == 0 || (x.x > 0 && x.x <= blocks && x.y >= 0 && (x.y >> 7) + x.x <= blocks && (x.y & 127) < a.tile_rows);
     };
@@ -384,8 +389,12 @@ __global__ void __launch_bounds__(kShareJoinThreads) k_share_join(AttendArgs a, 
                 if (i0 + f < x.x) take_part<V>(s, mm[f], ll[f], oo[f]);
         }
     };
-    parts_of(x0, m0, l0, o0);
-    if (kind == 2) parts_of(x1, m1, l1, o1);
+    if (lost) {
+        s.L = __int_as_float(0x7fc00000);
+    } else {
+        parts_of(x0, m0, l0, o0);
+        if (kind == 2) parts_of(x1, m1, l1, o1);
+    }
     const float inv = 1.0f / s.L;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -406,8 +415,6 @@ __global__ void __launch_bounds__(kShareJoinThreads) k_share_join(AttendArgs a, 
 using namespace specv;
 
 namespace {
-
-constexpr int kMostSms = 160;
 
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -474,7 +481,7 @@ bool plan_shape_ok(int B, int gamma, int rows) {
 
 // The workspace's size may not depend on the GPU, nor on the types.
 struct ShareLayout {
-    size_t parts, side, side_ml, where, total;
+    size_t failed, parts, side, side_ml, where, total;
     ShareLayout(int rows, int q_heads, int head_dim) {
         const AttendPlan plans[6] = {
             attend_f32_shared_plan(head_dim, kMostSms),           attend_mma_shared_plan(1, head_dim, false, kMostSms),
@@ -484,7 +491,8 @@ struct ShareLayout {
         for (const AttendPlan& p : plans)
             most = std::max(most, sizeof(float) * 2 * (size_t)p.blocks * p.tile_rows * (head_dim + 2));
         const size_t n = 2 * (size_t)rows * q_heads;
-        parts = 256;
+        failed = 256;
+        parts = failed + up(sizeof(int) * kMostSms);
         side = parts + up(most);
         side_ml = side + up(n * head_dim * sizeof(float));
         where = side_ml + up(n * sizeof(float2));
@@ -623,6 +631,7 @@ int spec_attend_shared(const void* q, long long q_row_stride, long long q_head_s
     const AttendPlan p = dt == SPEC_F32 ? attend_f32_shared_plan(c.head_dim, sms)
                          : tc           ? attend_tc_plan(sms)
                                         : attend_mma_shared_plan(most, c.head_dim, f8, sms);
+    a.failed = tc ? (int*)(ws + at.failed) : nullptr;
     a.tile_rows = p.tile_rows;
     while ((1 << a.tile_shift) < p.tile_rows) ++a.tile_shift;
     a.part_floats = (long long)p.tile_rows * (c.head_dim + 2);
