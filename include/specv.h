@@ -371,13 +371,13 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
  * or any requests whose page tables begin with the same pages): the plan, made once
  * for a round and used by all its layers.
  *
- * Requests whose first page is the same are a class, the lowest of them its head.
- * depth_b is the number of leading entries that request b's row of the page table
- * has like the head's, among pages that both have filled (cache_len / page_size).
- * Of the depths d with d * page_size >= least, the one with the largest
- * d * (members of depth >= d but the head), on ties the smallest, makes those members
- * and the head a group that shares d pages.  The head leaves the class in any case, and
- * the rest is taken again, up to 32 times.
+ * Requests whose first max(1, ceil(least / page_size)) pages are the same, and full, are
+ * a class, the lowest of them its head.  depth_b is the number of leading entries that
+ * request b's row of the page table has like the head's, among pages that both have
+ * filled (cache_len / page_size).  Of the depths d with d * page_size >= least, the one
+ * with the largest d * (members of depth >= d but the head), on ties the smallest, makes
+ * those members and the head a group that shares d pages.  The head leaves the class in
+ * any case, and the rest is taken again until none is left.
  *   page_table .. B, gamma   as for spec_attend; verify_len and q_row may be NULL.
  *   least          shorter prefixes (in positions) are not shared; about 256.
  *   out_leader     [B] int32: the group's head; b itself if alone.

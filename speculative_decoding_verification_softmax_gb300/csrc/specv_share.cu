@@ -24,7 +24,7 @@ namespace specv {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanCluster = 16;
-constexpr int kPlanPasses = 32;
+constexpr int kPlanAgain = 32;  // passes until classes are taken apart by the first page too
 
 struct PlanArgs {
     const int32_t* table;
@@ -39,6 +39,7 @@ struct PlanArgs {
     uint8_t* kinds;
     int rows, B, gamma, max_pages, page_size, least;
     int limit;
+    int key;   // the last entry of a prefix of `least` positions
     int hash;  // places of the classes' table, a power of two
 };
 
@@ -71,12 +72,20 @@ __device__ __forceinline__ void put_item(ShareItem* to, int n, int ell, int base
     p[1] = make_int4(b, skip, kind, code);
 }
 
-// The plan.  Requests that begin with the same page are a class, the lowest of
-// them its head.  Each counts the leading full pages that it has like the head;
-// the depth d that saves most reads, (members of depth >= d but the head) * d, makes
-// those members and the head a group.  The head leaves its class in any case, the
-// others go into the next pass: a tree of prompts takes a pass for each of its
-// groups.  Then the groups' rows are listed and the items written.
+// The plan.  Requests with the same page where a prefix of `least` positions ends are
+// a class, the lowest of them its head.  Each counts the leading full pages that it has
+// like the head; the depth d that saves most reads, (members of depth >= d but the
+// head) * d, makes those members and the head a group.  The head leaves its class in
+// any case, the others go into the next pass, until none is left: a pass for each group
+// of a tree of prompts.  Who shares `least` positions with a head is in its class, so
+// how coarse classes are decides the passes and nothing else.  By the first page, chats
+// behind a short common prompt were one class: 64 of them with four samples each took
+// 106 us for 32 passes and as many groups, now 8.7 for all; 1000 lone requests ahead of a
+// group 187 and 11.5.  (By both pages at once: a load more, plan of 1024 alone 7.7 -> 10 us.)
+// Passes in number need groups whose own pages save more than the prompt of all, 40 of
+// them, 900 pages deep, 160 us, or tables that no call here makes, with a page alike
+// behind other ones: those are taken apart by the first page after a while.
+// Then the groups' rows are listed and the items written.
 //
 // The requests' few numbers are in every block's shared memory.  What takes a step
 // for each pair of requests, or reads the tables, is divided over the cluster's warps
@@ -97,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
     int* s_rows = s_shared + a.B;                     // rows, 0 of a request with an error
     int* s_depth = s_rows + a.B;                      // [2][B] by pass; then the groups' rows and their places
     int* s_others = s_depth + 2 * a.B;                // members of its depth or more, but the head
-    int* s_page = s_others + a.B;                     // [hash] the classes' first pages
+    int* s_page = s_others + a.B;                     // [hash] the classes' keys
     int* s_low = s_page + a.hash;                     // [hash] the lowest request of a class
     __shared__ unsigned long long s_scan[kPlanWarps];
     cg::cluster_group cluster = cg::this_cluster();
@@ -109,24 +118,32 @@ __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
         else __syncthreads();
     };
 
-    int code[PER], n[PER], ell[PER], base[PER], first[PER];
+    int code[PER], n[PER], ell[PER], base[PER], from[PER];
     for (int i = tid; i < a.hash; i += kPlanThreads) s_page[i] = -1;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int b = i * kPlanThreads + tid;
         code[i] = SPEC_OK;
         n[i] = ell[i] = base[i] = 0;
-        first[i] = -1;
+        from[i] = -1;
         if (b < a.B) {
             n[i] = a.len[b];
             ell[i] = a.ell ? a.ell[b] : a.gamma;
             base[i] = a.row ? a.row[b] : b * (a.gamma + 1);
-            first[i] = a.table[(size_t)b * a.max_pages];
+            if (a.key < a.max_pages) from[i] = a.table[(size_t)b * a.max_pages + a.key];
         }
     }
     if (rank == 0 && tid == 0) a.plan[kPlanStatus] = SPEC_OK;
     for (int r = rank * kPlanThreads + tid; r < a.rows; r += ranks * kPlanThreads) a.kinds[r] = 0;
     __syncthreads();
+    // the place of a class in the table, of which at least half is free
+    auto place_of = [&](int key) {
+        int at = (int)((uint32_t)key * 2654435761u >> 12 & (uint32_t)(a.hash - 1));
+        for (;; at = (at + 1) & (a.hash - 1)) {
+            const int old = atomicCAS(&s_page[at], -1, key);
+            if (old == -1 || old == key) return at;
+        }
+    };
     bool any = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -137,12 +154,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
         else if (n[i] < 0 || n[i] >= a.limit - ell[i]) code[i] = SPEC_ERR_CACHE_LEN;
         const int full = code[i] == SPEC_OK ? n[i] / a.page_size : 0;
         int at = -1;
-        if (full > 0 && first[i] >= 0) {
-            at = (int)((uint32_t)first[i] * 2654435761u >> 12 & (uint32_t)(a.hash - 1));
-            for (;; at = (at + 1) & (a.hash - 1)) {  // at least half of the table is free
-                const int old = atomicCAS(&s_page[at], -1, first[i]);
-                if (old == -1 || old == first[i]) break;
-            }
+        if (full > a.key && from[i] >= 0) {
+            at = place_of(from[i]);
             any = true;
         }
         s_class[b] = at;
@@ -154,8 +167,19 @@ __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
     }
     if (ranks > 1) cluster.sync();  // every block runs, and its kinds are zero
 
-    for (int pass = 0; pass < kPlanPasses && __syncthreads_or(any); ++pass) {
+    for (int pass = 0; pass < a.B && __syncthreads_or(any); ++pass) {  // a head a pass at least
         int* s_d = s_depth + (pass & 1) * a.B;
+        if (pass == kPlanAgain) {
+            for (int i = tid; i < a.hash; i += kPlanThreads) s_page[i] = -1;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int b = i * kPlanThreads + tid;
+                if (b >= a.B || s_class[b] < 0) continue;
+                const uint32_t x = (uint32_t)a.table[(size_t)b * a.max_pages];
+                s_class[b] = place_of((int)((x * 2246822519u ^ (uint32_t)from[i]) & 0x7fffffffu));
+            }
+        }
         for (int i = tid; i < a.hash; i += kPlanThreads) s_low[i] = 0x7fffffff;
         __syncthreads();
 #pragma unroll
@@ -556,6 +580,7 @@ int spec_share_plan(const int32_t* page_table, int max_pages, int page_size, con
     a.page_size = page_size;
     a.least = least;
     a.limit = (int)std::min((long long)max_pages * page_size, 0x7fffffc0ll);
+    a.key = std::max(1, (int)(((long long)least + page_size - 1) / page_size)) - 1;
     a.hash = 32;
     while (a.hash < 2 * B) a.hash *= 2;
     cudaStream_t st = (cudaStream_t)stream;
