@@ -484,7 +484,8 @@ int spec_append_rows(const void* q, long long q_row_stride, long long q_head_str
  *                 negative cache_len they have position -1).
  * A position whose entry is not a page gets slot -1 (SPEC_ERR_PAGE).  Once the rows
  * are appended, cache_len + new_len is the new length; spec_commit_pages with accept_len
- * = new_len - 1 sets it, and with -1 gives the new pages back.  Two launches.
+ * = new_len - 1 sets it, and with -1 gives the new pages back.  Two launches.  With
+ * B = 0 only out_first[0] = 0 and the -1 of all rows are written (out_first NULL: nothing).
  */
 int spec_map_rows(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, int pages, const int32_t* cache_len,
                   const int32_t* new_len, int B, int max_pages, int page_size, int rows, int32_t* out_first,

@@ -953,9 +953,21 @@ int spec_map_rows(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, i
                   size_t workspace_bytes, spec_stream_t stream) {
     TraceRange tr("spec_map_rows");
     if (!tables_shape_ok(pages, B, max_pages) || page_size < 1 || rows < 0 || rows > kMany) return SPEC_ERR_SHAPE;
-    if (B == 0) return SPEC_OK;
-    if (!cache_len || !new_len || !out_first || !out_status || (rows > 0 && (!out_request || !out_position || !out_slot)))
-        return SPEC_ERR_NULL;
+    const bool arrays = rows == 0 || (out_request && out_position && out_slot);
+    if (B == 0) {  // no rows, and all places say so
+        if (!out_first) return SPEC_OK;
+        if (!arrays) return SPEC_ERR_NULL;
+        if (((uintptr_t)out_first | (uintptr_t)out_request | (uintptr_t)out_position) & 3 || ((uintptr_t)out_slot & 7))
+            return SPEC_ERR_ALIGN;
+        cudaStream_t st = (cudaStream_t)stream;
+        if (cudaMemsetAsync(out_first, 0, sizeof(int32_t), st) != cudaSuccess) return SPEC_ERR_CUDA;
+        if (rows > 0 && (cudaMemsetAsync(out_request, 0xff, sizeof(int32_t) * (size_t)rows, st) != cudaSuccess ||
+                         cudaMemsetAsync(out_position, 0xff, sizeof(int32_t) * (size_t)rows, st) != cudaSuccess ||
+                         cudaMemsetAsync(out_slot, 0xff, sizeof(int64_t) * (size_t)rows, st) != cudaSuccess))
+            return SPEC_ERR_CUDA;
+        return SPEC_OK;
+    }
+    if (!cache_len || !new_len || !out_first || !out_status || !arrays) return SPEC_ERR_NULL;
     int rc = check_tables(page_table, num_pages, ref_count, pages, B, max_pages, workspace, workspace_bytes, 256);
     if (rc != SPEC_OK) return rc;
     if (((uintptr_t)cache_len | (uintptr_t)new_len | (uintptr_t)out_first | (uintptr_t)out_request |
