@@ -471,12 +471,13 @@ int spec_append_rows(const void* q, long long q_row_stride, long long q_head_str
  * Request b's slots are grown to hold them, with the lowest free pages in request
  * order as by spec_reserve_pages, and their rows are listed one request behind the
  * other: rows out_first[b] .. out_first[b] + new_len[b] - 1.
- *   out_first     [B+1] int32: sums of new_len; out_first[B] is the number of rows.
+ *   out_first     [B+1] int32: sums of new_len; out_first[B] is the number of rows.  Sums
+ *                 stop at 2^30 - 1.
  *   out_request   [rows] int32: b.
  *   out_position  [rows] int32: cache_len[b] + row - out_first[b].
  *   out_slot      [rows] int64: page * page_size + position % page_size, for
  *                 spec_append_rows.
- *   rows          what the arrays hold; rows behind the last one get -1 in all three.
+ *   rows          what the arrays hold, below 2^30 - 1; rows behind the last one get -1 in all three.
  *   out_status    [B] int32: SPEC_OK, SPEC_ERR_POOL, SPEC_ERR_CACHE_LEN (a negative
  *                 length, more than max_pages slots) or SPEC_ERR_ROW_INDEX (rows that
  *                 end behind the arrays).  Such a request is left as it was, and its

@@ -952,7 +952,8 @@ int spec_map_rows(int32_t* page_table, int32_t* num_pages, int32_t* ref_count, i
                   int32_t* out_request, int32_t* out_position, int64_t* out_slot, int32_t* out_status, void* workspace,
                   size_t workspace_bytes, spec_stream_t stream) {
     TraceRange tr("spec_map_rows");
-    if (!tables_shape_ok(pages, B, max_pages) || page_size < 1 || rows < 0 || rows > kMany) return SPEC_ERR_SHAPE;
+    if (!tables_shape_ok(pages, B, max_pages) || page_size < 1 || rows < 0 || rows >= kMany)
+        return SPEC_ERR_SHAPE;  // a sum that has stopped at kMany lies behind the arrays
     const bool arrays = rows == 0 || (out_request && out_position && out_slot);
     if (B == 0) {  // no rows, and all places say so
         if (!out_first) return SPEC_OK;

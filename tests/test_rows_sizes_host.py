@@ -19,3 +19,9 @@ def L():
 def test_a_map_of_no_requests_looks_at_its_arrays(L, bad, code):
     assert map_rows(L, B=0, table=None, num=None, ref=None, len=None, new=None, status=None, **bad) == \
         getattr(sv, "ERR_" + code)
+
+
+def test_rows_whose_sums_could_not_be_told_apart(L):
+    """Sums of lengths stop at 2^30 - 1: the arrays have to be smaller, so that such a sum lies behind them."""
+    assert map_rows(L, rows=0x3fffffff) == sv.ERR_SHAPE
+    assert map_rows(L, rows=0x3ffffffe, bytes=16) == sv.ERR_WORKSPACE
