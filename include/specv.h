@@ -396,8 +396,9 @@ int spec_share_plan(const int32_t* page_table, int max_pages, int page_size, con
                     const int32_t* verify_len, const int32_t* q_row, int rows, int B, int gamma, int least,
                     int32_t* out_leader, int32_t* out_shared, void* plan, size_t plan_bytes, spec_stream_t stream);
 
-/* Bytes of device workspace of spec_attend_shared; 0 if out of range.  `rows` is
- * that of the plan: B * (gamma+1), or the packed rows. */
+/* Bytes of device workspace of spec_attend_shared; 0 if out of range (rows * q_heads
+ * and B * (gamma+1) * q_heads / kv_heads are below 2^31 - 256).  `rows` is that of the
+ * plan: B * (gamma+1), or the packed rows. */
 size_t spec_attend_shared_workspace_bytes(int B, int gamma, int rows, int q_heads, int kv_heads, int head_dim);
 
 /*

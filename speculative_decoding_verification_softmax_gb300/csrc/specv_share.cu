@@ -528,9 +528,11 @@ bool heads_ok(int q_heads, int kv_heads) {
     return q_heads >= 1 && kv_heads >= 1 && q_heads <= 65535 && q_heads % kv_heads == 0;
 }
 
-// rows and heads countable in 31 bits, as the joining kernel does
+// rows and heads countable in 31 bits, as the joining kernel does, and so a group's rows of
+// a KV head (rows that two requests have are not allowed, but count twice there)
 bool share_shape_ok(int B, int gamma, int rows, int q_heads, int kv_heads) {
-    return plan_shape_ok(B, gamma, rows) && heads_ok(q_heads, kv_heads) && (long long)rows * q_heads < 0x7fffff00ll;
+    return plan_shape_ok(B, gamma, rows) && heads_ok(q_heads, kv_heads) && (long long)rows * q_heads < 0x7fffff00ll &&
+           (long long)B * (gamma + 1) * (q_heads / kv_heads) < 0x7fffff00ll;
 }
 
 template <typename T>
