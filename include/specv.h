@@ -390,6 +390,12 @@ int spec_attend(const void* q, long long q_row_stride, long long q_head_stride, 
  * The plan holds the lengths and rows of this call, and no page ids: it is to be
  * made again when they change or when a shared entry does.  Rows of two requests may
  * not overlap.  One launch.
+ *
+ * A plan pays where groups save much: (members - 1) * shared positions from about
+ * 16,000 on for requests of one to five rows, from about 100,000 on for 17 (32/8 heads
+ * of 128, bf16, a layer on the device: 64 requests of one token behind 2048 positions
+ * spec_attend 89 us, spec_attend_shared 34; 4 behind 1024 12 and 14; 64 of 17 rows behind
+ * 2048 80 and 81, behind 8192 245 and 170).  Below, spec_attend is the faster call.
  */
 size_t spec_share_plan_bytes(int B, int gamma, int rows);
 int spec_share_plan(const int32_t* page_table, int max_pages, int page_size, const int32_t* cache_len,

@@ -758,6 +758,8 @@ def share_plan(page_table, cache_len, verify_len=None, row=None, *, gamma: int, 
     same pages, for attend_shared.  page_table, cache_len, verify_len and row as for
     attend; rows: those of q where they are packed (with `row`).  The plan serves all
     layers of a round, and is made again when lengths, rows or shared entries change.
+    It pays from about 16,000 saved positions a group on, (members - 1) * shared, with
+    one to five rows a request, and from about 100,000 with 17; below, attend is faster.
     Returns (plan, out_leader [B], out_shared [B])."""
     torch = _torch()
     dev = _current_device(page_table)

@@ -90,9 +90,8 @@ __device__ __forceinline__ void put_item(ShareItem* to, int n, int ell, int base
 // The requests' few numbers are in every block's shared memory.  What takes a step
 // for each pair of requests, or reads the tables, is divided over the cluster's warps
 // (a request each), whose results go to all blocks.  Bound by latency: barriers, and a
-// few round trips to the tables a pass.  16 requests 8.4 us, 64 of one prompt 7.8, 64 in a
-// tree of 8 prompts 14; 1024 in a tree of 120 prompts 35 us (48 with 8 blocks; with 64
-// requests a block 256 take 21 us, with 32 of them 16).
+// few round trips to the tables a pass.  16 requests 8.5 us, 64 of one prompt 8.5, 64 in a
+// tree of 6 prompts 14.6; 1024 in a tree of 96 prompts 36 us (with 8 blocks 48).
 template <int PER>  // requests of a thread
 __global__ void __launch_bounds__(kPlanThreads) k_share_plan(PlanArgs a) {
     pdl_trigger();
@@ -362,8 +361,9 @@ __device__ __forceinline__ void load_part(const PartRow& p, int dim, float& m, f
 // are in `side`, and are read along with the word that says so: a round trip less.
 // The order of the parts is fixed.  Once a wait of any block has run out, `where` may
 // still be an earlier call's, and rows written directly an earlier call's too: all rows
-// become NaN.  34,816 rows and heads 17 us (28 with a round trip
-// each for the kind, the place and the parts), 2,048 5.5 us.
+// become NaN.  34,816 rows and heads 18 us (28 with a round trip
+// each for the kind, the place and the parts; 1 us of it for the failed blocks' words),
+// 2,048 5.5 us.
 template <typename T, int V>
 __global__ void __launch_bounds__(kShareJoinThreads) k_share_join(AttendArgs a, CacheView c, int blocks) {
     pdl_trigger();

@@ -22,7 +22,7 @@ constexpr int kF32Threads = 256;
 constexpr int kF32Rows = 64;
 
 constexpr int f32_keys(int dim) { return dim <= 64 ? 64 : 32; }
-// Blocks of an SM, by shared memory: 99, 109 and 207 KB each.
+// Blocks of an SM, by shared memory: 102, 109 and 207 KB each.
 constexpr int f32_per_sm(int dim) { return dim <= 128 ? 2 : 1; }
 
 template <int D>
